@@ -107,8 +107,8 @@ extern "C" {
 #define PDGEMM_ENULL (-3)       /* NULL pointer for an operand with nonzero extent */
 #define PDGEMM_EINVAL_I4 (-4)   /* gemm_i4: K, lda or ldb odd */
 #define PDGEMM_EALIGN (-5)      /* a pointer or leading dimension breaks the alignment rules */
-#define PDGEMM_EINVAL_CFG (-6)  /* unknown precision or tile configuration, or a dequantizing
-                                   epilogue for FP16; reported before any other check.  Every
+#define PDGEMM_EINVAL_CFG (-6)  /* unknown precision, element type, scale rule or tile configuration,
+                                   or a dequantizing epilogue for FP16; reported before any other check.  Every
                                    configuration, the K-split ones included, serves both B layouts */
 
 #define PDGEMM_EWORKSPACE (-7)  /* a workspace or FP6 image smaller than its entry point needs
@@ -346,6 +346,89 @@ int pdgemm_pick_config(int prec, int64_t M, int64_t N, int64_t K);
  * pointer may be NULL. */
 int pdgemm_config_info(int cfg, int *block_m, int *block_n, int *wave_m, int *wave_n,
                        int *threads);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4: microscaled 4-bit floating point.
+ *
+ * An operand of `rows` rows of K values is a pair of device arrays:
+ *   codes   4 bits a value, e2m1 (sign, 2 exponent bits of bias 1, 1 mantissa
+ *           bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two per byte along K with the
+ *           even k in the low nibble; ld counts values, as for gemm_i4;
+ *   scales  one byte per block of 32 consecutive k of a row, 2^(byte - 127),
+ *           byte 255 = NaN (the whole block).  They are stored by block: the
+ *           scale of block b = k / 32 of row i at scales[b * lds + i], lds >=
+ *           rows, ceil(K / 32) blocks.  (Checkpoints that keep them by row need
+ *           one transposition.)
+ * The value of element (i, k) is e2m1(code) * 2^(byte - 127).  This is the
+ * MXFP4 of the OCP Microscaling Formats (MX) Specification v1.0.  K is any
+ * length: the last block of a row may be short.  The pages stop at integer
+ * 4-bit operands ("Hand-Written PTX Tensor-Core GEMM Kernels ...", Listing 2,
+ * Section IV-C); this is the floating-point 4-bit type that gfx950's matrix
+ * cores multiply natively.
+ *
+ * Alignment: codes and scales 16-byte aligned, ld a multiple of 32 (16 bytes),
+ * lds a multiple of 16.  Dense arrays (the source of the quantiser, the result
+ * of the dequantiser, C) need only their element's alignment and any ld >= the
+ * row.  A row of any array spans at most 4 MiB.  As elsewhere, the 16-byte
+ * granule that holds the last element of a row (of codes or of scales) may be
+ * read whole, and values outside the operand never reach a stored result,
+ * whatever their bits.
+ * Errors, streams and ownership are those of the other entry points; nothing
+ * is allocated and no state is kept.  An unknown type or rule returns
+ * PDGEMM_EINVAL_CFG before any other check. */
+#define PDGEMM_F32 0
+#define PDGEMM_F16 1
+#define PDGEMM_BF16 2
+
+/* The scale of a block whose largest magnitude is a: 2^e, e >= -127, with
+ *   FLOOR  e = floor(log2 a) - 2, the rule of the MX specification: a lies in
+ *          [4, 8) of the scale and magnitudes above 6 * 2^e saturate;
+ *   FIT    the smallest e with a <= 6 * 2^e: nothing saturates. */
+#define PDGEMM_SCALE_FLOOR 0
+#define PDGEMM_SCALE_FIT 1
+
+/* Quantises a dense row-major src, rows x K of src_type (PDGEMM_F32, _F16 or
+ * _BF16; element (i, k) at src[i*ld + k]), along K into (q, scales) and / or
+ * along its rows into (qt, scales_t), the operand of K rows of `rows` values
+ * that is its transpose.  A pair of NULL pointers is a form that is not wanted
+ * (its ld are not looked at); with both wanted, src is read once.  A product
+ * that contracts over src's rows takes the transpose: the gradients of a linear
+ * layer Y = X W^T are dX = G W (W transposed) and dW = G^T X (G and X
+ * transposed).
+ *
+ * Each value is divided by its block's scale and rounded to the nearest e2m1
+ * value, ties to even, magnitudes above 6 to 6; the sign of a zero is kept.  A
+ * block of zeros takes byte 0.  A block that holds an infinity or a NaN takes
+ * byte 255 and zero codes.  The 16-byte chunk of codes that holds a row's last
+ * block is written whole, zeros after the last value; bytes of scales past the
+ * last row are left as they were.  The results are unique, bit for bit. */
+int pdgemm_mxf4_quantize(int64_t rows, int64_t K, const void *src, int64_t ld, int src_type, uint8_t *q,
+                         int64_t ldq, uint8_t *scales, int64_t lds, uint8_t *qt, int64_t ldqt,
+                         uint8_t *scales_t, int64_t ldst, int scale_rule, void *stream);
+
+/* The values of an MXFP4 operand, to a dense row-major dst of dst_type: exact
+ * in binary32 (a magnitude of 2^128 and above, which the quantiser never makes,
+ * is infinite), rounded to nearest even for the 16-bit types (binary16:
+ * overflow gives infinity). */
+int pdgemm_mxf4_dequantize(int64_t rows, int64_t K, const uint8_t *q, int64_t ldq, const uint8_t *scales,
+                           int64_t lds, void *dst, int64_t ldd, int dst_type, void *stream);
+
+/* C = A * B of two MXFP4 operands: A of M rows, B given as its N columns (rows
+ * of K values), C row-major of out_type.  Sums are binary32 in a fixed order,
+ * rounded once to out_type (overflow gives infinity); |C - exact| <=
+ * ceil(K / 64) * 2^-22 * sum |a b| plus that rounding where no sum leaves
+ * binary32's normal range.  K = 0 stores zeros. */
+int gemm_mxf4(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a, int64_t ldsa,
+              const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc,
+              int out_type, void *stream);
+
+/* C = A * B of 16-bit A (a_type PDGEMM_F16 or PDGEMM_BF16, row-major, rows of a
+ * multiple of 16 bytes, 16-byte aligned) and MXFP4 B: weights kept in 4 bits
+ * under activations that are not quantised.  B's values enter exactly; sums and
+ * rounding as in gemm_mxf4. */
+int gemm_a16_mxf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
+                  int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type,
+                  void *stream);
 
 /* Static message for a return code (never NULL): the PDGEMM_E* codes above,
  * or hipGetErrorString() for a positive hipError_t.  Part of the error

@@ -23,6 +23,12 @@ explicitly and the leading dimensions are counted in 4-bit elements.
 The dequantizing variants of the integer GEMMs take float32 scale vectors
 scale_a (M,) and scale_b (N,) and write ((float)sum * scale_a[i]) *
 scale_b[j] as float32, or rounded to float16.
+
+MXFP4 operands (microscaled 4-bit floating point) are a pair of uint8 tensors:
+packed codes (rows, ceil(K/2)), two e2m1 values per byte with the even k in the
+low nibble, and scales (ceil(K/32), rows), the e8m0 byte of each block of 32
+values stored by block (a checkpoint's scales, (rows, K/32), are transposed).
+Rows of both start on multiples of 16 bytes; mxf4_quantize allocates them so.
 """
 from __future__ import annotations
 
@@ -105,6 +111,14 @@ lib.gemm_i4_noalloc.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, 
 lib.gemm_i4_noalloc.restype = _i
 lib.pdgemm_i4_noalloc_max_bytes.argtypes = []
 lib.pdgemm_i4_noalloc_max_bytes.restype = _i64
+lib.pdgemm_mxf4_quantize.argtypes = [_i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p]
+lib.pdgemm_mxf4_quantize.restype = _i
+lib.pdgemm_mxf4_dequantize.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p]
+lib.pdgemm_mxf4_dequantize.restype = _i
+lib.gemm_mxf4.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p]
+lib.gemm_mxf4.restype = _i
+lib.gemm_a16_mxf4.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _p, _i64, _i, _p]
+lib.gemm_a16_mxf4.restype = _i
 lib.pdgemm_strerror.argtypes = [_i]
 lib.pdgemm_strerror.restype = ctypes.c_char_p
 lib.pdgemm_version.argtypes = []
@@ -529,6 +543,185 @@ def gemm_i4_dequant(A: torch.Tensor, Bt: torch.Tensor, scale_a: torch.Tensor,
         out = torch.empty((A.shape[0], Bt.shape[0]), dtype=out_dtype, device=A.device)
     return _call(PREC_I4, A, Bt, out, K, lda, ldb, stream, cfg, (scale_a, scale_b), workspace=workspace,
                  f6cfg=f6cfg)
+
+
+# ---- MXFP4 ----
+
+MX_BLOCK = 32
+_MX_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_MX_RULES = {"floor": 0, "fit": 1}
+
+
+def _round_up(x: int, m: int) -> int:
+    return (x + m - 1) // m * m
+
+
+def _mx_type(dtype, name: str) -> int:
+    if dtype not in _MX_TYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16")
+    return _MX_TYPES[dtype]
+
+
+def _mx_operand(codes: torch.Tensor, scales: torch.Tensor, K: int | None, name: str):
+    """(rows, K, ld in values, scale row stride) of an MXFP4 operand.  An array of a single
+    row has no stride to speak of: it takes the next multiple the library accepts."""
+    for t, what in ((codes, "codes"), (scales, "scales")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+            raise TypeError(f"{name}'s {what} must be a uint8 tensor")
+    ld, lds = _row_major_2d(codes, f"{name}'s codes"), _row_major_2d(scales, f"{name}'s scales")
+    rows = codes.shape[0]
+    K = 2 * codes.shape[1] if K is None else K
+    if K < 0 or 2 * codes.shape[1] < K:
+        raise ValueError(f"{name} holds fewer than K values per row")
+    blocks = (K + MX_BLOCK - 1) // MX_BLOCK
+    if scales.shape[0] < blocks or scales.shape[1] < rows:
+        raise ValueError(f"{name}'s scales must hold {blocks} blocks of {rows} rows")
+    if rows <= 1:
+        ld = _round_up(max(ld, codes.shape[1]), 16)
+    if scales.shape[0] <= 1:
+        lds = _round_up(max(lds, scales.shape[1]), 16)
+    return rows, K, 2 * ld, lds
+
+
+def _mx_call(fn, args, tensors, stream):
+    """Runs fn(*args, stream) for tensors of one GPU, with that GPU current: on `stream`, or
+    on its current stream."""
+    device = tensors[0].device
+    if any(t.device != device for t in tensors):
+        raise ValueError("all tensors must be on the same GPU")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError("stream must be on the tensors' GPU")
+    with torch.cuda.device(device):
+        rc = fn(*args, ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise PdgemmError(rc)
+
+
+def _mx_empty(shape, dtype, device, stream):
+    """A new tensor of the stream that will write it, so that its memory is not handed out
+    again before that stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _mx_alloc(rows: int, K: int, device, stream):
+    """A new MXFP4 operand (codes, scales): rows of a multiple of 16 bytes."""
+    blocks = (K + MX_BLOCK - 1) // MX_BLOCK
+    codes = _mx_empty((rows, 16 * blocks), torch.uint8, device, stream)
+    scales = _mx_empty((blocks, _round_up(rows, 16)), torch.uint8, device, stream)
+    return codes[:, :(K + 1) // 2], scales[:, :rows]
+
+
+def _mx_out(out, rows: int, K: int, device, stream, name: str):
+    """An operand to write: `out`, checked, or a new one; with its strides."""
+    codes, scales = _mx_alloc(rows, K, device, stream) if out is None else out
+    r, _, ld, lds = _mx_operand(codes, scales, K, name)
+    if r != rows:
+        raise ValueError(f"{name} must have {rows} rows")
+    return codes, scales, ld, lds
+
+
+def _mx_quantize(x, along_k: bool, along_rows: bool, scale_rule, out, out_t, stream):
+    kind = _mx_type(x.dtype, "x")
+    if scale_rule not in _MX_RULES:
+        raise ValueError(f"scale_rule must be one of {sorted(_MX_RULES)}")
+    ld = _row_major_2d(x, "x")
+    rows, K = x.shape
+    q = _mx_out(out, rows, K, x.device, stream, "out") if along_k else None
+    qt = _mx_out(out_t, K, rows, x.device, stream, "the transposed out") if along_rows else None
+    tensors, forms = [x], []
+    for form in (q, qt):
+        if form is None:
+            forms += [None, 0, None, 0]
+        else:
+            tensors += form[:2]
+            forms += [form[0].data_ptr(), form[2], form[1].data_ptr(), form[3]]
+    if rows and K:
+        _mx_call(lib.pdgemm_mxf4_quantize, (rows, K, x.data_ptr(), ld, kind, *forms, _MX_RULES[scale_rule]),
+                 tensors, stream)
+    return (None if q is None else q[:2]), (None if qt is None else qt[:2])
+
+
+def mxf4_quantize(x: torch.Tensor, transpose: bool = False, scale_rule: str = "floor", out=None, stream=None):
+    """(codes, scales) of x (rows, K), float32, float16 or bfloat16, in MXFP4 along K; with
+    transpose, of its transpose: K rows quantised along x's rows, for a product that contracts
+    over them.  scale_rule "floor" is the rule of the MX specification (values above 6 times
+    the scale saturate), "fit" takes the smallest scale at which none does.  A block that holds
+    an infinity or a NaN becomes NaN.  out: a (codes, scales) pair to write."""
+    if transpose:
+        return _mx_quantize(x, False, True, scale_rule, None, out, stream)[1]
+    return _mx_quantize(x, True, False, scale_rule, out, None, stream)[0]
+
+
+def mxf4_quantize_both(x: torch.Tensor, scale_rule: str = "floor", out=None, stream=None):
+    """((codes, scales), (codes_t, scales_t)): mxf4_quantize of x and of its transpose, from one
+    read of x.  out: a pair of such pairs to write."""
+    first, second = (None, None) if out is None else out
+    return _mx_quantize(x, True, True, scale_rule, first, second, stream)
+
+
+def mxf4_dequantize(codes: torch.Tensor, scales: torch.Tensor, K: int | None = None,
+                    out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                    stream=None) -> torch.Tensor:
+    """The values (rows, K) of an MXFP4 operand, as out's dtype, else out_dtype (float32: exact)."""
+    rows, K, ld, lds = _mx_operand(codes, scales, K, "the operand")
+    _mx_type(out_dtype if out is None else out.dtype, "the output")
+    if out is None:
+        out = _mx_empty((rows, K), out_dtype, codes.device, stream)
+    elif tuple(out.shape) != (rows, K):
+        raise ValueError(f"out must have shape {(rows, K)}")
+    if rows and K:
+        _mx_call(lib.pdgemm_mxf4_dequantize, (rows, K, codes.data_ptr(), ld, scales.data_ptr(), lds, out.data_ptr(),
+                                              _row_major_2d(out, "out"), _mx_type(out.dtype, "out")),
+                 [codes, scales, out], stream)
+    return out
+
+
+def _mx_product_out(out, M, N, out_dtype, device, stream):
+    _mx_type(out_dtype if out is None else out.dtype, "the output")
+    if out is None:
+        out = _mx_empty((M, N), out_dtype, device, stream)
+    elif tuple(out.shape) != (M, N):
+        raise ValueError(f"out must have shape {(M, N)}")
+    return out, _row_major_2d(out, "out")
+
+
+def gemm_mxf4(A: torch.Tensor, scale_a: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, K: int | None = None,
+              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """C = A * B of MXFP4 A (M rows) and Bt (N rows); binary32 sums, C (M, N) float32, float16
+    or bfloat16 (out's dtype, else out_dtype)."""
+    K = 2 * min(A.shape[1], Bt.shape[1]) if K is None else K
+    M, K, lda, ldsa = _mx_operand(A, scale_a, K, "A")
+    N, K, ldb, ldsb = _mx_operand(Bt, scale_b, K, "Bt")
+    out, ldc = _mx_product_out(out, M, N, out_dtype, A.device, stream)
+    if M and N:
+        _mx_call(lib.gemm_mxf4, (M, N, K, A.data_ptr(), lda, scale_a.data_ptr(), ldsa, Bt.data_ptr(), ldb,
+                                 scale_b.data_ptr(), ldsb, out.data_ptr(), ldc, _mx_type(out.dtype, "out")),
+                 [A, scale_a, Bt, scale_b, out], stream)
+    return out
+
+
+def gemm_a16_mxf4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, out: torch.Tensor | None = None,
+                  out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """C = A * B of float16 or bfloat16 A (M, K), rows of a multiple of 16 bytes, and MXFP4 Bt
+    (N rows of K values); binary32 sums, C (M, N) float32, float16 or bfloat16."""
+    if A.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("gemm_a16_mxf4 takes a float16 or bfloat16 A")
+    lda = _row_major_2d(A, "A")
+    M, K = A.shape
+    if M <= 1:
+        lda = _round_up(lda, 8)
+    N, K, ldb, ldsb = _mx_operand(Bt, scale_b, K, "Bt")
+    out, ldc = _mx_product_out(out, M, N, out_dtype, A.device, stream)
+    if M and N:
+        _mx_call(lib.gemm_a16_mxf4, (M, N, K, A.data_ptr(), lda, _mx_type(A.dtype, "A"), Bt.data_ptr(), ldb,
+                                     scale_b.data_ptr(), ldsb, out.data_ptr(), ldc, _mx_type(out.dtype, "out")),
+                 [A, scale_b, out, Bt], stream)
+    return out
 
 
 def prepare(prec: str, A: torch.Tensor, Bt: torch.Tensor, out: torch.Tensor, K: int | None = None,

@@ -6,7 +6,7 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", "pdgemm.hip")]
+SOURCES = [os.path.join(HERE, "csrc", name) for name in ("pdgemm.hip", "mxfp4.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libpdgemm.so")
 

@@ -1,0 +1,913 @@
+// mxfp4.hip -- microscaled 4-bit floating point (MXFP4) for gfx950 (MI355X):
+// quantising, reading back, and the products, behind the C ABI declared in
+// include/pdgemm.h.
+//
+// An MXFP4 operand holds `rows` rows of K values.  32 consecutive values of K
+// share a block scale: value = e2m1(code) * 2^(byte - 127), byte 255 = NaN.
+// The codes are packed two per byte (even k in the low nibble), so a block is
+// one 16-byte chunk of its row.  The scales are stored by block: scale of block b
+// of row i at scales[b * lds + i].  A tile of rows then reads its scales of one
+// block as one contiguous run (with a row's scales side by side instead, a tile's
+// scales of one stage would be a few bytes of each of its rows' lines, and the L2
+// returns whole lines).
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+#include <stdlib.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "pdgemm.h"
+
+namespace {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float floatx2_t __attribute__((ext_vector_type(2)));
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+typedef int intx8_t __attribute__((ext_vector_type(8)));
+typedef unsigned int uintx4_t __attribute__((ext_vector_type(4)));
+typedef unsigned short ushortx2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kF32 = PDGEMM_F32;
+constexpr int kF16 = PDGEMM_F16;
+constexpr int kBF16 = PDGEMM_BF16;
+
+constexpr int kWave = 64;
+constexpr int kBlock = 32;   // values per scale
+
+// Buffer resource word 3 for raw (untyped) buffer loads on gfx9-family parts.
+constexpr int kRsrcWord3 = 0x00020000;
+
+template <int T> struct ElemOf { using type = float; };
+template <> struct ElemOf<kF16> { using type = _Float16; };
+template <> struct ElemOf<kBF16> { using type = __bf16; };
+constexpr int elem_size(int t) { return t == kF32 ? 4 : 2; }
+
+// ---------------------------------------------------------------------------
+// Block scales
+//
+// With a = the largest magnitude of a block and E = floor(log2 a), the scale is
+// 2^e, e = max(E - 2, -127): the largest power of two of e2m1 is 2^2, so a lies in
+// [4, 8) of it and what exceeds 6 saturates (PDGEMM_SCALE_FLOOR, the rule of the
+// OCP microscaling formats).  PDGEMM_SCALE_FIT takes e one higher where a > 6 * 2^e,
+// so nothing saturates.  A block of zeros takes byte 0; one that holds an infinity
+// or a NaN takes byte 255, which makes the whole block NaN, and zero codes.
+
+// what is added to the bits of a before its exponent is read: FIT carries into the
+// exponent where the mantissa is above 1.5
+__host__ __device__ constexpr uint32_t rule_bias(int rule) { return rule == PDGEMM_SCALE_FIT ? 0x3FFFFFu : 0u; }
+
+// the scale's byte from the binary32 bits of a
+__device__ __forceinline__ uint32_t scale_byte(uint32_t a, uint32_t bias) {
+    const int b = max((int)((a + bias) >> 23) - 2, 0);
+    return a >= 0x7F800000u ? 255u : (uint32_t)b;
+}
+
+// binary32 2^(byte - 127) of a byte below 255 (byte 0: the subnormal 2^-127)
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    return __builtin_bit_cast(float, max(byte << 23, 0x00400000u));
+}
+
+// binary32 bits of the magnitude whose 16-bit pattern (f16 or bf16) is h
+template <int T>
+__device__ __forceinline__ uint32_t magnitude_bits(uint32_t h) {
+    if constexpr (T == kBF16) return h << 16;
+    return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)h));
+}
+
+// Two values of a pair (16-bit types: packed in `x`) over `scale`, rounded to nearest
+// even and saturated at 6, as byte kSel of `old`.
+template <int T, int kSel>
+__device__ __forceinline__ uint32_t codes16(uint32_t old, uint32_t x, float scale) {
+    if constexpr (T == kF16)
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(half2_t, x), scale, kSel);
+    else
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2_t, x), scale, kSel);
+}
+template <int kSel>
+__device__ __forceinline__ uint32_t codes32(uint32_t old, float x, float y, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, x, y, scale, kSel);
+}
+
+// maximum over groups of 4, 8 or 16 lanes (in every lane); every lane is active
+template <int kLanes>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));                            // quad_perm 1 0 3 2
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));                            // quad_perm 2 3 0 1
+    if constexpr (kLanes >= 8) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));   // row_half_mirror
+    if constexpr (kLanes >= 16) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));  // row_mirror
+    return v;
+}
+
+struct QuantArgs {
+    const void *src;
+    uint8_t *q;    // packed along K (NULL: not written)
+    uint8_t *s;
+    uint8_t *qt;   // the transpose: packed along the rows (NULL: not written)
+    uint8_t *st;
+    int64_t ld;    // elements
+    int64_t ldq;   // bytes
+    int64_t lds;
+    int64_t ldqt;  // bytes
+    int64_t ldst;
+    int rows, K;
+    int tiles_k;   // workgroups along K
+    uint32_t bias;
+};
+
+// Rows along K only.  A lane takes 16 bytes of a row, a wave a span of 64 of them,
+// so every load instruction reads 1 KB of one row, and a block is 4 (fp32: 8)
+// neighbouring lanes.  A workgroup of 4 waves takes 4 * kRpw rows of one span; the
+// scales go through LDS so that a block's scales of those rows are written as one run.
+template <int T, int kRpw>
+__global__ __launch_bounds__(256) void mx_quant_rows_kernel(QuantArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using Elem = typename ElemOf<T>::type;
+    constexpr int kVals = 16 / elem_size(T);      // values per lane
+    constexpr int kLanes = kBlock / kVals;        // lanes per block
+    constexpr int kSpan = kWave * kVals;
+    constexpr int kBlocks = kSpan / kBlock;       // blocks per span
+    constexpr int kRows = 4 * kRpw;
+    __shared__ uint8_t sc[kBlocks][kRows];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int tile_m = blockIdx.x / args.tiles_k, tile_k = blockIdx.x % args.tiles_k;
+    const int row0 = tile_m * kRows + wave * kRpw;
+    const int k0 = tile_k * kSpan + lane * kVals;
+    const int K = args.K;
+
+    uint32_t v[kRpw][4];
+    const Elem *const src = static_cast<const Elem *>(args.src) + k0;
+#pragma unroll
+    for (int r = 0; r < kRpw; ++r) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) v[r][d] = 0;
+        if (row0 + r >= args.rows) continue;
+        const Elem *const p = src + (int64_t)(row0 + r) * args.ld;
+        if (k0 + kVals <= K) {
+            __builtin_memcpy(v[r], p, 16);        // rows need only the element's alignment
+        } else {
+            Elem e[kVals] = {};
+#pragma unroll
+            for (int x = 0; x < kVals; ++x)
+                if (k0 + x < K) e[x] = p[x];
+            __builtin_memcpy(v[r], e, 16);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRpw; ++r) {
+        uint32_t a;
+        if constexpr (T == kF32) {
+            a = max(max(v[r][0] & 0x7FFFFFFFu, v[r][1] & 0x7FFFFFFFu), max(v[r][2] & 0x7FFFFFFFu, v[r][3] & 0x7FFFFFFFu));
+            a = group_max<kLanes>(a);
+        } else {
+            // magnitudes of either 16-bit type order as their bit patterns
+            ushortx2_t m = __builtin_bit_cast(ushortx2_t, v[r][0] & 0x7FFF7FFFu);
+#pragma unroll
+            for (int d = 1; d < 4; ++d)
+                m = __builtin_elementwise_max(m, __builtin_bit_cast(ushortx2_t, v[r][d] & 0x7FFF7FFFu));
+            a = magnitude_bits<T>(group_max<kLanes>(max((uint32_t)m[0], (uint32_t)m[1])));
+        }
+        const uint32_t byte = scale_byte(a, args.bias);
+        const float scale = scale_value(byte);
+        uint32_t c = 0;
+        if constexpr (T == kF32) {
+            c = codes32<0>(c, __builtin_bit_cast(float, v[r][0]), __builtin_bit_cast(float, v[r][1]), scale);
+            c = codes32<1>(c, __builtin_bit_cast(float, v[r][2]), __builtin_bit_cast(float, v[r][3]), scale);
+        } else {
+            c = codes16<T, 0>(c, v[r][0], scale);
+            c = codes16<T, 1>(c, v[r][1], scale);
+            c = codes16<T, 2>(c, v[r][2], scale);
+            c = codes16<T, 3>(c, v[r][3], scale);
+        }
+        if (byte == 255) c = 0;
+        if (lane % kLanes == 0) sc[lane / kLanes][wave * kRpw + r] = (uint8_t)byte;
+        // the chunk that holds the row's last value is written whole
+        if (row0 + r < args.rows && k0 - k0 % kBlock < K) {
+            uint8_t *const q = args.q + (int64_t)(row0 + r) * args.ldq + k0 / 2;
+            if constexpr (T == kF32)
+                *reinterpret_cast<uint16_t *>(q) = (uint16_t)c;
+            else
+                *reinterpret_cast<uint32_t *>(q) = c;
+        }
+    }
+    __syncthreads();
+    const int blocks = (K + kBlock - 1) / kBlock;
+    for (int x = tid; x < kBlocks * kRows; x += 256) {
+        const int b = tile_k * kBlocks + x / kRows, i = tile_m * kRows + x % kRows;
+        if (b < blocks && i < args.rows) args.s[(int64_t)b * args.lds + i] = sc[x / kRows][x % kRows];
+    }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// The transpose, and with kBoth the rows along K too, from one read.  A lane takes two
+// neighbouring columns of 32 rows, so a load instruction of a wave reads a run of 128
+// columns of one row; a column's block is in one lane's registers and a row's block in
+// 16 neighbouring lanes.  A workgroup of 8 waves takes 256 rows x 128 columns, and the
+// codes (4 bits a value) go through LDS so that both forms are written in runs of whole
+// chunks: 128 bytes per column, 64 bytes per row.
+template <int T, bool kBoth>
+__global__ __launch_bounds__(512) void mx_quant_cols_kernel(QuantArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using Elem = typename ElemOf<T>::type;
+    constexpr int kRows = 256, kCols = 128;
+    constexpr int kD = T == kF32 ? 2 : 1;         // dwords per pair of columns
+    __shared__ uint4 lqt[kCols][8];               // chunk w of column c at w ^ ((c / 2) % 8)
+    __shared__ __align__(16) uint8_t lq[kBoth ? kRows : 1][64];
+    __shared__ uint8_t sct[8][kCols];
+    __shared__ uint8_t scr[4][kBoth ? kRows : 1];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int tile_m = blockIdx.x / args.tiles_k, tile_k = blockIdx.x % args.tiles_k;
+    const int m0 = tile_m * kRows, c0 = tile_k * kCols;
+    const int row0 = m0 + wave * 32;
+    const int k = c0 + 2 * lane;
+    const int rows = args.rows, K = args.K;
+
+    uint32_t v[32][kD];
+    const Elem *const src = static_cast<const Elem *>(args.src) + k;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+#pragma unroll
+        for (int d = 0; d < kD; ++d) v[r][d] = 0;
+        if (row0 + r >= rows) continue;
+        const Elem *const p = src + (int64_t)(row0 + r) * args.ld;
+        if (k + 1 < K) {
+            __builtin_memcpy(v[r], p, 4 * kD);
+        } else if (k < K) {
+            Elem e[2] = {};
+            e[0] = p[0];
+            __builtin_memcpy(v[r], e, 4 * kD);
+        }
+    }
+
+    if constexpr (kBoth) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            uint32_t a;
+            if constexpr (T == kF32)
+                a = group_max<16>(max(v[r][0] & 0x7FFFFFFFu, v[r][1] & 0x7FFFFFFFu));
+            else
+                a = magnitude_bits<T>(group_max<16>(max(v[r][0] & 0x7FFFu, (v[r][0] >> 16) & 0x7FFFu)));
+            const uint32_t byte = scale_byte(a, args.bias);
+            const float scale = scale_value(byte);
+            uint32_t c;
+            if constexpr (T == kF32)
+                c = codes32<0>(0, __builtin_bit_cast(float, v[r][0]), __builtin_bit_cast(float, v[r][1]), scale);
+            else
+                c = codes16<T, 0>(0, v[r][0], scale);
+            lq[wave * 32 + r][lane] = byte == 255 ? 0 : (uint8_t)c;
+            if (lane % 16 == 0) scr[lane / 16][wave * 32 + r] = (uint8_t)byte;
+        }
+    }
+
+    uint32_t a0 = 0, a1 = 0;   // the two columns' magnitudes
+    if constexpr (T == kF32) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            a0 = max(a0, v[r][0] & 0x7FFFFFFFu);
+            a1 = max(a1, v[r][1] & 0x7FFFFFFFu);
+        }
+    } else {
+        ushortx2_t m = {0, 0};
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(ushortx2_t, v[r][0] & 0x7FFF7FFFu));
+        a0 = magnitude_bits<T>(m[0]);
+        a1 = magnitude_bits<T>(m[1]);
+    }
+    const uint32_t b0 = scale_byte(a0, args.bias), b1 = scale_byte(a1, args.bias);
+    const float s0 = scale_value(b0), s1 = scale_value(b1);
+    uint32_t w0[4], w1[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        uint32_t x = 0, y = 0;
+        const auto pair = [&](auto sel_c) __attribute__((always_inline)) {
+            constexpr int kSel = decltype(sel_c)::value;
+            const int r = 8 * d + 2 * kSel;
+            if constexpr (T == kF32) {
+                x = codes32<kSel>(x, __builtin_bit_cast(float, v[r][0]), __builtin_bit_cast(float, v[r + 1][0]), s0);
+                y = codes32<kSel>(y, __builtin_bit_cast(float, v[r][kD - 1]), __builtin_bit_cast(float, v[r + 1][kD - 1]), s1);
+            } else {
+                x = codes16<T, kSel>(x, __builtin_amdgcn_perm(v[r + 1][0], v[r][0], 0x05040100u), s0);
+                y = codes16<T, kSel>(y, __builtin_amdgcn_perm(v[r + 1][0], v[r][0], 0x07060302u), s1);
+            }
+        };
+        pair(std::integral_constant<int, 0>{});
+        pair(std::integral_constant<int, 1>{});
+        pair(std::integral_constant<int, 2>{});
+        pair(std::integral_constant<int, 3>{});
+        w0[d] = b0 == 255 ? 0 : x;
+        w1[d] = b1 == 255 ? 0 : y;
+    }
+    const int pos = wave ^ (lane & 7);
+    lqt[2 * lane][pos] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+    lqt[2 * lane + 1][pos] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+    sct[wave][2 * lane] = (uint8_t)b0;
+    sct[wave][2 * lane + 1] = (uint8_t)b1;
+    __syncthreads();
+
+    const int blocks_k = (K + kBlock - 1) / kBlock, blocks_m = (rows + kBlock - 1) / kBlock;
+#pragma unroll
+    for (int x = tid; x < kCols * 8; x += 512) {
+        const int c = x / 8, w = x % 8;
+        if (c0 + c < K && m0 + 32 * w < rows)
+            *reinterpret_cast<uint4 *>(args.qt + (int64_t)(c0 + c) * args.ldqt + m0 / 2 + 16 * w) =
+                lqt[c][w ^ ((c >> 1) & 7)];
+    }
+    for (int x = tid; x < 8 * kCols; x += 512) {
+        const int w = x / kCols, c = x % kCols;
+        if (c0 + c < K && m0 / 32 + w < blocks_m) args.st[(int64_t)(m0 / 32 + w) * args.ldst + c0 + c] = sct[w][c];
+    }
+    if constexpr (kBoth) {
+#pragma unroll
+        for (int x = tid; x < kRows * 4; x += 512) {
+            const int r = x / 4, w = x % 4;
+            if (m0 + r < rows && c0 + 32 * w < K)
+                *reinterpret_cast<uint4 *>(args.q + (int64_t)(m0 + r) * args.ldq + c0 / 2 + 16 * w) =
+                    *reinterpret_cast<const uint4 *>(&lq[r][16 * w]);
+        }
+        for (int x = tid; x < 4 * kRows; x += 512) {
+            const int w = x / kRows, r = x % kRows;
+            if (m0 + r < rows && c0 / 32 + w < blocks_k) args.s[(int64_t)(c0 / 32 + w) * args.lds + m0 + r] = scr[w][r];
+        }
+    }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+struct DequantArgs {
+    const uint8_t *q;
+    const uint8_t *s;
+    void *dst;
+    int64_t ldq;   // bytes
+    int64_t lds;
+    int64_t ldd;   // elements
+    int rows, K;
+    int tiles_k;
+};
+
+// Values back from codes and scales.  A lane takes 8 values (4 bytes) of a row, a wave
+// 512, a workgroup of 4 waves 4 * kRpw rows of that span, whose scales it first reads
+// into LDS, a run of rows per block.
+template <int T, int kRpw>
+__global__ __launch_bounds__(256) void mx_dequant_kernel(DequantArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using Elem = typename ElemOf<T>::type;
+    constexpr int kVals = 8, kSpan = kWave * kVals, kBlocks = kSpan / kBlock, kRows = 4 * kRpw;
+    __shared__ uint8_t sc[kBlocks][kRows];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int tile_m = blockIdx.x / args.tiles_k, tile_k = blockIdx.x % args.tiles_k;
+    const int row0 = tile_m * kRows + wave * kRpw;
+    const int k0 = tile_k * kSpan + lane * kVals;
+    const int K = args.K;
+    const int blocks = (K + kBlock - 1) / kBlock;
+
+    uint32_t w[kRpw];
+#pragma unroll
+    for (int r = 0; r < kRpw; ++r) {
+        w[r] = 0;
+        if (row0 + r < args.rows && k0 < K)
+            w[r] = *reinterpret_cast<const uint32_t *>(args.q + (int64_t)(row0 + r) * args.ldq + k0 / 2);
+    }
+    for (int x = tid; x < kBlocks * kRows; x += 256) {
+        const int b = tile_k * kBlocks + x / kRows, i = tile_m * kRows + x % kRows;
+        sc[x / kRows][x % kRows] = b < blocks && i < args.rows ? args.s[(int64_t)b * args.lds + i] : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRpw; ++r) {
+        if (row0 + r >= args.rows || k0 >= K) continue;
+        const uint32_t byte = sc[lane / (kBlock / kVals)][wave * kRpw + r];
+        const float scale = scale_value(byte);
+        float f[kVals];
+        const auto pair = [&](auto sel_c) __attribute__((always_inline)) {
+            constexpr int kSel = decltype(sel_c)::value;
+            const floatx2_t p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r], scale, kSel);
+            f[2 * kSel] = byte == 255 ? __builtin_nanf("") : p[0];
+            f[2 * kSel + 1] = byte == 255 ? __builtin_nanf("") : p[1];
+        };
+        pair(std::integral_constant<int, 0>{});
+        pair(std::integral_constant<int, 1>{});
+        pair(std::integral_constant<int, 2>{});
+        pair(std::integral_constant<int, 3>{});
+        Elem e[kVals];
+#pragma unroll
+        for (int x = 0; x < kVals; ++x) e[x] = (Elem)f[x];
+        Elem *const p = static_cast<Elem *>(args.dst) + (int64_t)(row0 + r) * args.ldd + k0;
+        if (k0 + kVals <= K) {
+            __builtin_memcpy(p, e, sizeof(e));
+        } else {
+#pragma unroll
+            for (int x = 0; x < kVals; ++x)
+                if (k0 + x < K) p[x] = e[x];
+        }
+    }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// ---------------------------------------------------------------------------
+// Products
+//
+// C[i][j] = sum over blocks b of 2^(sa + sb - 254) * sum over k in b of a * b: the
+// scaled MFMA v_mfma_scale_f32_16x16x128_f8f6f4 with e2m1 operands.  Lane l of a
+// 16-row fragment holds the 32 values of block l / 16 of row l % 16, one 16-byte chunk,
+// and that block's scale in a byte of a scale register.
+
+struct MxArgs {
+    const uint8_t *A;    // packed e2m1, or 16-bit values (the a16 product)
+    const uint8_t *SA;
+    const uint8_t *B;
+    const uint8_t *SB;
+    void *C;
+    int64_t lda, ldb;    // bytes
+    int64_t ldsa, ldsb;
+    int64_t ldc;         // elements
+    int M, N, K;
+    int tiles_m, tiles_n;
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int range) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, range, kRsrcWord3);
+}
+
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    const uintx4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// n (1, 2 or 4) bytes, zero-extended
+template <int n>
+__device__ __forceinline__ uint32_t load_bytes(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    if constexpr (n == 1) return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
+    if constexpr (n == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    if constexpr (n == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+}
+
+template <int kOpA, int kOpB>
+__device__ __forceinline__ floatx4_t mfma_fp4(const uint4 &a, const uint4 &b, const floatx4_t &c, uint32_t sa, uint32_t sb) {
+    const intx8_t a8 = {(int)a.x, (int)a.y, (int)a.z, (int)a.w};
+    const intx8_t b8 = {(int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    // format 4 of both operands: e2m1
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, kOpA, (int)sa, kOpB, (int)sb);
+}
+
+// f(std::integral_constant<int, i>) for i = 0 .. N-1, in order
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(F &&f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        static_for<N, I + 1>(f);
+    }
+}
+
+// Sum of the waves' partial tiles (each wave summed its own range of K) in wave order,
+// rounded once to C's type and stored.  acc[i][j] of a wave holds, in register e of lane
+// l, row FM * (4 (l / 16) + e) + i and column FN * (l % 16) + j of the tile.
+template <int FM, int FN, int W, int OT>
+__device__ __forceinline__ void join_and_store(floatx4_t (&acc)[FM][FN], const MxArgs &args, int m0, int n0, int tid,
+                                               int lane, int wave) {
+    using Out = typename ElemOf<OT>::type;
+    constexpr int BM = 16 * FM, BN = 16 * FN;
+    __shared__ float part[W][FM * FN * 4][kWave];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[wave][(i * FN + j) * 4 + e][lane] = acc[i][j][e];
+    __syncthreads();
+    Out *const C = static_cast<Out *>(args.C);
+    for (int x = tid; x < BM * BN; x += W * kWave) {
+        const int row = x / BN, col = x % BN;
+        if (m0 + row >= args.M || n0 + col >= args.N) continue;
+        const int rr = row / FM, cc = col / FN;
+        const int reg = ((row % FM) * FN + col % FN) * 4 + (rr & 3), l = (rr >> 2) * 16 + cc;
+        float sum = part[0][reg][l];
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += part[w][reg][l];
+        C[(int64_t)(m0 + row) * args.ldc + n0 + col] = (Out)sum;
+    }
+}
+
+// Few rows: a tile of 16 FM x 16 FN of C per workgroup, whose W waves take the 128-byte
+// lines of K in turn and read them from memory straight into the fragments' registers,
+// kLines lines at once.  Fragment i holds rows FM r + i (r = 0 .. 15), so that a lane's
+// scales of its fragments are neighbouring bytes.
+template <int FM, int FN, int W, int kLines, int OT>
+__global__ __launch_bounds__(W *kWave) void mx_small_kernel(MxArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int BM = 16 * FM, BN = 16 * FN;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int r = lane & 15, g = lane >> 4;
+    const int m0 = (blockIdx.x / args.tiles_n) * BM, n0 = (blockIdx.x % args.tiles_n) * BN;
+    const int M = args.M, N = args.N, K = args.K;
+    const int blocks = (K + kBlock - 1) / kBlock;
+    const int lines = (blocks + 7) / 8;
+
+    // rows past M (N) repeat the last one; their results are not stored
+    uint32_t va[FM], vb[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) va[i] = (uint32_t)((min(m0 + FM * r + i, M - 1) - m0) * args.lda) + g * 16;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) vb[j] = (uint32_t)((min(n0 + FN * r + j, N - 1) - n0) * args.ldb) + g * 16;
+    const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
+    const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
+    const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + blocks * 16;
+    const int b_end = (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16;
+    // a block's scales are read up to the 16-byte granule that holds the last row's
+    const int sa_cols = min(((M + 15) & ~15) - m0, BM), sb_cols = min(((N + 15) & ~15) - n0, BN);
+
+    floatx4_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0, 0, 0, 0};
+
+    for (int first = wave; first < lines; first += W * kLines) {
+        uint4 fa[kLines][2][FM], fb[kLines][2][FN];
+        uint32_t sa[kLines][2], sb[kLines][2];
+#pragma unroll
+        for (int u = 0; u < kLines; ++u) {
+            // a line past K reads nothing: zeros come back
+            const int line = first + u * W;
+            const int nb = min(blocks - line * 8, 8);
+            const auto ra = rsrc(a_base, nb > 0 ? a_end : 0), rb = rsrc(b_base, nb > 0 ? b_end : 0);
+            const auto rsa = rsrc(args.SA + (int64_t)line * 8 * args.ldsa + m0, nb > 0 ? (int)((nb - 1) * args.ldsa) + sa_cols : 0);
+            const auto rsb = rsrc(args.SB + (int64_t)line * 8 * args.ldsb + n0, nb > 0 ? (int)((nb - 1) * args.ldsb) + sb_cols : 0);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) fb[u][q][j] = load16(rb, vb[j] + line * 128 + q * 64);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) fa[u][q][i] = load16(ra, va[i] + line * 128 + q * 64);
+                sa[u][q] = load_bytes<FM>(rsa, (uint32_t)((4 * q + g) * args.ldsa) + FM * r);
+                sb[u][q] = load_bytes<FN>(rsb, (uint32_t)((4 * q + g) * args.ldsb) + FN * r);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kLines; ++u) {
+            const int line = first + u * W;
+            if (line * 256 + 256 > K) {
+                // A's values at and beyond K become zeros: what is beside them in B is
+                // finite (e2m1 holds nothing else), and scales past the last block are zero
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int n = K - (line * 256 + q * 128 + g * kBlock);
+                    uint32_t m[4];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int left = n - 8 * d;
+                        m[d] = left >= 8 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (4 * left)) - 1u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) {
+                        fa[u][q][i].x &= m[0];
+                        fa[u][q][i].y &= m[1];
+                        fa[u][q][i].z &= m[2];
+                        fa[u][q][i].w &= m[3];
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                static_for<FM>([&](auto i_c) __attribute__((always_inline)) {
+                    static_for<FN>([&](auto j_c) __attribute__((always_inline)) {
+                        constexpr int i = decltype(i_c)::value, j = decltype(j_c)::value;
+                        acc[i][j] = mfma_fp4<i, j>(fa[u][q][i], fb[u][q][j], acc[i][j], sa[u][q], sb[u][q]);
+                    });
+                });
+        }
+    }
+    join_and_store<FM, FN, W, OT>(acc, args, m0, n0, tid, lane, wave);
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// 16-bit activations times MXFP4 weights.  The codes become the 16-bit type exactly
+// (e2m1 values need two significant bits); an MFMA of 32 values of K covers one block,
+// and its result is scaled by the block's 2^(byte - 127) as it is added to the sum, in
+// binary32: with the scale in the 16-bit operand instead, an f16 weight below 2^-24
+// would vanish.
+template <int T>
+__device__ __forceinline__ floatx4_t mfma16(const uint4 &a, const uint4 &b) {
+    const floatx4_t zero = {0, 0, 0, 0};
+    if constexpr (T == kF16) {
+        half8_t x, y;
+        __builtin_memcpy(&x, &a, 16);
+        __builtin_memcpy(&y, &b, 16);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, zero, 0, 0, 0);
+    } else {
+        bf16x8_t x, y;
+        __builtin_memcpy(&x, &a, 16);
+        __builtin_memcpy(&y, &b, 16);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, zero, 0, 0, 0);
+    }
+}
+
+// the eight values of a dword of codes as the 16-bit type
+template <int T>
+__device__ __forceinline__ uint4 widen(uint32_t w) {
+    uint32_t x[4];
+    static_for<4>([&](auto s_c) __attribute__((always_inline)) {
+        constexpr int s = decltype(s_c)::value;
+        if constexpr (T == kF16) {
+            const half2_t h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, s);
+            x[s] = __builtin_bit_cast(uint32_t, h);
+        } else {
+            const bf16x2_t h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, s);
+            x[s] = __builtin_bit_cast(uint32_t, h);
+        }
+    });
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// binary32 of a scale byte, 255 included (NaN)
+__device__ __forceinline__ float scale_or_nan(uint32_t byte) {
+    return byte == 255 ? __builtin_nanf("") : scale_value(byte);
+}
+
+// Dword t of the chunks that the four 16-lane groups hold goes to group t: chunk g of
+// group g holds block g, and afterwards w[t] of group g is dword g of block t.
+__device__ __forceinline__ void transpose_groups(uint32_t (&w)[4]) {
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    w[0] = c[0];
+    w[1] = c[1];
+    w[2] = d[0];
+    w[3] = d[1];
+}
+
+// The same tile as mx_small_kernel, with A in 16 bits (T).
+template <int T, int FM, int FN, int W, int OT>
+__global__ __launch_bounds__(W *kWave) void a16_small_kernel(MxArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int BM = 16 * FM, BN = 16 * FN;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int r = lane & 15, g = lane >> 4;
+    const int m0 = (blockIdx.x / args.tiles_n) * BM, n0 = (blockIdx.x % args.tiles_n) * BN;
+    const int M = args.M, N = args.N, K = args.K;
+    const int blocks = (K + kBlock - 1) / kBlock;
+    const int lines = (blocks + 7) / 8;
+
+    uint32_t va[FM], vb[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) va[i] = (uint32_t)((min(m0 + FM * r + i, M - 1) - m0) * args.lda) + g * 16;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) vb[j] = (uint32_t)((min(n0 + FN * r + j, N - 1) - n0) * args.ldb) + g * 16;
+    const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
+    const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
+    const auto ra = rsrc(a_base, (int)((min(BM, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15));
+    const auto rb = rsrc(b_base, (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16);
+    const int sb_cols = min(((N + 15) & ~15) - n0, BN);
+
+    floatx4_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0, 0, 0, 0};
+
+    for (int line = wave; line < lines; line += W) {
+        const int nb = min(blocks - line * 8, 8);
+        const auto rsb = rsrc(args.SB + (int64_t)line * 8 * args.ldsb + n0, (int)((nb - 1) * args.ldsb) + sb_cols);
+        uint4 fb[2][FN];
+        uint32_t sb[8];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) fb[q][j] = load16(rb, vb[j] + line * 128 + q * 64);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) sb[b] = load_bytes<FN>(rsb, (uint32_t)(b * args.ldsb) + FN * r);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t w[FN][4];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                w[j][0] = fb[q][j].x;
+                w[j][1] = fb[q][j].y;
+                w[j][2] = fb[q][j].z;
+                w[j][3] = fb[q][j].w;
+                transpose_groups(w[j]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint4 fa[FM];
+#pragma unroll
+                for (int i = 0; i < FM; ++i) fa[i] = load16(ra, va[i] + line * 512 + (4 * q + t) * 64);
+                if (line * 256 + 256 > K) {
+                    // A's values at and beyond K may be anything, a NaN too: they become zeros
+                    const int n = K - (line * 256 + (4 * q + t) * kBlock + g * 8);
+                    uint32_t m[4];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) m[d] = n >= 2 * d + 2 ? 0xFFFFFFFFu : n == 2 * d + 1 ? 0xFFFFu : 0u;
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) {
+                        fa[i].x &= m[0];
+                        fa[i].y &= m[1];
+                        fa[i].z &= m[2];
+                        fa[i].w &= m[3];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const uint4 b = widen<T>(w[j][t]);
+                    const float s = scale_or_nan((sb[4 * q + t] >> (8 * j)) & 255u);
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) {
+                        const floatx4_t p = mfma16<T>(fa[i], b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], s, acc[i][j][e]);
+                    }
+                }
+            }
+        }
+    }
+    join_and_store<FM, FN, W, OT>(acc, args, m0, n0, tid, lane, wave);
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// ---------------------------------------------------------------------------
+// host side
+
+constexpr int64_t kMaxRowBytes = int64_t(1) << 22;  // 4 MiB, as for the other operands
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int finish(hipError_t e, hipStream_t s) {
+    // PDGEMM_SYNC_CHECK=1 at the first call: every call waits for its kernel
+    static const bool check = [] {
+        const char *v = getenv("PDGEMM_SYNC_CHECK");
+        return v && strcmp(v, "1") == 0;
+    }();
+    if (e == hipSuccess && check) e = hipStreamSynchronize(s);
+    return (int)e;
+}
+
+int run(const void *fn, int64_t blocks, int threads, void *args, void *stream) {
+    // a launch counts its work-items in 32 bits
+    if (blocks * threads > (int64_t)UINT32_MAX) return PDGEMM_EINVAL_DIM;
+    void *kargs[] = {args};
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return finish(hipLaunchKernel(fn, dim3((unsigned)blocks), dim3((unsigned)threads), kargs, 0, s), s);
+}
+
+bool known_type(int t) { return t == kF32 || t == kF16 || t == kBF16; }
+
+// The checks of one MXFP4 operand of `rows` x K, in two steps, so that a call's size
+// errors come before its pointer errors whichever operand has them.
+int check_mx_sizes(int64_t rows, int64_t K, int64_t ldq, int64_t lds) {
+    if (rows < 0 || K < 0 || rows > INT32_MAX || K > (int64_t(1) << 30)) return PDGEMM_EINVAL_DIM;
+    if (ldq < K || lds < rows) return PDGEMM_EINVAL_LD;
+    return PDGEMM_OK;
+}
+int check_mx_memory(const void *q, int64_t ldq, const void *s, int64_t lds) {
+    if (!q || !s) return PDGEMM_ENULL;
+    if (ldq > 2 * kMaxRowBytes || lds > kMaxRowBytes) return PDGEMM_EINVAL_LD;
+    if (ldq % 32 || lds % 16 || ((uintptr_t)q & 15) || ((uintptr_t)s & 15)) return PDGEMM_EALIGN;
+    return PDGEMM_OK;
+}
+
+// rows of a dense matrix with only its element's alignment
+int check_plain(const void *p, int64_t ld, int type) {
+    if (!p) return PDGEMM_ENULL;
+    if (ld > kMaxRowBytes / elem_size(type)) return PDGEMM_EINVAL_LD;
+    if ((uintptr_t)p & (elem_size(type) - 1)) return PDGEMM_EALIGN;
+    return PDGEMM_OK;
+}
+
+template <int T>
+int launch_quant(const QuantArgs &base, void *stream) {
+    QuantArgs args = base;
+    if (args.qt) {
+        args.tiles_k = (int)cdiv(args.K, 128);
+        const void *fn = args.q ? reinterpret_cast<const void *>(&mx_quant_cols_kernel<T, true>)
+                                : reinterpret_cast<const void *>(&mx_quant_cols_kernel<T, false>);
+        return run(fn, cdiv(args.rows, 256) * args.tiles_k, 512, &args, stream);
+    }
+    args.tiles_k = (int)cdiv(args.K, 64 * 16 / elem_size(T));
+    return run(reinterpret_cast<const void *>(&mx_quant_rows_kernel<T, 4>), cdiv(args.rows, 16) * args.tiles_k, 256,
+               &args, stream);
+}
+
+template <int FM, int OT>
+const void *mx_small_ptr() {
+    return reinterpret_cast<const void *>(&mx_small_kernel<FM, 2, 8, FM == 4 ? 1 : 2, OT>);
+}
+template <int OT>
+const void *mx_small_ptr(int fm) {
+    return fm == 1 ? mx_small_ptr<1, OT>() : fm == 2 ? mx_small_ptr<2, OT>() : mx_small_ptr<4, OT>();
+}
+const void *mx_small_ptr(int fm, int ot) {
+    return ot == kF32 ? mx_small_ptr<kF32>(fm) : ot == kF16 ? mx_small_ptr<kF16>(fm) : mx_small_ptr<kBF16>(fm);
+}
+
+template <int T, int FM, int OT>
+const void *a16_small_ptr() {
+    return reinterpret_cast<const void *>(&a16_small_kernel<T, FM, 2, 8, OT>);
+}
+template <int T, int OT>
+const void *a16_small_ptr(int fm) {
+    return fm == 1 ? a16_small_ptr<T, 1, OT>() : fm == 2 ? a16_small_ptr<T, 2, OT>() : a16_small_ptr<T, 4, OT>();
+}
+template <int T>
+const void *a16_small_ptr(int fm, int ot) {
+    return ot == kF32 ? a16_small_ptr<T, kF32>(fm) : ot == kF16 ? a16_small_ptr<T, kF16>(fm) : a16_small_ptr<T, kBF16>(fm);
+}
+
+}  // namespace
+
+extern "C" {
+
+int pdgemm_mxf4_quantize(int64_t rows, int64_t K, const void *src, int64_t ld, int src_type, uint8_t *q, int64_t ldq,
+                         uint8_t *scales, int64_t lds, uint8_t *qt, int64_t ldqt, uint8_t *scales_t, int64_t ldst,
+                         int scale_rule, void *stream) {
+    if (!known_type(src_type) || (scale_rule != PDGEMM_SCALE_FLOOR && scale_rule != PDGEMM_SCALE_FIT))
+        return PDGEMM_EINVAL_CFG;
+    const bool along_k = q || scales, along_rows = qt || scales_t;
+    if (rows < 0 || K < 0 || rows > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return PDGEMM_EINVAL_DIM;
+    if (ld < K) return PDGEMM_EINVAL_LD;
+    int rc = along_k ? check_mx_sizes(rows, K, ldq, lds) : PDGEMM_OK;
+    if (rc == PDGEMM_OK && along_rows) rc = check_mx_sizes(K, rows, ldqt, ldst);
+    if (rc != PDGEMM_OK) return rc;
+    if (rows == 0 || K == 0) return PDGEMM_OK;
+    if (!along_k && !along_rows) return PDGEMM_ENULL;
+    rc = check_plain(src, ld, src_type);
+    if (rc == PDGEMM_OK && along_k) rc = check_mx_memory(q, ldq, scales, lds);
+    if (rc == PDGEMM_OK && along_rows) rc = check_mx_memory(qt, ldqt, scales_t, ldst);
+    if (rc != PDGEMM_OK) return rc;
+    const QuantArgs args = {src, q, scales, qt, scales_t, ld, ldq / 2, lds, ldqt / 2, ldst, (int)rows, (int)K, 0,
+                            rule_bias(scale_rule)};
+    return src_type == kF32 ? launch_quant<kF32>(args, stream)
+                            : src_type == kF16 ? launch_quant<kF16>(args, stream) : launch_quant<kBF16>(args, stream);
+}
+
+int pdgemm_mxf4_dequantize(int64_t rows, int64_t K, const uint8_t *q, int64_t ldq, const uint8_t *scales, int64_t lds,
+                           void *dst, int64_t ldd, int dst_type, void *stream) {
+    if (!known_type(dst_type)) return PDGEMM_EINVAL_CFG;
+    int rc = check_mx_sizes(rows, K, ldq, lds);
+    if (rc != PDGEMM_OK) return rc;
+    if (ldd < K) return PDGEMM_EINVAL_LD;
+    if (rows == 0 || K == 0) return PDGEMM_OK;
+    rc = check_mx_memory(q, ldq, scales, lds);
+    if (rc == PDGEMM_OK) rc = check_plain(dst, ldd, dst_type);
+    if (rc != PDGEMM_OK) return rc;
+    DequantArgs args = {q, scales, dst, ldq / 2, lds, ldd, (int)rows, (int)K, (int)cdiv(K, 512)};
+    const void *fn = dst_type == kF32   ? reinterpret_cast<const void *>(&mx_dequant_kernel<kF32, 4>)
+                     : dst_type == kF16 ? reinterpret_cast<const void *>(&mx_dequant_kernel<kF16, 4>)
+                                        : reinterpret_cast<const void *>(&mx_dequant_kernel<kBF16, 4>);
+    return run(fn, cdiv(rows, 16) * args.tiles_k, 256, &args, stream);
+}
+
+int gemm_mxf4(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a, int64_t ldsa,
+              const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type,
+              void *stream) {
+    if (!known_type(out_type)) return PDGEMM_EINVAL_CFG;
+    int rc = check_mx_sizes(M, K, lda, ldsa);
+    if (rc == PDGEMM_OK) rc = check_mx_sizes(N, K, ldb, ldsb);
+    if (rc != PDGEMM_OK) return rc;
+    if (ldc < N) return PDGEMM_EINVAL_LD;
+    if (M == 0 || N == 0) return PDGEMM_OK;
+    rc = check_plain(C, ldc, out_type);
+    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(A, lda, scale_a, ldsa);
+    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(B, ldb, scale_b, ldsb);
+    if (rc != PDGEMM_OK) return rc;
+    const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    // with K = 0 no operand is read: the kernels form addresses from C instead
+    const uint8_t *const c = static_cast<const uint8_t *>(C);
+    MxArgs args = {K ? A : c, K ? scale_a : c, K ? B : c, K ? scale_b : c, C, K ? lda / 2 : 0, K ? ldb / 2 : 0,
+                   K ? ldsa : 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, 16 * fm), (int)cdiv(N, 32)};
+    return run(mx_small_ptr(fm, out_type), (int64_t)args.tiles_m * args.tiles_n, 512, &args, stream);
+}
+
+int gemm_a16_mxf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B, int64_t ldb,
+                  const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type, void *stream) {
+    if ((a_type != kF16 && a_type != kBF16) || !known_type(out_type)) return PDGEMM_EINVAL_CFG;
+    if (M < 0 || M > INT32_MAX) return PDGEMM_EINVAL_DIM;
+    int rc = check_mx_sizes(N, K, ldb, ldsb);
+    if (rc != PDGEMM_OK) return rc;
+    if (lda < K || ldc < N) return PDGEMM_EINVAL_LD;
+    if (M == 0 || N == 0) return PDGEMM_OK;
+    rc = check_plain(C, ldc, out_type);
+    if (rc == PDGEMM_OK && K > 0) rc = check_plain(A, lda, a_type);
+    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(B, ldb, scale_b, ldsb);
+    if (rc == PDGEMM_OK && K > 0 && (lda % 8 || ((uintptr_t)A & 15))) rc = PDGEMM_EALIGN;
+    if (rc != PDGEMM_OK) return rc;
+    const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    const uint8_t *const c = static_cast<const uint8_t *>(C);
+    MxArgs args = {K ? static_cast<const uint8_t *>(A) : c, nullptr, K ? B : c, K ? scale_b : c, C, K ? 2 * lda : 0,
+                   K ? ldb / 2 : 0, 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, 16 * fm), (int)cdiv(N, 32)};
+    const void *fn = a_type == kF16 ? a16_small_ptr<kF16>(fm, out_type) : a16_small_ptr<kBF16>(fm, out_type);
+    return run(fn, (int64_t)args.tiles_m * args.tiles_n, 512, &args, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,537 @@
+"""GPU parity of the MXFP4 entry points against the 64-bit oracle: codes and scales bit for
+bit, values exactly, products within the rounding of binary32 sums.
+
+Every buffer is wider than the operand and holds poison outside it (NaN, 0x77 codes, 0xFF
+scales), every output sits among sentinels, and each case prints its name before it touches
+the GPU.
+
+Tolerance of a product: each matrix instruction adds at least 32 products to a binary32
+sum; its result is taken to be within four half units (2^-22) of the magnitudes it adds, so
+a sum of K products is within ceil(K / 64) * 2^-22 of the sum of magnitudes (steps of 32
+values: ceil(K / 32) half of that each for the a16 product, whose partial sums are scaled
+exactly).  Rounding to a 16-bit type adds half a unit of the result (2^-11, 2^-8), or half
+its smallest subnormal.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import oracle.mxfp4 as mx
+from tests import gpu_util as gu
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+HALF_UNIT = {"f32": 0.0, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+HALF_TINY = {"f32": 2.0 ** -149, "f16": 2.0 ** -25, "bf16": 2.0 ** -134}
+SENTINEL = 0xA5
+
+
+@pytest.fixture(scope="module")
+def pd():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import precision_dense_gemm_amd as pd
+    return pd
+
+
+@pytest.fixture(scope="module")
+def dev(pd):
+    return torch.device("cuda:0")
+
+
+def to_type(x, kind):
+    """float64 host values -> (CPU tensor of the type, the float64 values it holds)."""
+    t = torch.from_numpy(np.ascontiguousarray(x)).to(TYPES[kind])
+    return t, t.double().numpy()
+
+
+def source(t, dev, pad=5, fill=float("nan")):
+    """t on the GPU with rows `pad` elements apart that hold `fill`, and rows after the last."""
+    buf = torch.full((t.shape[0] + 2, t.shape[1] + pad), fill, dtype=t.dtype)
+    buf[:t.shape[0], :t.shape[1]] = t
+    return buf.to(dev)[:t.shape[0], :t.shape[1]]
+
+
+def blank_operand(rows, K, dev):
+    """(codes, scales) views into sentinel-filled buffers, and the buffers."""
+    nb = mx.blocks_of(K)
+    cb = torch.full((rows + 2, 16 * nb + 32), SENTINEL, dtype=torch.uint8, device=dev)
+    sb = torch.full((nb + 2, gu.round_up(rows, 16) + 16), SENTINEL, dtype=torch.uint8, device=dev)
+    return (cb[:rows, :(K + 1) // 2], sb[:nb, :rows]), (cb, sb)
+
+
+def check_operand(buffers, rows, K, want, what):
+    """The written operand equals the oracle's, and nothing else was written."""
+    cb, sb = (b.cpu().numpy() for b in buffers)
+    codes, scales = want
+    wc, ws = np.full_like(cb, SENTINEL), np.full_like(sb, SENTINEL)
+    wc[:rows, :codes.shape[1]], ws[:scales.shape[0], :rows] = codes, scales
+    assert np.array_equal(sb, ws), f"{what}: scales differ at {np.argwhere(sb != ws)[:5].tolist()}"
+    assert np.array_equal(cb, wc), f"{what}: codes differ at {np.argwhere(cb != wc)[:5].tolist()}"
+
+
+def stored(codes, scales, K, dev):
+    """An oracle operand on the GPU among poison: codes of 0x77 after the last value's byte
+    and in the high nibble of an odd K, scales of 0xFF after the last row and block."""
+    rows, nb = codes.shape[0], scales.shape[0]
+    cb = np.full((rows + 1, gu.round_up(16 * nb, 16) + 32), 0x77, np.uint8)
+    cb[:rows, :(K + 1) // 2] = codes[:, :(K + 1) // 2]
+    if K % 2:
+        cb[:rows, K // 2] = (cb[:rows, K // 2] & 0x0F) | 0x70
+    sb = np.full((nb + 1, gu.round_up(rows, 16) + 16), 0xFF, np.uint8)
+    sb[:nb, :rows] = scales
+    c, s = torch.from_numpy(cb).to(dev), torch.from_numpy(sb).to(dev)
+    return c[:rows, :(K + 1) // 2], s[:nb, :rows]
+
+
+def random_operand(rows, K, seed, lo=120, hi=134):
+    """Random codes and scales (bytes lo .. hi), as the oracle's arrays."""
+    rng = np.random.default_rng(seed)
+    nb = mx.blocks_of(K)
+    return (rng.integers(0, 256, (rows, 16 * nb), dtype=np.uint8),
+            rng.integers(lo, hi + 1, (nb, rows), dtype=np.uint8))
+
+
+def spread(rows, K, seed):
+    """Values of many magnitudes: normal, times a power of two of the row and of the column."""
+    rng = np.random.default_rng(seed)
+    return (rng.standard_normal((rows, K)) * np.exp2(rng.integers(-6, 7, (rows, 1)))
+            * np.exp2(rng.integers(-4, 5, (1, K))))
+
+
+def assert_close(C, R, S, steps, kind, what):
+    """C (a GPU tensor of the kind) against the 64-bit product R and the sum of magnitudes S."""
+    got = C.cpu().double().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(R)), f"{what}: NaN where there is none, or none where one is"
+    top = float(torch.finfo(TYPES[kind]).max)
+    tol = steps * 2.0 ** -22 * S
+    tol = tol + (np.abs(R) + tol) * HALF_UNIT[kind] + HALF_TINY[kind]
+    with np.errstate(invalid="ignore"):
+        clear = np.abs(R) + tol < top                # far enough from the type's overflow
+        over = np.abs(R) - tol > top * (1 + 2 * HALF_UNIT[kind] + 2.0 ** -23)
+        bad = clear & ~(np.abs(got - R) <= tol)
+        bad |= over & (got != np.sign(R) * np.inf)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} off, first {tuple(np.argwhere(bad)[0])}: got "
+                           f"{got[tuple(np.argwhere(bad)[0])]} want {R[tuple(np.argwhere(bad)[0])]}")
+
+
+# ---- quantising ----
+
+QSHAPES = [(1, 1), (1, 31), (1, 33), (3, 4096), (17, 515), (64, 256), (65, 130), (257, 127), (300, 1029), (513, 64)]
+
+
+@pytest.mark.parametrize("form", ["rows", "transpose", "both"])
+@pytest.mark.parametrize("rule", ["floor", "fit"])
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("shape", QSHAPES, ids=[f"{r}x{k}" for r, k in QSHAPES])
+def test_quantize(pd, dev, shape, kind, rule, form):
+    rows, K = shape
+    gu.note(f"[case] quantize {rows}x{K} {kind} {rule} {form}")
+    t, x = to_type(spread(rows, K, 100 + rows + K), kind)
+    x_dev = source(t, dev)
+    out, bufs = blank_operand(rows, K, dev)
+    out_t, bufs_t = blank_operand(K, rows, dev)
+    if form == "rows":
+        pd.mxf4_quantize(x_dev, scale_rule=rule, out=out)
+    elif form == "transpose":
+        pd.mxf4_quantize(x_dev, transpose=True, scale_rule=rule, out=out_t)
+    else:
+        pd.mxf4_quantize_both(x_dev, scale_rule=rule, out=(out, out_t))
+    torch.cuda.synchronize()
+    if form != "transpose":
+        check_operand(bufs, rows, K, mx.quantize(x, rule), "rows")
+    if form != "rows":
+        check_operand(bufs_t, K, rows, mx.quantize(x.T, rule), "transpose")
+
+
+def special_rows(kind):
+    """Rows of one block: its first value sets the scale, the other 31 run over every value of
+    the 16-bit types that is not larger (fp32: ties and their neighbours at many scales)."""
+    rng = np.random.default_rng(3)
+    if kind == "f32":
+        tops = [np.ldexp(m, e) for e in (-149, -140, -127, -126, -125, -124, -20, 0, 1, 60, 125, 127)
+                for m in (1.0, 1.25, 1.5, 1.5 + 2.0 ** -23, 1.75, 2 - 2.0 ** -23)]
+        tops = np.array(tops, np.float32)
+        rows = []
+        for top in tops[(tops > 0) & np.isfinite(tops)]:
+            f = np.array([0, .25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6], np.float64) / 8
+            e = np.floor(np.log2(float(top)))
+            v = np.ldexp(f * 2, int(e)).astype(np.float32)
+            v = np.concatenate([v, np.nextafter(v, np.float32(np.inf)), np.nextafter(v, np.float32(0))])
+            v = np.minimum(v, top)[:31]
+            rows.append(np.concatenate([[top], v, np.zeros(31 - len(v), np.float32)]) * rng.choice([-1, 1], 32))
+        return torch.from_numpy(np.array(rows, np.float32))
+    bits = np.arange(0, 0x7C00 if kind == "f16" else 0x7F80, dtype=np.uint16)
+    every = torch.from_numpy(bits.view(np.int16)).view(TYPES[kind])
+    vals = every.double().numpy()
+    rows = []
+    for top in vals[len(vals) % 31::977]:
+        if top == 0:
+            continue
+        below = vals[vals <= top][-31 * 40:]
+        below = below[:len(below) // 31 * 31].reshape(-1, 31)
+        rows.append(np.hstack([np.full((len(below), 1), top), below]))
+    rows = np.vstack(rows) if rows else np.zeros((0, 32))
+    rows = rows * np.where(np.random.default_rng(4).random(rows.shape) < 0.5, -1, 1)
+    return torch.from_numpy(rows).to(TYPES[kind])
+
+
+@pytest.mark.parametrize("rule", ["floor", "fit"])
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_quantize_values(pd, dev, kind, rule):
+    t = special_rows(kind)
+    gu.note(f"[case] quantize values {kind} {rule} {tuple(t.shape)}")
+    want = mx.quantize(t.double().numpy(), rule)
+    q, s = pd.mxf4_quantize(t.to(dev), scale_rule=rule)
+    qt, st = pd.mxf4_quantize(t.t().contiguous().to(dev), transpose=True, scale_rule=rule)
+    (b, sb), (bt, sbt) = pd.mxf4_quantize_both(torch.cat([t, t], 1).contiguous().to(dev), scale_rule=rule)
+    torch.cuda.synchronize()
+    for name, codes, scales in (("rows", q, s), ("transpose", qt, st)):
+        assert np.array_equal(scales.cpu().numpy(), want[1]), name
+        assert np.array_equal(codes.cpu().numpy(), want[0]), name
+    assert np.array_equal(b.cpu().numpy(), np.hstack([want[0], want[0]]))
+    assert np.array_equal(sb.cpu().numpy(), np.vstack([want[1], want[1]]))
+    again = mx.quantize(torch.cat([t, t], 1).double().numpy().T, rule)
+    assert np.array_equal(bt.cpu().numpy(), again[0][:, :bt.shape[1]]) and np.array_equal(sbt.cpu().numpy(), again[1])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_quantize_special_blocks(pd, dev, kind):
+    gu.note(f"[case] quantize special blocks {kind}")
+    x = spread(40, 100, 9)
+    x[0, 5], x[1, 40], x[2, 99], x[39, 70] = np.nan, np.inf, -np.inf, np.nan
+    x[3, :], x[4:, 64:96] = 0.0, -0.0
+    t, x = to_type(x, kind)
+    (q, s), (qt, st) = pd.mxf4_quantize_both(t.to(dev))
+    q1, s1 = pd.mxf4_quantize(t.to(dev))
+    torch.cuda.synchronize()
+    want, want_t = mx.quantize(x), mx.quantize(x.T)
+    for got, ref in (((q, s), want), ((q1, s1), want), ((qt, st), want_t)):
+        assert np.array_equal(got[1].cpu().numpy(), ref[1])
+        assert np.array_equal(got[0].cpu().numpy(), ref[0][:, :got[0].shape[1]])
+    v = pd.mxf4_dequantize(q, s, 100).cpu().double().numpy()
+    assert np.array_equal(v, mx.values(*want, 100), equal_nan=True)
+
+
+# ---- reading back ----
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_dequantize_every_code_and_scale(pd, dev, kind):
+    gu.note(f"[case] dequantize every code and scale {kind}")
+    codes = np.tile(np.array([0x10, 0x32, 0x54, 0x76, 0x98, 0xBA, 0xDC, 0xFE] * 2, np.uint8), (256, 1))
+    scales = np.arange(256, dtype=np.uint8)[None, :]
+    out = pd.mxf4_dequantize(torch.from_numpy(codes).to(dev), torch.from_numpy(scales).to(dev), out_dtype=TYPES[kind])
+    want = torch.from_numpy(mx.values(codes, scales, 32))
+    want = want.float().to(TYPES[kind])              # exact in binary32 (or infinite), then rounded once
+    got = out.cpu()
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(torch.where(nan, torch.zeros_like(got), got), torch.where(nan, torch.zeros_like(want), want))
+    assert torch.equal(torch.signbit(got)[~nan], torch.signbit(want)[~nan])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("shape", QSHAPES, ids=[f"{r}x{k}" for r, k in QSHAPES])
+def test_dequantize_shapes(pd, dev, shape, kind):
+    rows, K = shape
+    gu.note(f"[case] dequantize {rows}x{K} {kind}")
+    codes, scales = random_operand(rows, K, rows + K)
+    buf = torch.full((rows + 2, K + 3), 7.0, dtype=TYPES[kind], device=dev)
+    pd.mxf4_dequantize(*stored(codes, scales, K, dev), K, out=buf[:rows, :K])
+    want = torch.full((rows + 2, K + 3), 7.0, dtype=torch.float64)
+    want[:rows, :K] = torch.from_numpy(mx.values(codes, scales, K))
+    assert torch.equal(buf.cpu().double(), want)     # few significant bits: exact in every type
+
+
+# ---- products ----
+
+PSHAPES = [(1, 1, 1), (1, 33, 31), (2, 3, 32), (5, 17, 33), (16, 32, 64), (17, 31, 255), (33, 65, 256), (64, 64, 257),
+           (65, 63, 513), (100, 130, 1000), (127, 257, 640), (129, 128, 384), (255, 300, 1030), (520, 260, 2049),
+           (1, 600, 8192), (31, 100, 8191)]
+
+
+def operands(M, N, K, seed, lo=120, hi=134):
+    a, b = random_operand(M, K, seed, lo, hi), random_operand(N, K, seed + 1, lo, hi)
+    R, S = mx.product(mx.values(*a, K), mx.values(*b, K))
+    return a, b, R, S
+
+
+def guarded(M, N, kind, dev):
+    """An output of odd row stride among sentinels."""
+    buf = torch.full((M + 2, N + 3), 7.0, dtype=TYPES[kind], device=dev)
+    return buf, buf[:M, :N]
+
+
+def check_rest(buf, M, N):
+    rest = buf.clone()
+    rest[:M, :N] = 7.0
+    assert bool((rest == 7.0).all()), "stores outside the M x N block"
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("shape", PSHAPES, ids=[f"{m}x{n}x{k}" for m, n, k in PSHAPES])
+def test_product(pd, dev, shape, kind):
+    M, N, K = shape
+    gu.note(f"[case] gemm_mxf4 {M}x{N}x{K} {kind}")
+    a, b, R, S = operands(M, N, K, 1000 + M + 3 * N + K)
+    buf, out = guarded(M, N, kind, dev)
+    pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K, out=out)
+    torch.cuda.synchronize()
+    check_rest(buf, M, N)
+    assert_close(out, R, S, -(-K // 64), kind, f"{shape} {kind}")
+
+
+@pytest.mark.parametrize("bits", [(127, 127), (100, 150), (64, 190), (1, 253)])
+@pytest.mark.parametrize("shape", [(5, 40, 300), (150, 140, 700)], ids=["5x40x300", "150x140x700"])
+def test_product_wide_scales(pd, dev, shape, bits):
+    M, N, K = shape
+    gu.note(f"[case] gemm_mxf4 scales {bits} {shape}")
+    a, b, R, S = operands(M, N, K, 77, *bits)
+    C = pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K)
+    if bits == (1, 253):
+        # sums that leave binary32's range on the way may end infinite or NaN: those whose
+        # magnitudes stay inside have to be right
+        got = C.cpu().double().numpy()
+        inside = S < 2.0 ** 126
+        tol = -(-K // 64) * 2.0 ** -22 * S + K * 2.0 ** -149
+        assert (np.abs(got - R)[inside] <= tol[inside]).all()
+    else:
+        assert_close(C, R, S, -(-K // 64), "f32", f"{shape} {bits}")
+
+
+@pytest.mark.parametrize("shape", [(3, 50, 100), (200, 150, 600)], ids=["3x50x100", "200x150x600"])
+def test_product_nan_scales(pd, dev, shape):
+    M, N, K = shape
+    gu.note(f"[case] gemm_mxf4 NaN scales {shape}")
+    a, b, _, _ = operands(M, N, K, 5)
+    a[1][0, 1] = a[1][-1, M - 1] = 255          # first and last (short) block
+    a[0][M - 1, :] = 0                          # a NaN scale over zero codes is NaN too
+    b[1][1, 7] = 255
+    R, S = mx.product(mx.values(*a, K), mx.values(*b, K))
+    assert_close(pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K), R, S, -(-K // 64), "f32", "NaN scales")
+
+
+def test_product_overflow_of_16_bit_outputs(pd, dev):
+    gu.note("[case] gemm_mxf4 overflow")
+    M, N, K = 40, 50, 128
+    codes = np.full((M, 64), 0x77, np.uint8)
+    a = (codes, np.full((4, M), 140, np.uint8))
+    b = (np.full((N, 64), 0xF7, np.uint8), np.full((4, N), 130, np.uint8))
+    b[0][:, :] = 0x77
+    R, S = mx.product(mx.values(*a, K), mx.values(*b, K))
+    assert R.min() > 65504
+    for kind in TYPES:
+        assert_close(pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K, out_dtype=TYPES[kind]), R, S, 2, kind, kind)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_product_empty(pd, dev, kind):
+    gu.note(f"[case] gemm_mxf4 empty {kind}")
+    u = lambda r, c: torch.zeros((r, c), dtype=torch.uint8, device=dev)  # noqa: E731
+    for M, N in ((3, 5), (300, 70)):
+        buf, out = guarded(M, N, kind, dev)
+        pd.gemm_mxf4(u(M, 0), u(0, M), u(N, 0), u(0, N), 0, out=out)
+        check_rest(buf, M, N)
+        assert not bool(out.any())
+        pd.gemm_a16_mxf4(torch.zeros((M, 0), dtype=torch.float16, device=dev), u(N, 0), u(0, N), out=out.fill_(3))
+        assert not bool(out.any())
+    assert pd.gemm_mxf4(u(0, 16), u(1, 0), u(5, 16), u(1, 5), 32).shape == (0, 5)
+    assert pd.mxf4_quantize(torch.zeros((0, 40), device=dev))[0].shape == (0, 20)
+    assert pd.mxf4_dequantize(u(4, 0), u(0, 4)).shape == (4, 0)
+
+
+@pytest.mark.parametrize("a_kind", ["f16", "bf16"])
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("shape", PSHAPES, ids=[f"{m}x{n}x{k}" for m, n, k in PSHAPES])
+def test_a16(pd, dev, shape, kind, a_kind):
+    M, N, K = shape
+    gu.note(f"[case] gemm_a16_mxf4 {M}x{N}x{K} {a_kind} {kind}")
+    t, x = to_type(spread(M, K, 2000 + M + K), a_kind)
+    b = random_operand(N, K, 3000 + N + K)
+    R, S = mx.product(x, mx.values(*b, K))
+    buf, out = guarded(M, N, kind, dev)
+    pd.gemm_a16_mxf4(source(t, dev, gu.round_up(K, 8) - K + 8), *stored(*b, K, dev), out=out)
+    torch.cuda.synchronize()
+    check_rest(buf, M, N)
+    assert_close(out, R, S, -(-K // 64) + 1, kind, f"{shape} {a_kind} {kind}")
+
+
+@pytest.mark.parametrize("a_kind", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [5, 150])
+def test_a16_wide_and_nan_scales(pd, dev, M, a_kind):
+    N, K = 70, 500
+    gu.note(f"[case] gemm_a16_mxf4 wide scales M={M} {a_kind}")
+    t, x = to_type(spread(M, K, 8), a_kind)
+    for lo, hi in ((60, 190), (0, 20), (200, 240)):
+        b = random_operand(N, K, lo, lo, hi)
+        R, S = mx.product(x, mx.values(*b, K))
+        C = pd.gemm_a16_mxf4(source(t, dev, 12), *stored(*b, K, dev))
+        got = C.cpu().double().numpy()
+        tol = (-(-K // 64) + 1) * 2.0 ** -22 * S + K * 2.0 ** -149
+        # every partial sum of an element is at most S (1 + 2^-19) in magnitude: below 2^128,
+        # binary32's overflow, where S < 2^127; the largest S here is 1.78 * 2^128
+        inside = S < 2.0 ** 127
+        assert inside.mean() > 0.9 and (np.abs(got - R)[inside] <= tol[inside]).all(), (lo, hi)
+    b = random_operand(N, K, 1)
+    b[1][0, 3] = b[1][-1, 69] = 255
+    x[1, 2], x[2, 499] = np.nan, np.inf
+    t = torch.from_numpy(x).to(TYPES[a_kind])
+    got = pd.gemm_a16_mxf4(source(t, dev, 12), *stored(*b, K, dev)).cpu().double().numpy()
+    nan_b = np.zeros(N, bool)
+    nan_b[[3, 69]] = True
+    assert np.isnan(got[1]).all() and np.isnan(got[:, nan_b]).all()
+    assert not np.isfinite(got[2]).any()             # infinity times zero, or an infinity
+    rest = np.delete(np.delete(got, [1, 2], 0), np.flatnonzero(nan_b), 1)
+    assert np.isfinite(rest).all()
+
+
+def test_products_are_reproducible(pd, dev):
+    gu.note("[case] repeated products")
+    for M, N, K in ((7, 200, 4000), (300, 500, 1000)):
+        a, b, _, _ = operands(M, N, K, 31)
+        A, B = stored(*a, K, dev), stored(*b, K, dev)
+        x = source(to_type(spread(M, K, 3), "bf16")[0], dev, gu.round_up(K, 8) - K)
+        first = pd.gemm_mxf4(*A, *B, K), pd.gemm_a16_mxf4(x, *B)
+        for _ in range(3):
+            assert torch.equal(pd.gemm_mxf4(*A, *B, K), first[0])
+            assert torch.equal(pd.gemm_a16_mxf4(x, *B), first[1])
+
+
+# ---- used together ----
+
+def layer_step(pd, x, w, g, out_dtype):
+    """Forward product and both gradients of Y = X W^T with every product in MXFP4."""
+    (xq, xs), (xt, xst) = pd.mxf4_quantize_both(x)
+    (wq, ws), (wt, wst) = pd.mxf4_quantize_both(w)
+    (gq, gs), (gt, gst) = pd.mxf4_quantize_both(g)
+    M, K, N = x.shape[0], x.shape[1], w.shape[0]
+    return (pd.gemm_mxf4(xq, xs, wq, ws, K, out_dtype=out_dtype), pd.gemm_mxf4(gq, gs, wt, wst, N, out_dtype=out_dtype),
+            pd.gemm_mxf4(gt, gst, xt, xst, M))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 64, 96), (77, 130, 200), (300, 257, 515)], ids=["1x64x96", "77x130x200", "300x257x515"])
+def test_layer_step(pd, dev, shape, kind):
+    M, N, K = shape
+    gu.note(f"[case] layer step {shape} {kind}")
+    (xt, x), (wt, w), (gt, g) = (to_type(spread(*s, 40 + n), kind) for n, s in enumerate(((M, K), (N, K), (M, N))))
+    y, dx, dw = layer_step(pd, source(xt, dev), source(wt, dev), source(gt, dev), TYPES[kind])
+    val = lambda t: mx.values(*mx.quantize(t), t.shape[1])  # noqa: E731
+    for name, got, a, b, k, out in (("y", y, x, w, K, kind), ("dx", dx, g, w.T, N, kind), ("dw", dw, g.T, x.T, M, "f32")):
+        R, S = mx.product(val(a), val(b))
+        assert_close(got, R, S, -(-k // 64), out, f"{name} {shape}")
+
+
+def test_gradients_by_differences(pd, dev):
+    """With operands that MXFP4 holds exactly along both axes (one magnitude per tensor, so
+    every block's scale is the same), dX and dW are the differences of the loss sum(G * Y)
+    itself: it is linear in each element of X and W, and its every term is a dyadic number
+    that binary32 holds exactly."""
+    gu.note("[case] gradients by differences")
+    M, N, K = 33, 40, 65
+    rng = np.random.default_rng(17)
+    grid = np.array([-6, -4, -3, -2, -1.5, -1, -.5, 0, .5, 1, 1.5, 2, 3, 4, 6])
+
+    def exact(rows, cols):
+        v = rng.choice(grid, (rows, cols))
+        # every 32-block along either axis holds a 4 or 6, so that its scale is 1
+        for i in range(rows):
+            for b in range(0, cols, 32):
+                v[i, b + (i % min(32, cols - b))] = 4.0
+        for j in range(cols):
+            for b in range(0, rows, 32):
+                v[b + (j % min(32, rows - b)), j] = 6.0
+        return v
+
+    x, w, g = exact(M, K), exact(N, K), exact(M, N)
+    for t in (x, w, g):
+        for u in (t, t.T):
+            assert np.array_equal(mx.values(*mx.quantize(u), u.shape[1]), u)
+    put = lambda v: torch.from_numpy(v).half().to(dev)  # noqa: E731
+    y, dx, dw = (t.cpu().double().numpy() for t in layer_step(pd, put(x), put(w), put(g), torch.float32))
+    assert np.array_equal(y, x @ w.T) and np.array_equal(dx, g @ w) and np.array_equal(dw, g.T @ x)
+
+    def loss(xv, wv):
+        q = pd.mxf4_quantize(put(xv)), pd.mxf4_quantize(put(wv))
+        return float((pd.gemm_mxf4(*q[0], *q[1], K).cpu().double().numpy() * g).sum())
+
+    base = loss(x, w)
+    for i, k in ((0, 0), (32, 64), (17, 31), (5, 40)):
+        for t, grad, which in ((x, dx, 0), (w, dw, 1)):
+            v = t.copy()
+            old = v[i, k]
+            v[i, k] = 2.0 if old != 2.0 else 3.0
+            if not np.array_equal(mx.values(*mx.quantize(v), K), v):
+                continue                             # the only 4 or 6 of its block: the scale would move
+            moved = loss(v, w) if which == 0 else loss(x, v)
+            assert moved - base == grad[i, k] * (v[i, k] - old)
+
+
+def test_captured_step_replays(pd, dev):
+    """Quantising and the products recorded into a graph, beside an eager run of the same
+    call; each replay follows eager work that overwrites the outputs."""
+    gu.note("[case] graph of a layer step")
+    M, N, K = 130, 200, 330
+    x, w, g = (source(to_type(spread(*s, 60 + n), "bf16")[0], dev) for n, s in enumerate(((M, K), (N, K), (M, N))))
+    ops = [pd.mxf4_quantize_both(t) for t in (x, w, g)]
+    outs = [torch.empty((M, N), device=dev), torch.empty((M, K), device=dev), torch.empty((N, K), device=dev),
+            torch.empty((M, K), device=dev)]
+    a16_out = torch.empty((M, N), device=dev)
+    x16 = source(to_type(spread(M, K, 60), "bf16")[0], dev, gu.round_up(K, 8) - K)
+
+    def call():
+        for t, o in zip((x, w, g), ops):
+            pd.mxf4_quantize_both(t, out=o)
+        (xq, xt), (wq, wt), (gq, gt) = ops
+        pd.gemm_mxf4(*xq, *wq, K, out=outs[0])
+        pd.gemm_mxf4(*gq, *wt, N, out=outs[1])
+        pd.gemm_mxf4(*gt, *xt, M, out=outs[2])
+        pd.mxf4_dequantize(*xq, K, out=outs[3])
+        pd.gemm_a16_mxf4(x16, *wq, out=a16_out)
+
+    call()
+    torch.cuda.synchronize()
+    eager = [t.clone() for t in outs + [a16_out]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for replay in range(3):
+        for t in outs + [a16_out]:
+            t.fill_(float("nan"))
+        for pair in ops:
+            for codes, scales in pair:
+                codes.fill_(0x55)
+                scales.fill_(0x7F)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, (t, e) in enumerate(zip(outs + [a16_out], eager)):
+            assert torch.equal(t, e), f"replay {replay}, output {n}"
+    del graph
+
+
+def test_another_stream(pd, dev):
+    gu.note("[case] another stream")
+    M, N, K = 200, 300, 520
+    t, x = to_type(spread(M, K, 71), "f16")
+    b = random_operand(N, K, 72)
+    R, S = mx.product(mx.values(*mx.quantize(x), K), mx.values(*b, K))
+    B = stored(*b, K, dev)
+    xd = t.to(dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    q, s = pd.mxf4_quantize(xd, stream=side)
+    C = pd.gemm_mxf4(q, s, *B, K, stream=side)
+    v = pd.mxf4_dequantize(q, s, K, stream=side)
+    side.synchronize()
+    assert_close(C, R, S, -(-K // 64), "f32", "side stream")
+    assert np.array_equal(v.cpu().double().numpy(), mx.values(*mx.quantize(x), K))

@@ -422,6 +422,15 @@ int gemm_mxf4(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, co
               const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc,
               int out_type, void *stream);
 
+/* The same with an explicit tile configuration (0 <= cfg <
+ * pdgemm_mxf4_num_configs(), any shape; else PDGEMM_EINVAL_CFG), and the one
+ * gemm_mxf4 takes for a shape.  The sums' order depends on the configuration. */
+int pdgemm_mxf4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a,
+                    int64_t ldsa, const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C,
+                    int64_t ldc, int out_type, void *stream);
+int pdgemm_mxf4_num_configs(void);
+int pdgemm_mxf4_pick(int64_t M, int64_t N, int64_t K);
+
 /* C = A * B of 16-bit A (a_type PDGEMM_F16 or PDGEMM_BF16, row-major, rows of a
  * multiple of 16 bytes, 16-byte aligned) and MXFP4 B: weights kept in 4 bits
  * under activations that are not quantised.  B's values enter exactly; sums and

@@ -117,6 +117,12 @@ lib.pdgemm_mxf4_dequantize.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _p, _i64,
 lib.pdgemm_mxf4_dequantize.restype = _i
 lib.gemm_mxf4.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p]
 lib.gemm_mxf4.restype = _i
+lib.pdgemm_mxf4_cfg.argtypes = [_i] + lib.gemm_mxf4.argtypes
+lib.pdgemm_mxf4_cfg.restype = _i
+lib.pdgemm_mxf4_num_configs.argtypes = []
+lib.pdgemm_mxf4_num_configs.restype = _i
+lib.pdgemm_mxf4_pick.argtypes = [_i64, _i64, _i64]
+lib.pdgemm_mxf4_pick.restype = _i
 lib.gemm_a16_mxf4.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _p, _i64, _i, _p]
 lib.gemm_a16_mxf4.restype = _i
 lib.pdgemm_strerror.argtypes = [_i]
@@ -691,18 +697,28 @@ def _mx_product_out(out, M, N, out_dtype, device, stream):
 
 
 def gemm_mxf4(A: torch.Tensor, scale_a: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, K: int | None = None,
-              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32, stream=None,
+              cfg: int | None = None) -> torch.Tensor:
     """C = A * B of MXFP4 A (M rows) and Bt (N rows); binary32 sums, C (M, N) float32, float16
-    or bfloat16 (out's dtype, else out_dtype)."""
+    or bfloat16 (out's dtype, else out_dtype).  cfg: an explicit tile configuration."""
     K = 2 * min(A.shape[1], Bt.shape[1]) if K is None else K
     M, K, lda, ldsa = _mx_operand(A, scale_a, K, "A")
     N, K, ldb, ldsb = _mx_operand(Bt, scale_b, K, "Bt")
     out, ldc = _mx_product_out(out, M, N, out_dtype, A.device, stream)
-    if M and N:
-        _mx_call(lib.gemm_mxf4, (M, N, K, A.data_ptr(), lda, scale_a.data_ptr(), ldsa, Bt.data_ptr(), ldb,
-                                 scale_b.data_ptr(), ldsb, out.data_ptr(), ldc, _mx_type(out.dtype, "out")),
-                 [A, scale_a, Bt, scale_b, out], stream)
+    args = (M, N, K, A.data_ptr(), lda, scale_a.data_ptr(), ldsa, Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb,
+            out.data_ptr(), ldc, _mx_type(out.dtype, "out"))
+    fn, args = (lib.gemm_mxf4, args) if cfg is None else (lib.pdgemm_mxf4_cfg, (cfg,) + args)
+    _mx_call(fn, args, [A, scale_a, Bt, scale_b, out], stream)
     return out
+
+
+def mxf4_num_configs() -> int:
+    return lib.pdgemm_mxf4_num_configs()
+
+
+def mxf4_pick(M: int, N: int, K: int) -> int:
+    """The tile configuration gemm_mxf4 takes for a shape."""
+    return lib.pdgemm_mxf4_pick(M, N, K)
 
 
 def gemm_a16_mxf4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, out: torch.Tensor | None = None,

@@ -591,6 +591,323 @@ __global__ __launch_bounds__(W *kWave) void mx_small_kernel(MxArgs args) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+// Block id -> tile, the order of the other GEMM kernels: workgroups are dispatched
+// round-robin over the 8 XCDs, so each XCD takes a contiguous range of tiles, in bands
+// of GM block rows, whose operands its L2 then shares; a grid of whole 16 x 16 windows
+// of tiles goes window by window (one round of the 256 CUs each, serpentine), 4 x 8
+// tiles to an XCD.
+template <int GM, bool kWindows>
+__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int &tile_m, int &tile_n) {
+    const int nb = gridDim.x, bid = blockIdx.x;
+    const int xcd = bid & 7, loc = bid >> 3;
+    if (kWindows && ((tiles_m | tiles_n) & 15) == 0) {
+        const int w = loc >> 5, k = loc & 31;   // window; this XCD's k-th tile in it
+        const int wcols = tiles_n >> 4;
+        const int wm = w / wcols, wi = w - wm * wcols;
+        const int wn = (wm & 1) ? wcols - 1 - wi : wi;
+        tile_m = wm * 16 + (xcd & 3) * 4 + (k & 3);
+        tile_n = wn * 16 + (xcd >> 2) * 8 + (k >> 2);
+        return;
+    }
+    const int q = nb >> 3, r = nb & 7;
+    const int id = (xcd < r) ? xcd * (q + 1) + loc : r * (q + 1) + (xcd - r) * q + loc;
+    const int band = id / (GM * tiles_n);
+    const int first_m = band * GM;
+    const int rows = min(tiles_m - first_m, GM);
+    const int in_band = id - band * GM * tiles_n;
+    tile_m = first_m + in_band % rows;
+    tile_n = in_band / rows;
+}
+
+typedef float floatx16_t __attribute__((ext_vector_type(16)));
+typedef int intx4_t __attribute__((ext_vector_type(4)));
+
+template <int kOpA, int kOpB>
+__device__ __forceinline__ floatx16_t mfma32_fp4(const uint4 &a, const uint4 &b, const floatx16_t &c, uint32_t sa, uint32_t sb) {
+    const intx4_t a4 = {(int)a.x, (int)a.y, (int)a.z, (int)a.w}, b4 = {(int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    // format 4 reads four of an operand's eight registers
+    const intx8_t a8 = __builtin_shufflevector(a4, a4, 0, 1, 2, 3, -1, -1, -1, -1);
+    const intx8_t b8 = __builtin_shufflevector(b4, b4, 0, 1, 2, 3, -1, -1, -1, -1);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, kOpA, (int)sa, kOpB, (int)sb);
+}
+
+#define LDS_PTR(p) ((__attribute__((address_space(3))) void *)(p))
+
+// LDS position of 16-byte chunk c of the 128-byte stage row r is c ^ swizzle8(r): the
+// 16 lanes of a phase of a fragment read (16 consecutive rows, one chunk) fall in
+// distinct bank groups.
+__device__ __forceinline__ int swizzle8(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// Many rows: a BM x BN tile of C per workgroup of (BM / WM) x (BN / WN) waves on
+// v_mfma_scale_f32_32x32x64_f8f6f4 (one instruction, 64 values of K: twice the work per
+// instruction of the 16 x 16 form; a loop of nothing but MFMAs on random operands ran at
+// 6.5 PFLOP/s, of the 16 x 16 form at 5.9).
+//
+// A stage is one 128-byte line (256 values) of K of the tile's BM rows of A and BN of B,
+// copied from memory straight into LDS, LS stages deep, and its scales.  Fragment i of a
+// wave holds rows FM r + i (r = 0 .. 31) of the wave's WM rows, which the copy places at
+// LDS rows 32 i + r: so a lane's scales of its FM fragments are neighbouring bytes of a
+// dword, which one MFMA operand register takes whole (the instruction picks the byte), and
+// a lane's results of FN fragments are neighbouring columns of C, stored together.  A
+// stage's scales are copied by the first waves, 16 rows of a block per lane.
+template <int BM, int BN, int WM, int WN, int LS, int OT>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kernel(MxArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using Out = typename ElemOf<OT>::type;
+    constexpr int NW = (BM / WM) * (BN / WN);
+    constexpr int kWavesN = BN / WN;
+    constexpr int FM = WM / 32, FN = WN / 32;
+    constexpr int kRows = BM + BN;
+    constexpr int kDma = kRows / 8 / NW;           // copies of 1 KB (8 rows) per wave per stage
+    constexpr int kDmaA = BM / 8 / NW;
+    constexpr int kSc = kRows / 128;               // waves that copy 1 KB of scales too
+    constexpr int kAll = kDma + 1;
+    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "a stage's rows split evenly over the waves");
+    static_assert(BM % 128 == 0 && BN % 128 == 0 && kSc <= NW, "a wave copies scales of one operand");
+    static_assert((FM == 1 || FM == 2 || FM == 4) && (FN == 1 || FN == 2 || FN == 4), "scales of a lane in one dword");
+    static_assert((LS - 1) * kAll <= 63, "vmcnt holds at most 63 outstanding loads");
+    struct Stage {
+        uint4 rows[kRows][8];
+        uint4 sc[kRows / 2 + 64];   // bytes: [A: 8 blocks of BM rows | B: 8 blocks of BN rows | unused]
+    };
+    __shared__ Stage l0, l1;
+    __shared__ typename std::conditional<(LS > 2), Stage, char>::type l2;
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int M = args.M, N = args.N, K = args.K;
+    int tile_m, tile_n;
+    tile_of<4, true>(args.tiles_m, args.tiles_n, tile_m, tile_n);
+    const int m0 = tile_m * BM, n0 = tile_n * BN;
+    const int blocks = (K + kBlock - 1) / kBlock;
+    const int n_st = (blocks + 7) / 8;
+
+    const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
+    const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
+    const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + blocks * 16;
+    const int b_end = (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16;
+    // a block's scales are read up to the 16-byte granule that holds the last row's
+    const int sa_cols = min(((M + 15) & ~15) - m0, BM), sb_cols = min(((N + 15) & ~15) - n0, BN);
+
+    // copy j of this wave fills LDS rows (j NW + wave) 8 .. + 7, lane l chunk position l % 8
+    // of row l / 8; rows of the tile past M (N) repeat the last one, not stored
+    uint32_t voff[kDma];
+#pragma unroll
+    for (int j = 0; j < kDma; ++j) {
+        const int cr = (j * NW + wave) * 8 + (lane >> 3);
+        const int chunk = (lane & 7) ^ swizzle8(cr);
+        if (j < kDmaA) {
+            const int row = cr / WM * WM + FM * (cr % 32) + cr % WM / 32;
+            voff[j] = (uint32_t)((min(m0 + row, M - 1) - m0) * args.lda) + chunk * 16;
+        } else {
+            const int cb = cr - BM;
+            const int row = cb / WN * WN + FN * (cb % 32) + cb % WN / 32;
+            voff[j] = (uint32_t)((min(n0 + row, N - 1) - n0) * args.ldb) + chunk * 16;
+        }
+    }
+    // scale copy `wave`, 16 rows of one block per lane.  The waves beyond copy nothing (an
+    // empty range: zeros into a kilobyte nobody reads), so that a stage is straight-line code
+    // and every wave counts its copies alike
+    const bool sc_a = wave < BM / 128, sc_none = wave >= kSc;
+    const int sd = (sc_a ? wave : wave - BM / 128) * 64 + lane, sq = (sc_a ? BM : BN) / 16;
+    const int sc_ld = sc_none ? 0 : (int)(sc_a ? args.ldsa : args.ldsb);
+    const int sc_cols = sc_none ? 0 : sc_a ? sa_cols : sb_cols;
+    const uint8_t *const sc_base = sc_a ? args.SA + m0 : args.SB + n0;
+    const uint32_t soff = (uint32_t)(sd / sq * sc_ld) + sd % sq * 16;
+    auto stage = [&](int st, Stage &buf) __attribute__((always_inline)) {
+        const int nb = min(blocks - st * 8, 8);   // at most 0 past K: nothing is read, zeros arrive
+        const bool live = nb > 0;
+        const auto ra = rsrc(a_base + st * 128, live ? a_end - st * 128 : 0);
+        const auto rb = rsrc(b_base + st * 128, live ? b_end - st * 128 : 0);
+#pragma unroll
+        for (int j = 0; j < kDma; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(j < kDmaA ? ra : rb, LDS_PTR(&buf.rows[(j * NW + wave) * 8][0]), 16,
+                                                     voff[j], 0, 0, 0);
+        // (a scale row holds at least the tile's columns, so the range of no blocks is not positive)
+        const auto rs = rsrc(sc_base + (int64_t)st * 8 * sc_ld, max((nb - 1) * sc_ld + sc_cols, 0));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, LDS_PTR(&buf.sc[sc_none ? kSc * 64 : wave * 64]), 16, soff, 0, 0, 0);
+    };
+
+    const int wm0 = (wave / kWavesN) * WM, wn0 = (wave % kWavesN) * WN;
+    const int r = lane & 31, h = lane >> 5;
+    // fragment rows start at multiples of 32, so the swizzle of row r applies
+    auto read_frags = [&](const Stage &buf, int s, uint4 (&fa)[FM], uint4 (&fb)[FN]) __attribute__((always_inline)) {
+        const int ch = (2 * s + h) ^ swizzle8(r);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j] = buf.rows[BM + wn0 + j * 32 + r][ch];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[i] = buf.rows[wm0 + i * 32 + r][ch];
+    };
+    // this lane's dwords of a stage's four k-steps: block 2 s + h, the rows around its own
+    const int ia = h * BM + (wm0 + FM * r), ib = 8 * BM + h * BN + (wn0 + FN * r);
+    auto read_scales = [&](const Stage &buf, uint32_t (&sa)[4], uint32_t (&sb)[4]) __attribute__((always_inline)) {
+        const uint32_t *const sc = reinterpret_cast<const uint32_t *>(&buf.sc[0]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) sa[s] = sc[(ia + 2 * s * BM) / 4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) sb[s] = sc[(ib + 2 * s * BN) / 4];
+    };
+    // a lane's bytes to the bottom of each dword
+    const int sha = 8 * ((FM * r) & 3), shb = 8 * ((FN * r) & 3);
+
+    floatx16_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    auto mma = [&](const uint4 (&fa)[FM], const uint4 (&fb)[FN], uint32_t sa, uint32_t sb) __attribute__((always_inline)) {
+        if constexpr (FM < 4) sa >>= sha;
+        if constexpr (FN < 4) sb >>= shb;
+        static_for<FM>([&](auto i_c) __attribute__((always_inline)) {
+            static_for<FN>([&](auto j_c) __attribute__((always_inline)) {
+                constexpr int i = decltype(i_c)::value, j = decltype(j_c)::value;
+                acc[i][j] = mfma32_fp4<i, j>(fa[i], fb[j], acc[i][j], sa, sb);
+            });
+        });
+    };
+    // issue order of a k-step: its MFMAs, the next one's fragment reads and (after the
+    // stage barrier) the copies of a later stage slotted between them
+    constexpr int kMfma = FM * FN;
+    auto interleave = [&](auto reads_c, auto dma_c) __attribute__((always_inline)) {
+        constexpr int reads = decltype(reads_c)::value, dma = decltype(dma_c)::value;
+        constexpr int rper = (reads + kMfma - 1) / kMfma, dper = (dma + kMfma - 1) / kMfma;
+#pragma unroll
+        for (int i = 0; i < kMfma; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                    // MFMA
+            if (i * rper < reads) __builtin_amdgcn_sched_group_barrier(0x100, rper, 0);           // LDS reads
+            if (i * dper < dma) __builtin_amdgcn_sched_group_barrier(0x020, dper, 0);             // copies
+        }
+    };
+    using kNone = std::integral_constant<int, 0>;
+    using kFrags = std::integral_constant<int, FM + FN>;
+    using kFragsScales = std::integral_constant<int, FM + FN + 8>;
+    using kCopies = std::integral_constant<int, kAll>;
+
+    // fragments of the even (0) and odd (1) k-steps; the scales of the current and next stage
+    uint4 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
+    uint32_t sa[4], sb[4], sa_next[4], sb_next[4];
+    // stage st (not the last) from `cur`, whose k-step 0 is in fa0 / fb0 and scales in sa / sb;
+    // refills `cur` with stage st + LS and reads the same of stage st + 1 from `nxt`
+    auto full_stage = [&](Stage &cur, const Stage &nxt, int st) __attribute__((always_inline)) {
+        read_frags(cur, 1, fa1, fb1);
+        mma(fa0, fb0, sa[0], sb[0]);
+        interleave(kFrags{}, kNone{});
+        read_frags(cur, 2, fa0, fb0);
+        mma(fa1, fb1, sa[1], sb[1]);
+        interleave(kFrags{}, kNone{});
+        read_frags(cur, 3, fa1, fb1);
+        mma(fa0, fb0, sa[2], sb[2]);
+        interleave(kFrags{}, kNone{});
+        // this wave's copies of stage st + 1 have landed (later ones may be in flight) and its
+        // reads of `cur` are done; after the barrier the same holds for every wave
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((LS - 2) * kAll) : "memory");
+        stage(st + LS, cur);
+        read_scales(nxt, sa_next, sb_next);
+        read_frags(nxt, 0, fa0, fb0);
+        mma(fa1, fb1, sa[3], sb[3]);
+        interleave(kFragsScales{}, kCopies{});
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            sa[s] = sa_next[s];
+            sb[s] = sb_next[s];
+        }
+    };
+    // A's values at and beyond K become zeros: what is beside them in B is finite (e2m1
+    // holds nothing else), and scales past the last block are zero
+    auto mask = [&](int st, int s, uint4 (&f)[FM]) __attribute__((always_inline)) {
+        const int n = K - (st * 256 + s * 64 + h * kBlock);
+        uint32_t m[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int left = n - 8 * d;
+            m[d] = left >= 8 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (4 * left)) - 1u;
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            f[i].x &= m[0];
+            f[i].y &= m[1];
+            f[i].z &= m[2];
+            f[i].w &= m[3];
+        }
+    };
+    auto last_stage = [&](const Stage &cur, int st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s > 0) read_frags(cur, s, fa0, fb0);
+            mask(st, s, fa0);
+            mma(fa0, fb0, sa[s], sb[s]);
+        }
+    };
+    if (n_st > 0) {
+        stage(0, l0);
+        stage(1, l1);
+        if constexpr (LS > 2) stage(2, l2);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((LS - 1) * kAll) : "memory");
+        read_frags(l0, 0, fa0, fb0);
+        read_scales(l0, sa, sb);
+        int st = 0;
+        if constexpr (LS == 2) {
+            for (; st + 2 < n_st; st += 2) {
+                full_stage(l0, l1, st);
+                full_stage(l1, l0, st + 1);
+            }
+            if (st + 1 < n_st) full_stage(l0, l1, st++);
+            last_stage((st & 1) ? l1 : l0, st);
+        } else {
+            for (; st + 3 < n_st; st += 3) {
+                full_stage(l0, l1, st);
+                full_stage(l1, l2, st + 1);
+                full_stage(l2, l0, st + 2);
+            }
+            if (st + 1 < n_st) {
+                full_stage(l0, l1, st++);
+                if (st + 1 < n_st) full_stage(l1, l2, st++);
+            }
+            const int q = st % 3;
+            last_stage(q == 0 ? l0 : q == 1 ? l1 : l2, st);
+        }
+        // no copy may still be writing this workgroup's LDS when it exits
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+
+    // C, non-temporal.  Register e of lane l in block (i, j): row FM (8 (e / 4) + 4 h + e % 4)
+    // + i, column FN (l % 32) + j of the wave's tile, so a store of a lane's FN columns by 32
+    // lanes is a run of WN columns of one row.
+    typedef Out vec_t __attribute__((ext_vector_type(FN)));
+    typedef vec_t packed_t __attribute__((aligned(sizeof(Out))));
+    const int row0 = m0 + wm0 + FM * 4 * h, col0 = n0 + wn0 + FN * r;
+    Out *const c_lane = static_cast<Out *>(args.C) + (int64_t)row0 * args.ldc + col0;
+    const int rows_left = M - row0, cols_left = N - col0;
+    auto store_all = [&](auto interior_c) __attribute__((always_inline)) {
+        constexpr bool kInterior = decltype(interior_c)::value;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int row = FM * (8 * (e >> 2) + (e & 3)) + i;   // wave-uniform part of the row
+                Out *const p = c_lane + row * args.ldc;
+                vec_t v;
+#pragma unroll
+                for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
+                if (kInterior || (row < rows_left && FN <= cols_left)) {
+                    __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
+                } else if (row < rows_left) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        if (j < cols_left) p[j] = v[j];
+                }
+            }
+    };
+    if (m0 + BM <= M && n0 + BN <= N)
+        store_all(std::true_type{});
+    else
+        store_all(std::false_type{});
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
 // 16-bit activations times MXFP4 weights.  The codes become the 16-bit type exactly
 // (e2m1 values need two significant bits); an MFMA of 32 values of K covers one block,
 // and its result is scaled by the block's 2^(byte - 127) as it is added to the sum, in
@@ -803,12 +1120,23 @@ template <int FM, int OT>
 const void *mx_small_ptr() {
     return reinterpret_cast<const void *>(&mx_small_kernel<FM, 2, 8, FM == 4 ? 1 : 2, OT>);
 }
+
+struct MxConfig {
+    int bm, bn, threads;
+};
+constexpr MxConfig kMxConfigs[] = {{256, 256, 512}, {256, 128, 512}, {128, 128, 256}, {16, 32, 512}, {32, 32, 512}, {64, 32, 512}};
+constexpr int kNumMxConfigs = sizeof(kMxConfigs) / sizeof(kMxConfigs[0]);
+
 template <int OT>
-const void *mx_small_ptr(int fm) {
-    return fm == 1 ? mx_small_ptr<1, OT>() : fm == 2 ? mx_small_ptr<2, OT>() : mx_small_ptr<4, OT>();
-}
-const void *mx_small_ptr(int fm, int ot) {
-    return ot == kF32 ? mx_small_ptr<kF32>(fm) : ot == kF16 ? mx_small_ptr<kF16>(fm) : mx_small_ptr<kBF16>(fm);
+const void *mx_ptr(int cfg) {
+    switch (cfg) {
+    case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 256, 128, 64, 2, OT>);
+    case 1: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 128, 64, 64, 2, OT>);
+    case 2: return reinterpret_cast<const void *>(&mx_tile_kernel<128, 128, 64, 64, 2, OT>);
+    case 3: return mx_small_ptr<1, OT>();
+    case 4: return mx_small_ptr<2, OT>();
+    default: return mx_small_ptr<4, OT>();
+    }
 }
 
 template <int T, int FM, int OT>
@@ -822,6 +1150,33 @@ const void *a16_small_ptr(int fm) {
 template <int T>
 const void *a16_small_ptr(int fm, int ot) {
     return ot == kF32 ? a16_small_ptr<T, kF32>(fm) : ot == kF16 ? a16_small_ptr<T, kF16>(fm) : a16_small_ptr<T, kBF16>(fm);
+}
+
+int pick_mx(int64_t M, int64_t N, int64_t K) {
+    return M <= 16 ? 3 : M <= 32 ? 4 : M <= 64 ? 5 : 2;
+}
+
+int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a,
+              int64_t ldsa, const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc,
+              int out_type, void *stream) {
+    if (cfg >= kNumMxConfigs || !known_type(out_type)) return PDGEMM_EINVAL_CFG;
+    int rc = check_mx_sizes(M, K, lda, ldsa);
+    if (rc == PDGEMM_OK) rc = check_mx_sizes(N, K, ldb, ldsb);
+    if (rc != PDGEMM_OK) return rc;
+    if (ldc < N) return PDGEMM_EINVAL_LD;
+    if (M == 0 || N == 0) return PDGEMM_OK;
+    rc = check_plain(C, ldc, out_type);
+    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(A, lda, scale_a, ldsa);
+    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(B, ldb, scale_b, ldsb);
+    if (rc != PDGEMM_OK) return rc;
+    if (cfg < 0) cfg = pick_mx(M, N, K);
+    const MxConfig &c = kMxConfigs[cfg];
+    // with K = 0 no operand is read: the kernels form addresses from C instead
+    const uint8_t *const p = static_cast<const uint8_t *>(C);
+    MxArgs args = {K ? A : p, K ? scale_a : p, K ? B : p, K ? scale_b : p, C, K ? lda / 2 : 0, K ? ldb / 2 : 0,
+                   K ? ldsa : 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, c.bm), (int)cdiv(N, c.bn)};
+    const void *fn = out_type == kF32 ? mx_ptr<kF32>(cfg) : out_type == kF16 ? mx_ptr<kF16>(cfg) : mx_ptr<kBF16>(cfg);
+    return run(fn, (int64_t)args.tiles_m * args.tiles_n, c.threads, &args, stream);
 }
 
 }  // namespace
@@ -871,23 +1226,19 @@ int pdgemm_mxf4_dequantize(int64_t rows, int64_t K, const uint8_t *q, int64_t ld
 int gemm_mxf4(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a, int64_t ldsa,
               const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type,
               void *stream) {
-    if (!known_type(out_type)) return PDGEMM_EINVAL_CFG;
-    int rc = check_mx_sizes(M, K, lda, ldsa);
-    if (rc == PDGEMM_OK) rc = check_mx_sizes(N, K, ldb, ldsb);
-    if (rc != PDGEMM_OK) return rc;
-    if (ldc < N) return PDGEMM_EINVAL_LD;
-    if (M == 0 || N == 0) return PDGEMM_OK;
-    rc = check_plain(C, ldc, out_type);
-    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(A, lda, scale_a, ldsa);
-    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(B, ldb, scale_b, ldsb);
-    if (rc != PDGEMM_OK) return rc;
-    const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    // with K = 0 no operand is read: the kernels form addresses from C instead
-    const uint8_t *const c = static_cast<const uint8_t *>(C);
-    MxArgs args = {K ? A : c, K ? scale_a : c, K ? B : c, K ? scale_b : c, C, K ? lda / 2 : 0, K ? ldb / 2 : 0,
-                   K ? ldsa : 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, 16 * fm), (int)cdiv(N, 32)};
-    return run(mx_small_ptr(fm, out_type), (int64_t)args.tiles_m * args.tiles_n, 512, &args, stream);
+    return launch_mx(-1, M, N, K, A, lda, scale_a, ldsa, B, ldb, scale_b, ldsb, C, ldc, out_type, stream);
 }
+
+int pdgemm_mxf4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a,
+                    int64_t ldsa, const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C,
+                    int64_t ldc, int out_type, void *stream) {
+    if (cfg < 0) return PDGEMM_EINVAL_CFG;
+    return launch_mx(cfg, M, N, K, A, lda, scale_a, ldsa, B, ldb, scale_b, ldsb, C, ldc, out_type, stream);
+}
+
+int pdgemm_mxf4_num_configs(void) { return kNumMxConfigs; }
+
+int pdgemm_mxf4_pick(int64_t M, int64_t N, int64_t K) { return pick_mx(M, N, K); }
 
 int gemm_a16_mxf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B, int64_t ldb,
                   const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type, void *stream) {

@@ -284,6 +284,24 @@ def test_product(pd, dev, shape, kind):
     assert_close(out, R, S, -(-K // 64), kind, f"{shape} {kind}")
 
 
+TILE_SHAPES = [(1, 1, 1), (33, 65, 256), (65, 63, 513), (255, 257, 1030), (260, 130, 640), (520, 260, 2049),
+               (300, 520, 8191), (129, 300, 300)]
+
+
+@pytest.mark.parametrize("cfg", range(6))
+@pytest.mark.parametrize("shape", TILE_SHAPES, ids=[f"{m}x{n}x{k}" for m, n, k in TILE_SHAPES])
+def test_product_every_tile(pd, dev, shape, cfg):
+    M, N, K = shape
+    kind = list(TYPES)[(M + cfg) % 3]
+    gu.note(f"[case] gemm_mxf4 {M}x{N}x{K} cfg={cfg} {kind}")
+    a, b, R, S = operands(M, N, K, 4000 + M + N + K, 110, 140)
+    buf, out = guarded(M, N, kind, dev)
+    pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K, out=out, cfg=cfg)
+    torch.cuda.synchronize()
+    check_rest(buf, M, N)
+    assert_close(out, R, S, -(-K // 64), kind, f"{shape} cfg {cfg} {kind}")
+
+
 @pytest.mark.parametrize("bits", [(127, 127), (100, 150), (64, 190), (1, 253)])
 @pytest.mark.parametrize("shape", [(5, 40, 300), (150, 140, 700)], ids=["5x40x300", "150x140x700"])
 def test_product_wide_scales(pd, dev, shape, bits):

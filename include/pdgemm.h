@@ -433,11 +433,17 @@ int pdgemm_mxf4_pick(int64_t M, int64_t N, int64_t K);
 
 /* C = A * B of 16-bit A (a_type PDGEMM_F16 or PDGEMM_BF16, row-major, rows of a
  * multiple of 16 bytes, 16-byte aligned) and MXFP4 B: weights kept in 4 bits
- * under activations that are not quantised.  B's values enter exactly; sums and
- * rounding as in gemm_mxf4. */
+ * under activations that are not quantised.  B's values enter exactly (those of
+ * 2^128 and above, which the quantiser never makes, may be infinite); sums and
+ * rounding as in gemm_mxf4, explicit tiles as pdgemm_mxf4_cfg. */
 int gemm_a16_mxf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                   int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type,
                   void *stream);
+int pdgemm_a16_mxf4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type,
+                        const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc,
+                        int out_type, void *stream);
+int pdgemm_a16_mxf4_num_configs(void);
+int pdgemm_a16_mxf4_pick(int64_t M, int64_t N, int64_t K);
 
 /* Static message for a return code (never NULL): the PDGEMM_E* codes above,
  * or hipGetErrorString() for a positive hipError_t.  Part of the error

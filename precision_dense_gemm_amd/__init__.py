@@ -125,6 +125,12 @@ lib.pdgemm_mxf4_pick.argtypes = [_i64, _i64, _i64]
 lib.pdgemm_mxf4_pick.restype = _i
 lib.gemm_a16_mxf4.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _p, _i64, _i, _p]
 lib.gemm_a16_mxf4.restype = _i
+lib.pdgemm_a16_mxf4_cfg.argtypes = [_i] + lib.gemm_a16_mxf4.argtypes
+lib.pdgemm_a16_mxf4_cfg.restype = _i
+lib.pdgemm_a16_mxf4_num_configs.argtypes = []
+lib.pdgemm_a16_mxf4_num_configs.restype = _i
+lib.pdgemm_a16_mxf4_pick.argtypes = [_i64, _i64, _i64]
+lib.pdgemm_a16_mxf4_pick.restype = _i
 lib.pdgemm_strerror.argtypes = [_i]
 lib.pdgemm_strerror.restype = ctypes.c_char_p
 lib.pdgemm_version.argtypes = []
@@ -722,9 +728,10 @@ def mxf4_pick(M: int, N: int, K: int) -> int:
 
 
 def gemm_a16_mxf4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, out: torch.Tensor | None = None,
-                  out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+                  out_dtype: torch.dtype = torch.float32, stream=None, cfg: int | None = None) -> torch.Tensor:
     """C = A * B of float16 or bfloat16 A (M, K), rows of a multiple of 16 bytes, and MXFP4 Bt
-    (N rows of K values); binary32 sums, C (M, N) float32, float16 or bfloat16."""
+    (N rows of K values); binary32 sums, C (M, N) float32, float16 or bfloat16.  cfg: an
+    explicit tile configuration."""
     if A.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("gemm_a16_mxf4 takes a float16 or bfloat16 A")
     lda = _row_major_2d(A, "A")
@@ -733,11 +740,20 @@ def gemm_a16_mxf4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, out:
         lda = _round_up(lda, 8)
     N, K, ldb, ldsb = _mx_operand(Bt, scale_b, K, "Bt")
     out, ldc = _mx_product_out(out, M, N, out_dtype, A.device, stream)
-    if M and N:
-        _mx_call(lib.gemm_a16_mxf4, (M, N, K, A.data_ptr(), lda, _mx_type(A.dtype, "A"), Bt.data_ptr(), ldb,
-                                     scale_b.data_ptr(), ldsb, out.data_ptr(), ldc, _mx_type(out.dtype, "out")),
-                 [A, scale_b, out, Bt], stream)
+    args = (M, N, K, A.data_ptr(), lda, _mx_type(A.dtype, "A"), Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb,
+            out.data_ptr(), ldc, _mx_type(out.dtype, "out"))
+    fn, args = (lib.gemm_a16_mxf4, args) if cfg is None else (lib.pdgemm_a16_mxf4_cfg, (cfg,) + args)
+    _mx_call(fn, args, [A, Bt, scale_b, out], stream)
     return out
+
+
+def a16_mxf4_num_configs() -> int:
+    return lib.pdgemm_a16_mxf4_num_configs()
+
+
+def a16_mxf4_pick(M: int, N: int, K: int) -> int:
+    """The tile configuration gemm_a16_mxf4 takes for a shape."""
+    return lib.pdgemm_a16_mxf4_pick(M, N, K)
 
 
 def prepare(prec: str, A: torch.Tensor, Bt: torch.Tensor, out: torch.Tensor, K: int | None = None,

@@ -438,6 +438,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int range)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, range, kRsrcWord3);
 }
 
+// byte offset of a tile's row: a row spans at most 4 MiB and a tile 256 rows
+__device__ __forceinline__ uint32_t row_offset(int row, int64_t ld) { return (uint32_t)row * (uint32_t)ld; }
+
 __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     const uintx4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
     return make_uint4(v[0], v[1], v[2], v[3]);
@@ -516,9 +519,9 @@ __global__ __launch_bounds__(W *kWave) void mx_small_kernel(MxArgs args) {
     // rows past M (N) repeat the last one; their results are not stored
     uint32_t va[FM], vb[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) va[i] = (uint32_t)((min(m0 + FM * r + i, M - 1) - m0) * args.lda) + g * 16;
+    for (int i = 0; i < FM; ++i) va[i] = row_offset(min(m0 + FM * r + i, M - 1) - m0, args.lda) + g * 16;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) vb[j] = (uint32_t)((min(n0 + FN * r + j, N - 1) - n0) * args.ldb) + g * 16;
+    for (int j = 0; j < FN; ++j) vb[j] = row_offset(min(n0 + FN * r + j, N - 1) - n0, args.ldb) + g * 16;
     const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
     const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
     const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + blocks * 16;
@@ -698,11 +701,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
         const int chunk = (lane & 7) ^ swizzle8(cr);
         if (j < kDmaA) {
             const int row = cr / WM * WM + FM * (cr % 32) + cr % WM / 32;
-            voff[j] = (uint32_t)((min(m0 + row, M - 1) - m0) * args.lda) + chunk * 16;
+            voff[j] = row_offset(min(m0 + row, M - 1) - m0, args.lda) + chunk * 16;
         } else {
             const int cb = cr - BM;
             const int row = cb / WN * WN + FN * (cb % 32) + cb % WN / 32;
-            voff[j] = (uint32_t)((min(n0 + row, N - 1) - n0) * args.ldb) + chunk * 16;
+            voff[j] = row_offset(min(n0 + row, N - 1) - n0, args.ldb) + chunk * 16;
         }
     }
     // scale copy `wave`, 16 rows of one block per lane.  The waves beyond copy nothing (an
@@ -979,9 +982,9 @@ __global__ __launch_bounds__(W *kWave) void a16_small_kernel(MxArgs args) {
 
     uint32_t va[FM], vb[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) va[i] = (uint32_t)((min(m0 + FM * r + i, M - 1) - m0) * args.lda) + g * 16;
+    for (int i = 0; i < FM; ++i) va[i] = row_offset(min(m0 + FM * r + i, M - 1) - m0, args.lda) + g * 16;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) vb[j] = (uint32_t)((min(n0 + FN * r + j, N - 1) - n0) * args.ldb) + g * 16;
+    for (int j = 0; j < FN; ++j) vb[j] = row_offset(min(n0 + FN * r + j, N - 1) - n0, args.ldb) + g * 16;
     const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
     const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
     const auto ra = rsrc(a_base, (int)((min(BM, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15));
@@ -1050,6 +1053,325 @@ __global__ __launch_bounds__(W *kWave) void a16_small_kernel(MxArgs args) {
         }
     }
     join_and_store<FM, FN, W, OT>(acc, args, m0, n0, tid, lane, wave);
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// Many rows of 16-bit activations: a BM x BN tile of C per workgroup on 16 x 16 x 32
+// MFMAs.  A is staged in lines of 128 bytes (64 values of K), two deep, as the FP16 GEMM
+// does; B in lines of 128 bytes too, which are 256 values of K, two deep, so a line of B
+// serves four steps of A and is copied a quarter per step.  The codes become the 16-bit
+// type in registers, once per wave and step.
+//
+// bf16: its exponents reach the weights' (a code times 2^(byte - 127) is exact, subnormals
+// included, which the MFMA keeps), so the scale goes into the operand: lane group g = l / 16
+// takes half a block, values 16 g .. + 15 of the step, and MFMA u its values 8 u .. + 7.
+// f16: group g takes dword g of a block, the MFMA covers one block and its result is scaled
+// as it is added (see mfma16 above): 4 vector instructions per MFMA, as many cycles as it
+// takes itself.
+//
+// Fragment j holds columns FN n + j (n = l % 16) of the wave's, so a lane's scales of its
+// fragments are one dword and its results neighbouring columns of C.
+template <int T> struct A16Map;
+template <> struct A16Map<kBF16> {
+    static __device__ __forceinline__ int chunk(int u, int g) { return 2 * g + u; }       // of A's 8
+    static __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 3; }
+};
+template <> struct A16Map<kF16> {
+    static __device__ __forceinline__ int chunk(int u, int g) { return 4 * u + g; }
+    static __device__ __forceinline__ int swizzle(int r) { return ((r ^ (r >> 1)) & 1) | ((r >> 2) & 2) | (r & 4); }
+};
+
+// the eight values of a dword of codes times 2^(byte - 127), exact in bf16
+__device__ __forceinline__ uint4 widen_bf16(uint32_t w, float scale) {
+    uint32_t x[4];
+    static_for<4>([&](auto s_c) __attribute__((always_inline)) {
+        constexpr int s = decltype(s_c)::value;
+        const bf16x2_t h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, s);
+        x[s] = __builtin_bit_cast(uint32_t, h);
+    });
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+template <int T, int BM, int BN, int WM, int WN, int OT>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_kernel(MxArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using Out = typename ElemOf<OT>::type;
+    using Map = A16Map<T>;
+    constexpr int NW = (BM / WM) * (BN / WN);
+    constexpr int kWavesN = BN / WN;
+    constexpr int FM = WM / 16, FN = WN / 16, FH = FM / 2;
+    constexpr int kDmaA = BM / 8 / NW;             // copies of 1 KB (8 rows) per wave per step
+    constexpr int kDmaB = BN / 8 / NW / 4;         // ... of a quarter of B's line
+    constexpr int kSc = BN / 128;                  // waves that copy 1 KB of scales
+    static_assert(BM % (8 * NW) == 0 && BN % (32 * NW) == 0 && BN % 128 == 0 && FM % 2 == 0 && FN == 4, "tile");
+    struct LineB {
+        uint4 rows[BN][8];
+        uint4 sc[BN / 2 + 64];   // bytes: [8 blocks of BN columns | unused]
+    };
+    __shared__ uint4 la0[BM][8], la1[BM][8];
+    __shared__ LineB lb0, lb1;
+    using LineA = uint4[BM][8];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int M = args.M, N = args.N, K = args.K;
+    int tile_m, tile_n;
+    tile_of<4, true>(args.tiles_m, args.tiles_n, tile_m, tile_n);
+    const int m0 = tile_m * BM, n0 = tile_n * BN;
+    const int blocks = (K + kBlock - 1) / kBlock;
+    const int n_ln = (blocks + 7) / 8;             // lines of B; four steps each
+    const int whole16 = 2 * (K & ~7);              // bytes of a row's whole chunks of A
+
+    const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
+    const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
+    const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15);
+    const int b_end = (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16;
+    const int sb_cols = min(((N + 15) & ~15) - n0, BN);
+
+    uint32_t va[kDmaA], vb[4 * kDmaB];
+    // (rows of a lane's copies differ by multiples of 16, so their swizzles are the same)
+    static_assert(NW % 2 == 0, "copies of a wave are whole 16-row groups apart");
+    const int a_chunk = ((lane & 7) ^ Map::swizzle(wave * 8 + (lane >> 3))) * 16;
+#pragma unroll
+    for (int j = 0; j < kDmaA; ++j) {
+        const int cr = (j * NW + wave) * 8 + (lane >> 3);
+        va[j] = row_offset(min(m0 + cr, M - 1) - m0, args.lda) + a_chunk;
+    }
+#pragma unroll
+    for (int j = 0; j < 4 * kDmaB; ++j) {
+        const int cr = (j * NW + wave) * 8 + (lane >> 3);
+        const int col = cr / WN * WN + FN * (cr % 16) + cr % WN / 16;   // column FN n + j at LDS row 16 j + n
+        vb[j] = row_offset(min(n0 + col, N - 1) - n0, args.ldb) + ((lane & 7) ^ swizzle8(cr)) * 16;
+    }
+    const bool sc_none = wave >= kSc;
+    const int sd = wave * 64 + lane;
+    const int sc_ld = sc_none ? 0 : (int)args.ldsb, sc_cols = sc_none ? 0 : sb_cols;
+    const uint32_t soff = (uint32_t)(sd / (BN / 16) * sc_ld) + sd % (BN / 16) * 16;
+
+    // step `step` of A; a chunk that reaches past K becomes zeros (its lane's offset leaves the
+    // range), as what lies there, a NaN say, is not to enter a sum
+    auto copy_a = [&](int step, LineA &buf) __attribute__((always_inline)) {
+        const int kb = step * 128;
+        const auto ra = rsrc(a_base + kb, max(a_end - kb, 0));
+#pragma unroll
+        for (int j = 0; j < kDmaA; ++j) {
+            const uint32_t off = kb + a_chunk < whole16 ? va[j] : 0x80000000u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_PTR(&buf[(j * NW + wave) * 8][0]), 16, off, 0, 0, 0);
+        }
+    };
+    // quarter q of line ln of B; with the first one, the line's scales
+    auto copy_b = [&](int ln, auto q_c, LineB &buf) __attribute__((always_inline)) {
+        constexpr int q = decltype(q_c)::value;
+        const int nb = min(blocks - ln * 8, 8);   // at most 0 past K: nothing is read, zeros arrive
+        const auto rb = rsrc(b_base + ln * 128, nb > 0 ? b_end - ln * 128 : 0);
+#pragma unroll
+        for (int j = q * kDmaB; j < (q + 1) * kDmaB; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_PTR(&buf.rows[(j * NW + wave) * 8][0]), 16, vb[j], 0, 0, 0);
+        if constexpr (q == 0) {
+            // (a scale row holds at least the tile's columns, so the range of no blocks is not positive)
+            const auto rs = rsrc(args.SB + n0 + (int64_t)ln * 8 * sc_ld, max((nb - 1) * sc_ld + sc_cols, 0));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, LDS_PTR(&buf.sc[sc_none ? kSc * 64 : wave * 64]), 16, soff, 0, 0, 0);
+        }
+    };
+
+    const int wm0 = (wave / kWavesN) * WM, wn0 = (wave % kWavesN) * WN;
+    const int r = lane & 15, g = lane >> 4;
+    auto read_a = [&](const LineA &buf, int u, int half, uint4 (&fa)[FH]) __attribute__((always_inline)) {
+        const int ch = Map::chunk(u, g) ^ Map::swizzle(r);
+#pragma unroll
+        for (int i = 0; i < FH; ++i) fa[i] = buf[wm0 + (half * FH + i) * 16 + r][ch];
+    };
+    // the codes and scales of step t of a line: bf16 the half block of this group, f16 dword g
+    // of the step's two blocks
+    struct Codes {
+        uint32_t w[FN][2];
+        uint32_t s[T == kBF16 ? 1 : 2];
+    };
+    auto read_b = [&](const LineB &buf, int t, Codes &c) __attribute__((always_inline)) {
+        const uint32_t *const sc = reinterpret_cast<const uint32_t *>(&buf.sc[0]) + (wn0 + FN * r) / 4;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t *const row = reinterpret_cast<const uint32_t *>(&buf.rows[wn0 + j * 16 + r][0]);
+            if constexpr (T == kBF16) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(&row[((2 * t + (g >> 1)) ^ swizzle8(r)) * 4 + 2 * (g & 1)]);
+                c.w[j][0] = v.x;
+                c.w[j][1] = v.y;
+            } else {
+                c.w[j][0] = row[((2 * t) ^ swizzle8(r)) * 4 + g];
+                c.w[j][1] = row[((2 * t + 1) ^ swizzle8(r)) * 4 + g];
+            }
+        }
+        if constexpr (T == kBF16) {
+            c.s[0] = sc[(2 * t + (g >> 1)) * (BN / 4)];
+        } else {
+            c.s[0] = sc[2 * t * (BN / 4)];
+            c.s[1] = sc[(2 * t + 1) * (BN / 4)];
+        }
+    };
+    // B fragments of MFMA u of a step, and (f16) the columns' scales of its block
+    struct FragB {
+        uint4 f[FN];
+        float s[T == kBF16 ? 1 : FN];
+    };
+    auto make_b = [&](const Codes &c, int u, FragB &b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t byte = (c.s[T == kBF16 ? 0 : u] >> (8 * j)) & 255u;
+            if constexpr (T == kBF16) {
+                // the conversion reads the exponent alone: 0 is 2^-127 and 255 gives NaN
+                b.f[j] = widen_bf16(c.w[j][u], __builtin_bit_cast(float, byte << 23));
+            } else {
+                b.f[j] = widen<T>(c.w[j][u]);
+                b.s[j] = scale_or_nan(byte);
+            }
+        }
+    };
+
+    floatx4_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0, 0, 0, 0};
+    auto mma = [&](int half, const uint4 (&fa)[FH], const FragB &b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FH; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                floatx4_t &c = acc[half * FH + i][j];
+                if constexpr (T == kBF16) {
+                    bf16x8_t x, y;
+                    __builtin_memcpy(&x, &fa[i], 16);
+                    __builtin_memcpy(&y, &b.f[j], 16);
+                    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+                } else {
+                    const floatx4_t p = mfma16<T>(fa[i], b.f[j]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[e] = __builtin_fmaf(p[e], b.s[j], c[e]);
+                }
+            }
+    };
+    // The last K % 8 values, which the loop leaves out, first: one MFMA per block, from memory,
+    // in which lane group 0 holds that chunk and the others zeros
+    if (K % 8 != 0) {
+        const int kt = K & ~7;
+        const auto ra = rsrc(a_base, a_end), rb = rsrc(b_base, b_end);
+        const auto rs = rsrc(args.SB + n0 + (int64_t)(kt / kBlock) * args.ldsb, sb_cols);
+        Codes c;
+        FragB b;
+        uint4 fa[FH];
+        const uint32_t sc = load_bytes<4>(rs, wn0 + FN * r);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            c.w[j][0] = load_bytes<4>(rb, row_offset(min(n0 + wn0 + FN * r + j, N - 1) - n0, args.ldb) + kt / 2);
+        c.s[0] = sc;
+        make_b(c, 0, b);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < FH; ++i) {
+                const int row = wm0 + (half * FH + i) * 16 + r;
+                uint4 v = load16(ra, g == 0 ? row_offset(min(m0 + row, M - 1) - m0, args.lda) + 2 * kt : 0x80000000u);
+                uint32_t m[4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) m[d] = K % 8 >= 2 * d + 2 ? 0xFFFFFFFFu : K % 8 == 2 * d + 1 ? 0xFFFFu : 0u;
+                fa[i] = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
+            }
+            if (half == 0)
+                mma(0, fa, b);
+            else
+                mma(1, fa, b);
+        }
+    }
+
+    uint4 fl[FH], fu[FH];
+    Codes codes;
+    FragB b0, b1;
+    // step 4 ln + t from `cur`, whose first lower half is in fl, codes in `codes` and first B
+    // fragments in b0; afterwards the same of the next step, from `nxt` and, past the line's last step, from the other
+    // line.  Copies step + 2 of A into `cur` and the next quarter of the line after the next
+    // step's into the buffer that is free
+    auto step = [&](LineA &cur, const LineA &nxt, LineB &line, LineB &other, int ln, auto t_c)
+        __attribute__((always_inline)) {
+        constexpr int t = decltype(t_c)::value;
+        read_a(cur, 0, 1, fu);
+        mma(0, fl, b0);
+        __builtin_amdgcn_sched_barrier(0);
+        make_b(codes, 1, b1);
+        read_a(cur, 1, 0, fl);
+        mma(1, fu, b0);
+        __builtin_amdgcn_sched_barrier(0);
+        read_a(cur, 1, 1, fu);
+        mma(0, fl, b1);
+        // this wave's copies have landed and its reads of `cur` (and, after a line's last step,
+        // of `line`) are done; after the barrier the same holds for every wave
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        copy_a(4 * ln + t + 2, cur);
+        if constexpr (t < 3)
+            copy_b(ln + 1, std::integral_constant<int, (t + 1) & 3>{}, other);
+        else
+            copy_b(ln + 2, std::integral_constant<int, 0>{}, line);
+        read_a(nxt, 0, 0, fl);
+        read_b(t < 3 ? line : other, (t + 1) & 3, codes);
+        mma(1, fu, b1);
+        make_b(codes, 0, b0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto whole_line = [&](LineB &line, LineB &other, int ln) __attribute__((always_inline)) {
+        step(la0, la1, line, other, ln, std::integral_constant<int, 0>{});
+        step(la1, la0, line, other, ln, std::integral_constant<int, 1>{});
+        step(la0, la1, line, other, ln, std::integral_constant<int, 2>{});
+        step(la1, la0, line, other, ln, std::integral_constant<int, 3>{});
+    };
+    if (n_ln > 0) {
+        copy_a(0, la0);
+        copy_a(1, la1);
+        static_for<4>([&](auto q_c) __attribute__((always_inline)) { copy_b(0, q_c, lb0); });
+        copy_b(1, std::integral_constant<int, 0>{}, lb1);
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        read_a(la0, 0, 0, fl);
+        read_b(lb0, 0, codes);
+        make_b(codes, 0, b0);
+        int ln = 0;
+        for (; ln + 1 < n_ln; ln += 2) {
+            whole_line(lb0, lb1, ln);
+            whole_line(lb1, lb0, ln + 1);
+        }
+        if (ln < n_ln) whole_line(lb0, lb1, ln);
+        // no copy may still be writing this workgroup's LDS when it exits
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+
+    // C, non-temporal.  Register e of lane l in block (i, j): row 16 i + 4 (l / 16) + e, column
+    // FN (l % 16) + j of the wave's tile: a store writes runs of WN columns of four rows
+    typedef Out vec_t __attribute__((ext_vector_type(FN)));
+    typedef vec_t packed_t __attribute__((aligned(sizeof(Out))));
+    const int row0 = m0 + wm0 + 4 * g, col0 = n0 + wn0 + FN * r;
+    Out *const c_lane = static_cast<Out *>(args.C) + (int64_t)row0 * args.ldc + col0;
+    const int rows_left = M - row0, cols_left = N - col0;
+    auto store_all = [&](auto interior_c) __attribute__((always_inline)) {
+        constexpr bool kInterior = decltype(interior_c)::value;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 16 * i + e;
+                Out *const p = c_lane + row * args.ldc;
+                vec_t v;
+#pragma unroll
+                for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
+                if (kInterior || (row < rows_left && FN <= cols_left)) {
+                    __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
+                } else if (row < rows_left) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        if (j < cols_left) p[j] = v[j];
+                }
+            }
+    };
+    if (m0 + BM <= M && n0 + BN <= N)
+        store_all(std::true_type{});
+    else
+        store_all(std::false_type{});
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1131,7 +1453,7 @@ template <int OT>
 const void *mx_ptr(int cfg) {
     switch (cfg) {
     case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 256, 128, 64, 2, OT>);
-    case 1: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 128, 64, 64, 2, OT>);
+    case 1: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 128, 64, 64, 3, OT>);
     case 2: return reinterpret_cast<const void *>(&mx_tile_kernel<128, 128, 64, 64, 2, OT>);
     case 3: return mx_small_ptr<1, OT>();
     case 4: return mx_small_ptr<2, OT>();
@@ -1143,13 +1465,22 @@ template <int T, int FM, int OT>
 const void *a16_small_ptr() {
     return reinterpret_cast<const void *>(&a16_small_kernel<T, FM, 2, 8, OT>);
 }
+constexpr MxConfig kA16Configs[] = {{256, 256, 512}, {128, 128, 256}, {16, 32, 512}, {32, 32, 512}, {64, 32, 512}};
+constexpr int kNumA16Configs = sizeof(kA16Configs) / sizeof(kA16Configs[0]);
+
 template <int T, int OT>
-const void *a16_small_ptr(int fm) {
-    return fm == 1 ? a16_small_ptr<T, 1, OT>() : fm == 2 ? a16_small_ptr<T, 2, OT>() : a16_small_ptr<T, 4, OT>();
+const void *a16_ptr(int cfg) {
+    switch (cfg) {
+    case 0: return reinterpret_cast<const void *>(&a16_tile_kernel<T, 256, 256, 128, 64, OT>);
+    case 1: return reinterpret_cast<const void *>(&a16_tile_kernel<T, 128, 128, 64, 64, OT>);
+    case 2: return a16_small_ptr<T, 1, OT>();
+    case 3: return a16_small_ptr<T, 2, OT>();
+    default: return a16_small_ptr<T, 4, OT>();
+    }
 }
 template <int T>
-const void *a16_small_ptr(int fm, int ot) {
-    return ot == kF32 ? a16_small_ptr<T, kF32>(fm) : ot == kF16 ? a16_small_ptr<T, kF16>(fm) : a16_small_ptr<T, kBF16>(fm);
+const void *a16_ptr(int cfg, int ot) {
+    return ot == kF32 ? a16_ptr<T, kF32>(cfg) : ot == kF16 ? a16_ptr<T, kF16>(cfg) : a16_ptr<T, kBF16>(cfg);
 }
 
 int pick_mx(int64_t M, int64_t N, int64_t K) {
@@ -1176,6 +1507,32 @@ int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_
     MxArgs args = {K ? A : p, K ? scale_a : p, K ? B : p, K ? scale_b : p, C, K ? lda / 2 : 0, K ? ldb / 2 : 0,
                    K ? ldsa : 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, c.bm), (int)cdiv(N, c.bn)};
     const void *fn = out_type == kF32 ? mx_ptr<kF32>(cfg) : out_type == kF16 ? mx_ptr<kF16>(cfg) : mx_ptr<kBF16>(cfg);
+    return run(fn, (int64_t)args.tiles_m * args.tiles_n, c.threads, &args, stream);
+}
+
+int pick_a16(int64_t M, int64_t N, int64_t K) {
+    return M <= 16 ? 2 : M <= 32 ? 3 : M <= 64 ? 4 : cdiv(M, 256) * cdiv(N, 256) >= 192 ? 0 : 1;
+}
+
+int launch_a16(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
+               int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type, void *stream) {
+    if (cfg >= kNumA16Configs || (a_type != kF16 && a_type != kBF16) || !known_type(out_type)) return PDGEMM_EINVAL_CFG;
+    if (M < 0 || M > INT32_MAX) return PDGEMM_EINVAL_DIM;
+    int rc = check_mx_sizes(N, K, ldb, ldsb);
+    if (rc != PDGEMM_OK) return rc;
+    if (lda < K || ldc < N) return PDGEMM_EINVAL_LD;
+    if (M == 0 || N == 0) return PDGEMM_OK;
+    rc = check_plain(C, ldc, out_type);
+    if (rc == PDGEMM_OK && K > 0) rc = check_plain(A, lda, a_type);
+    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(B, ldb, scale_b, ldsb);
+    if (rc == PDGEMM_OK && K > 0 && (lda % 8 || ((uintptr_t)A & 15))) rc = PDGEMM_EALIGN;
+    if (rc != PDGEMM_OK) return rc;
+    if (cfg < 0) cfg = pick_a16(M, N, K);
+    const MxConfig &c = kA16Configs[cfg];
+    const uint8_t *const p = static_cast<const uint8_t *>(C);
+    MxArgs args = {K ? static_cast<const uint8_t *>(A) : p, nullptr, K ? B : p, K ? scale_b : p, C, K ? 2 * lda : 0,
+                   K ? ldb / 2 : 0, 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, c.bm), (int)cdiv(N, c.bn)};
+    const void *fn = a_type == kF16 ? a16_ptr<kF16>(cfg, out_type) : a16_ptr<kBF16>(cfg, out_type);
     return run(fn, (int64_t)args.tiles_m * args.tiles_n, c.threads, &args, stream);
 }
 
@@ -1242,23 +1599,18 @@ int pdgemm_mxf4_pick(int64_t M, int64_t N, int64_t K) { return pick_mx(M, N, K);
 
 int gemm_a16_mxf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B, int64_t ldb,
                   const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type, void *stream) {
-    if ((a_type != kF16 && a_type != kBF16) || !known_type(out_type)) return PDGEMM_EINVAL_CFG;
-    if (M < 0 || M > INT32_MAX) return PDGEMM_EINVAL_DIM;
-    int rc = check_mx_sizes(N, K, ldb, ldsb);
-    if (rc != PDGEMM_OK) return rc;
-    if (lda < K || ldc < N) return PDGEMM_EINVAL_LD;
-    if (M == 0 || N == 0) return PDGEMM_OK;
-    rc = check_plain(C, ldc, out_type);
-    if (rc == PDGEMM_OK && K > 0) rc = check_plain(A, lda, a_type);
-    if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(B, ldb, scale_b, ldsb);
-    if (rc == PDGEMM_OK && K > 0 && (lda % 8 || ((uintptr_t)A & 15))) rc = PDGEMM_EALIGN;
-    if (rc != PDGEMM_OK) return rc;
-    const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    const uint8_t *const c = static_cast<const uint8_t *>(C);
-    MxArgs args = {K ? static_cast<const uint8_t *>(A) : c, nullptr, K ? B : c, K ? scale_b : c, C, K ? 2 * lda : 0,
-                   K ? ldb / 2 : 0, 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, 16 * fm), (int)cdiv(N, 32)};
-    const void *fn = a_type == kF16 ? a16_small_ptr<kF16>(fm, out_type) : a16_small_ptr<kBF16>(fm, out_type);
-    return run(fn, (int64_t)args.tiles_m * args.tiles_n, 512, &args, stream);
+    return launch_a16(-1, M, N, K, A, lda, a_type, B, ldb, scale_b, ldsb, C, ldc, out_type, stream);
 }
+
+int pdgemm_a16_mxf4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type,
+                        const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc,
+                        int out_type, void *stream) {
+    if (cfg < 0) return PDGEMM_EINVAL_CFG;
+    return launch_a16(cfg, M, N, K, A, lda, a_type, B, ldb, scale_b, ldsb, C, ldc, out_type, stream);
+}
+
+int pdgemm_a16_mxf4_num_configs(void) { return kNumA16Configs; }
+
+int pdgemm_a16_mxf4_pick(int64_t M, int64_t N, int64_t K) { return pick_a16(M, N, K); }
 
 }  // extern "C"

@@ -378,6 +378,23 @@ def test_a16(pd, dev, shape, kind, a_kind):
 
 
 @pytest.mark.parametrize("a_kind", ["f16", "bf16"])
+@pytest.mark.parametrize("cfg", range(5))
+@pytest.mark.parametrize("shape", TILE_SHAPES, ids=[f"{m}x{n}x{k}" for m, n, k in TILE_SHAPES])
+def test_a16_every_tile(pd, dev, shape, cfg, a_kind):
+    M, N, K = shape
+    kind = list(TYPES)[(N + cfg) % 3]
+    gu.note(f"[case] gemm_a16_mxf4 {M}x{N}x{K} cfg={cfg} {a_kind} {kind}")
+    t, x = to_type(spread(M, K, 5000 + M + K), a_kind)
+    b = random_operand(N, K, 6000 + N + K, 110, 140)
+    R, S = mx.product(x, mx.values(*b, K))
+    buf, out = guarded(M, N, kind, dev)
+    pd.gemm_a16_mxf4(source(t, dev, gu.round_up(K, 8) - K + 8), *stored(*b, K, dev), out=out, cfg=cfg)
+    torch.cuda.synchronize()
+    check_rest(buf, M, N)
+    assert_close(out, R, S, -(-K // 64) + 1, kind, f"{shape} cfg {cfg} {a_kind} {kind}")
+
+
+@pytest.mark.parametrize("a_kind", ["f16", "bf16"])
 @pytest.mark.parametrize("M", [5, 150])
 def test_a16_wide_and_nan_scales(pd, dev, M, a_kind):
     N, K = 70, 500

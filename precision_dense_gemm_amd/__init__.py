@@ -569,44 +569,69 @@ def _round_up(x: int, m: int) -> int:
 
 
 def _mx_type(dtype, name: str) -> int:
-    if dtype not in _MX_TYPES:
+    kind = _MX_TYPES.get(dtype)
+    if kind is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16")
-    return _MX_TYPES[dtype]
+    return kind
+
+
+# The calls these serve can be shorter than their checks, so the checks are few and cheap:
+# one look at a tensor's shape and stride, device indices rather than device objects, and
+# the current stream's handle without a Stream object around it.
+
+def _mx_rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """(rows, columns, row stride) of a 2-D tensor with contiguous rows."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
+    return rows, cols, (ld if rows > 1 or ld > cols else cols)
 
 
 def _mx_operand(codes: torch.Tensor, scales: torch.Tensor, K: int | None, name: str):
     """(rows, K, ld in values, scale row stride) of an MXFP4 operand.  An array of a single
     row has no stride to speak of: it takes the next multiple the library accepts."""
-    for t, what in ((codes, "codes"), (scales, "scales")):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
-            raise TypeError(f"{name}'s {what} must be a uint8 tensor")
-    ld, lds = _row_major_2d(codes, f"{name}'s codes"), _row_major_2d(scales, f"{name}'s scales")
-    rows = codes.shape[0]
-    K = 2 * codes.shape[1] if K is None else K
-    if K < 0 or 2 * codes.shape[1] < K:
+    if not isinstance(codes, torch.Tensor) or codes.dtype is not torch.uint8:
+        raise TypeError(f"{name}'s codes must be a uint8 tensor")
+    if not isinstance(scales, torch.Tensor) or scales.dtype is not torch.uint8:
+        raise TypeError(f"{name}'s scales must be a uint8 tensor")
+    rows, width, ld = _mx_rows(codes, name)
+    have, cols, lds = _mx_rows(scales, name)
+    if K is None:
+        K = 2 * width
+    elif K < 0 or 2 * width < K:
         raise ValueError(f"{name} holds fewer than K values per row")
     blocks = (K + MX_BLOCK - 1) // MX_BLOCK
-    if scales.shape[0] < blocks or scales.shape[1] < rows:
+    if have < blocks or cols < rows:
         raise ValueError(f"{name}'s scales must hold {blocks} blocks of {rows} rows")
     if rows <= 1:
-        ld = _round_up(max(ld, codes.shape[1]), 16)
-    if scales.shape[0] <= 1:
-        lds = _round_up(max(lds, scales.shape[1]), 16)
+        ld = _round_up(ld, 16)
+    if have <= 1:
+        lds = _round_up(lds, 16)
     return rows, K, 2 * ld, lds
 
 
 def _mx_call(fn, args, tensors, stream):
     """Runs fn(*args, stream) for tensors of one GPU, with that GPU current: on `stream`, or
     on its current stream."""
-    device = tensors[0].device
-    if any(t.device != device for t in tensors):
-        raise ValueError("all tensors must be on the same GPU")
+    index = tensors[0].get_device()   # -1: not on a GPU
+    for t in tensors:
+        if t.get_device() != index or index < 0:
+            raise ValueError("all tensors must be on the same GPU")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index == index:
+        handle = stream.cuda_stream
+    else:
         raise ValueError("stream must be on the tensors' GPU")
-    with torch.cuda.device(device):
-        rc = fn(*args, ctypes.c_void_p(stream.cuda_stream))
+    if index == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
     if rc != 0:
         raise PdgemmError(rc)
 
@@ -620,42 +645,47 @@ def _mx_empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _mx_alloc(rows: int, K: int, device, stream):
-    """A new MXFP4 operand (codes, scales): rows of a multiple of 16 bytes."""
+def _mx_form(out, rows: int, K: int, device, stream, name: str):
+    """An operand to write, `out` or a new one whose rows are a multiple of 16 bytes: its
+    tensors, and its part of the C call's arguments."""
+    if out is not None:
+        codes, scales = out
+        r, _, ld, lds = _mx_operand(codes, scales, K, name)
+        if r != rows:
+            raise ValueError(f"{name} must have {rows} rows")
+        return (codes, scales), (codes.data_ptr(), ld, scales.data_ptr(), lds)
     blocks = (K + MX_BLOCK - 1) // MX_BLOCK
+    lds = _round_up(rows, 16)
     codes = _mx_empty((rows, 16 * blocks), torch.uint8, device, stream)
-    scales = _mx_empty((blocks, _round_up(rows, 16)), torch.uint8, device, stream)
-    return codes[:, :(K + 1) // 2], scales[:, :rows]
+    scales = _mx_empty((blocks, lds), torch.uint8, device, stream)
+    args = (codes.data_ptr(), 32 * blocks, scales.data_ptr(), lds)
+    if K & 31:
+        codes = codes[:, :(K + 1) // 2]
+    if rows != lds:
+        scales = scales[:, :rows]
+    return (codes, scales), args
 
 
-def _mx_out(out, rows: int, K: int, device, stream, name: str):
-    """An operand to write: `out`, checked, or a new one; with its strides."""
-    codes, scales = _mx_alloc(rows, K, device, stream) if out is None else out
-    r, _, ld, lds = _mx_operand(codes, scales, K, name)
-    if r != rows:
-        raise ValueError(f"{name} must have {rows} rows")
-    return codes, scales, ld, lds
+_MX_NO_FORM = (None, 0, None, 0)
 
 
 def _mx_quantize(x, along_k: bool, along_rows: bool, scale_rule, out, out_t, stream):
     kind = _mx_type(x.dtype, "x")
-    if scale_rule not in _MX_RULES:
+    rule = _MX_RULES.get(scale_rule)
+    if rule is None:
         raise ValueError(f"scale_rule must be one of {sorted(_MX_RULES)}")
-    ld = _row_major_2d(x, "x")
-    rows, K = x.shape
-    q = _mx_out(out, rows, K, x.device, stream, "out") if along_k else None
-    qt = _mx_out(out_t, K, rows, x.device, stream, "the transposed out") if along_rows else None
-    tensors, forms = [x], []
-    for form in (q, qt):
-        if form is None:
-            forms += [None, 0, None, 0]
-        else:
-            tensors += form[:2]
-            forms += [form[0].data_ptr(), form[2], form[1].data_ptr(), form[3]]
+    rows, K, ld = _mx_rows(x, "x")
+    device = x.device
+    q = qt = None
+    args = args_t = _MX_NO_FORM
+    if along_k:
+        q, args = _mx_form(out, rows, K, device, stream, "out")
+    if along_rows:
+        qt, args_t = _mx_form(out_t, K, rows, device, stream, "the transposed out")
     if rows and K:
-        _mx_call(lib.pdgemm_mxf4_quantize, (rows, K, x.data_ptr(), ld, kind, *forms, _MX_RULES[scale_rule]),
-                 tensors, stream)
-    return (None if q is None else q[:2]), (None if qt is None else qt[:2])
+        tensors = (x,) + (() if out is None else q) + (() if out_t is None else qt)
+        _mx_call(lib.pdgemm_mxf4_quantize, (rows, K, x.data_ptr(), ld, kind, *args, *args_t, rule), tensors, stream)
+    return q, qt
 
 
 def mxf4_quantize(x: torch.Tensor, transpose: bool = False, scale_rule: str = "floor", out=None, stream=None):
@@ -676,30 +706,27 @@ def mxf4_quantize_both(x: torch.Tensor, scale_rule: str = "floor", out=None, str
     return _mx_quantize(x, True, True, scale_rule, first, second, stream)
 
 
+def _mx_dense_out(out, rows, cols, out_dtype, device, stream):
+    """(out or a new tensor, its row stride, its type)."""
+    kind = _mx_type(out_dtype if out is None else out.dtype, "the output")
+    if out is None:
+        return _mx_empty((rows, cols), out_dtype, device, stream), cols, kind
+    r, c, ld = _mx_rows(out, "out")
+    if (r, c) != (rows, cols):
+        raise ValueError(f"out must have shape {(rows, cols)}")
+    return out, ld, kind
+
+
 def mxf4_dequantize(codes: torch.Tensor, scales: torch.Tensor, K: int | None = None,
                     out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
                     stream=None) -> torch.Tensor:
     """The values (rows, K) of an MXFP4 operand, as out's dtype, else out_dtype (float32: exact)."""
     rows, K, ld, lds = _mx_operand(codes, scales, K, "the operand")
-    _mx_type(out_dtype if out is None else out.dtype, "the output")
-    if out is None:
-        out = _mx_empty((rows, K), out_dtype, codes.device, stream)
-    elif tuple(out.shape) != (rows, K):
-        raise ValueError(f"out must have shape {(rows, K)}")
+    out, ldd, kind = _mx_dense_out(out, rows, K, out_dtype, codes.device, stream)
     if rows and K:
         _mx_call(lib.pdgemm_mxf4_dequantize, (rows, K, codes.data_ptr(), ld, scales.data_ptr(), lds, out.data_ptr(),
-                                              _row_major_2d(out, "out"), _mx_type(out.dtype, "out")),
-                 [codes, scales, out], stream)
+                                              ldd, kind), (codes, scales, out), stream)
     return out
-
-
-def _mx_product_out(out, M, N, out_dtype, device, stream):
-    _mx_type(out_dtype if out is None else out.dtype, "the output")
-    if out is None:
-        out = _mx_empty((M, N), out_dtype, device, stream)
-    elif tuple(out.shape) != (M, N):
-        raise ValueError(f"out must have shape {(M, N)}")
-    return out, _row_major_2d(out, "out")
 
 
 def gemm_mxf4(A: torch.Tensor, scale_a: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, K: int | None = None,
@@ -707,14 +734,15 @@ def gemm_mxf4(A: torch.Tensor, scale_a: torch.Tensor, Bt: torch.Tensor, scale_b:
               cfg: int | None = None) -> torch.Tensor:
     """C = A * B of MXFP4 A (M rows) and Bt (N rows); binary32 sums, C (M, N) float32, float16
     or bfloat16 (out's dtype, else out_dtype).  cfg: an explicit tile configuration."""
-    K = 2 * min(A.shape[1], Bt.shape[1]) if K is None else K
-    M, K, lda, ldsa = _mx_operand(A, scale_a, K, "A")
-    N, K, ldb, ldsb = _mx_operand(Bt, scale_b, K, "Bt")
-    out, ldc = _mx_product_out(out, M, N, out_dtype, A.device, stream)
-    args = (M, N, K, A.data_ptr(), lda, scale_a.data_ptr(), ldsa, Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb,
-            out.data_ptr(), ldc, _mx_type(out.dtype, "out"))
+    M, Ka, lda, ldsa = _mx_operand(A, scale_a, K, "A")
+    N, Kb, ldb, ldsb = _mx_operand(Bt, scale_b, K, "Bt")
+    if Ka != Kb:
+        raise ValueError("A and Bt disagree on K")
+    out, ldc, kind = _mx_dense_out(out, M, N, out_dtype, A.device, stream)
+    args = (M, N, Ka, A.data_ptr(), lda, scale_a.data_ptr(), ldsa, Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb,
+            out.data_ptr(), ldc, kind)
     fn, args = (lib.gemm_mxf4, args) if cfg is None else (lib.pdgemm_mxf4_cfg, (cfg,) + args)
-    _mx_call(fn, args, [A, scale_a, Bt, scale_b, out], stream)
+    _mx_call(fn, args, (A, scale_a, Bt, scale_b, out), stream)
     return out
 
 
@@ -734,16 +762,15 @@ def gemm_a16_mxf4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, out:
     explicit tile configuration."""
     if A.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("gemm_a16_mxf4 takes a float16 or bfloat16 A")
-    lda = _row_major_2d(A, "A")
-    M, K = A.shape
+    M, K, lda = _mx_rows(A, "A")
     if M <= 1:
         lda = _round_up(lda, 8)
     N, K, ldb, ldsb = _mx_operand(Bt, scale_b, K, "Bt")
-    out, ldc = _mx_product_out(out, M, N, out_dtype, A.device, stream)
-    args = (M, N, K, A.data_ptr(), lda, _mx_type(A.dtype, "A"), Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb,
-            out.data_ptr(), ldc, _mx_type(out.dtype, "out"))
+    out, ldc, kind = _mx_dense_out(out, M, N, out_dtype, A.device, stream)
+    args = (M, N, K, A.data_ptr(), lda, _MX_TYPES[A.dtype], Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb,
+            out.data_ptr(), ldc, kind)
     fn, args = (lib.gemm_a16_mxf4, args) if cfg is None else (lib.pdgemm_a16_mxf4_cfg, (cfg,) + args)
-    _mx_call(fn, args, [A, Bt, scale_b, out], stream)
+    _mx_call(fn, args, (A, Bt, scale_b, out), stream)
     return out
 
 

@@ -473,125 +473,33 @@ __device__ __forceinline__ void static_for(F &&f) {
 
 // Sum of the waves' partial tiles (each wave summed its own range of K) in wave order,
 // rounded once to C's type and stored.  acc[i][j] of a wave holds, in register e of lane
-// l, row FM * (4 (l / 16) + e) + i and column FN * (l % 16) + j of the tile.
-template <int FM, int FN, int W, int OT>
-__device__ __forceinline__ void join_and_store(floatx4_t (&acc)[FM][FN], const MxArgs &args, int m0, int n0, int tid,
-                                               int lane, int wave) {
+// l, row FM * (4 (l / 16) + e) + i (with kMixed; else 16 i + 4 (l / 16) + e) and column
+// FN * (l % 16) + j of the tile.  `part` is LDS of kStride floats per wave, each wave's part
+// free for it to write.
+template <int FM, int FN, int W, int OT, int kStride, bool kMixed>
+__device__ __forceinline__ void join_and_store(floatx4_t (&acc)[FM][FN], float *part, const MxArgs &args, int m0, int n0,
+                                               int tid, int lane, int wave) {
     using Out = typename ElemOf<OT>::type;
     constexpr int BM = 16 * FM, BN = 16 * FN;
-    __shared__ float part[W][FM * FN * 4][kWave];
+    static_assert(kStride >= FM * FN * 4 * kWave, "a wave's partial tile");
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[wave][(i * FN + j) * 4 + e][lane] = acc[i][j][e];
+            for (int e = 0; e < 4; ++e) part[wave * kStride + ((i * FN + j) * 4 + e) * kWave + lane] = acc[i][j][e];
     __syncthreads();
     Out *const C = static_cast<Out *>(args.C);
     for (int x = tid; x < BM * BN; x += W * kWave) {
         const int row = x / BN, col = x % BN;
         if (m0 + row >= args.M || n0 + col >= args.N) continue;
-        const int rr = row / FM, cc = col / FN;
-        const int reg = ((row % FM) * FN + col % FN) * 4 + (rr & 3), l = (rr >> 2) * 16 + cc;
-        float sum = part[0][reg][l];
+        const int i = kMixed ? row % FM : row / 16, rr = kMixed ? row / FM : row % 16;
+        const int at = ((i * FN + col % FN) * 4 + (rr & 3)) * kWave + (rr >> 2) * 16 + col / FN;
+        float sum = part[at];
 #pragma unroll
-        for (int w = 1; w < W; ++w) sum += part[w][reg][l];
+        for (int w = 1; w < W; ++w) sum += part[w * kStride + at];
         C[(int64_t)(m0 + row) * args.ldc + n0 + col] = (Out)sum;
     }
-}
-
-// Few rows: a tile of 16 FM x 16 FN of C per workgroup, whose W waves take the 128-byte
-// lines of K in turn and read them from memory straight into the fragments' registers,
-// kLines lines at once.  Fragment i holds rows FM r + i (r = 0 .. 15), so that a lane's
-// scales of its fragments are neighbouring bytes.
-template <int FM, int FN, int W, int kLines, int OT>
-__global__ __launch_bounds__(W *kWave) void mx_small_kernel(MxArgs args) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int BM = 16 * FM, BN = 16 * FN;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int r = lane & 15, g = lane >> 4;
-    const int m0 = (blockIdx.x / args.tiles_n) * BM, n0 = (blockIdx.x % args.tiles_n) * BN;
-    const int M = args.M, N = args.N, K = args.K;
-    const int blocks = (K + kBlock - 1) / kBlock;
-    const int lines = (blocks + 7) / 8;
-
-    // rows past M (N) repeat the last one; their results are not stored
-    uint32_t va[FM], vb[FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) va[i] = row_offset(min(m0 + FM * r + i, M - 1) - m0, args.lda) + g * 16;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) vb[j] = row_offset(min(n0 + FN * r + j, N - 1) - n0, args.ldb) + g * 16;
-    const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
-    const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
-    const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + blocks * 16;
-    const int b_end = (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16;
-    // a block's scales are read up to the 16-byte granule that holds the last row's
-    const int sa_cols = min(((M + 15) & ~15) - m0, BM), sb_cols = min(((N + 15) & ~15) - n0, BN);
-
-    floatx4_t acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0, 0, 0, 0};
-
-    for (int first = wave; first < lines; first += W * kLines) {
-        uint4 fa[kLines][2][FM], fb[kLines][2][FN];
-        uint32_t sa[kLines][2], sb[kLines][2];
-#pragma unroll
-        for (int u = 0; u < kLines; ++u) {
-            // a line past K reads nothing: zeros come back
-            const int line = first + u * W;
-            const int nb = min(blocks - line * 8, 8);
-            const auto ra = rsrc(a_base, nb > 0 ? a_end : 0), rb = rsrc(b_base, nb > 0 ? b_end : 0);
-            const auto rsa = rsrc(args.SA + (int64_t)line * 8 * args.ldsa + m0, nb > 0 ? (int)((nb - 1) * args.ldsa) + sa_cols : 0);
-            const auto rsb = rsrc(args.SB + (int64_t)line * 8 * args.ldsb + n0, nb > 0 ? (int)((nb - 1) * args.ldsb) + sb_cols : 0);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                for (int j = 0; j < FN; ++j) fb[u][q][j] = load16(rb, vb[j] + line * 128 + q * 64);
-#pragma unroll
-                for (int i = 0; i < FM; ++i) fa[u][q][i] = load16(ra, va[i] + line * 128 + q * 64);
-                sa[u][q] = load_bytes<FM>(rsa, (uint32_t)((4 * q + g) * args.ldsa) + FM * r);
-                sb[u][q] = load_bytes<FN>(rsb, (uint32_t)((4 * q + g) * args.ldsb) + FN * r);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kLines; ++u) {
-            const int line = first + u * W;
-            if (line * 256 + 256 > K) {
-                // A's values at and beyond K become zeros: what is beside them in B is
-                // finite (e2m1 holds nothing else), and scales past the last block are zero
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int n = K - (line * 256 + q * 128 + g * kBlock);
-                    uint32_t m[4];
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        const int left = n - 8 * d;
-                        m[d] = left >= 8 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (4 * left)) - 1u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < FM; ++i) {
-                        fa[u][q][i].x &= m[0];
-                        fa[u][q][i].y &= m[1];
-                        fa[u][q][i].z &= m[2];
-                        fa[u][q][i].w &= m[3];
-                    }
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                static_for<FM>([&](auto i_c) __attribute__((always_inline)) {
-                    static_for<FN>([&](auto j_c) __attribute__((always_inline)) {
-                        constexpr int i = decltype(i_c)::value, j = decltype(j_c)::value;
-                        acc[i][j] = mfma_fp4<i, j>(fa[u][q][i], fb[u][q][j], acc[i][j], sa[u][q], sb[u][q]);
-                    });
-                });
-        }
-    }
-    join_and_store<FM, FN, W, OT>(acc, args, m0, n0, tid, lane, wave);
-#endif  // __HIP_DEVICE_COMPILE__
 }
 
 // Block id -> tile, the order of the other GEMM kernels: workgroups are dispatched
@@ -911,40 +819,179 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+// Few rows: a tile of 16 FM x 16 FN of C per workgroup, whose W waves take the 128-byte lines
+// of K in turn, on 16 x 16 x 128 MFMAs, and join their sums at the end.  Every wave has its own
+// three slots of a line of the tile's rows in LDS, filled two lines ahead, so the loop has
+// no barrier.  (A fragment's lanes 0 .. 15 are 16 rows: read from memory straight into
+// registers it touches 16 lines per instruction, at about 16 bytes a clock per CU; copied in
+// whole lines, 8 lanes each, and read from LDS, 64 x 8192 x 8192 took 9.5 us and not 14.3,
+// 1 x 8192 x 8192 7.5 and not 7.7.)  Fragment i holds rows FM r + i (r = 0 .. 15), so that a lane's scales of
+// its fragments are neighbouring bytes.
+template <int FM, int FN, int W, int OT>
+__global__ __launch_bounds__(W *kWave) void mx_few_kernel(MxArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int BM = 16 * FM, BN = 16 * FN;
+    constexpr int kRows = BM + BN;
+    constexpr int kDma = kRows / 8;                // copies of 1 KB (8 rows) per line
+    constexpr int kAll = kDma + 4;                 // ... and 4 loads of scales
+    struct Slot {
+        uint4 rows[kRows][8];
+    };
+    struct Scales {
+        uint32_t a[2], b[2];
+    };
+    __shared__ Slot s0[W], s1[W], s2[W];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int r = lane & 15, g = lane >> 4;
+    const int m0 = (blockIdx.x / args.tiles_n) * BM, n0 = (blockIdx.x % args.tiles_n) * BN;
+    const int M = args.M, N = args.N, K = args.K;
+    const int blocks = (K + kBlock - 1) / kBlock;
+    const int lines = (blocks + 7) / 8;
+
+    const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
+    const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
+    const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + blocks * 16;
+    const int b_end = (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16;
+    // fragment i's row r of a tile (FM r + i) at LDS row 16 i + r; chunk c at c ^ swizzle16(row)
+    auto swizzle16 = [](int row) __attribute__((always_inline)) { return ((row ^ (row >> 1)) & 1) | ((row >> 2) & 2) | (row & 4); };
+    uint32_t voff[kDma];
+#pragma unroll
+    for (int j = 0; j < kDma; ++j) {
+        const int cr = j * 8 + (lane >> 3);
+        const int chunk = (lane & 7) ^ swizzle16(cr);
+        if (j < BM / 8)
+            voff[j] = row_offset(min(m0 + FM * (cr % 16) + cr / 16, M - 1) - m0, args.lda) + chunk * 16;
+        else
+            voff[j] = row_offset(min(n0 + FN * ((cr - BM) % 16) + (cr - BM) / 16, N - 1) - n0, args.ldb) + chunk * 16;
+    }
+    // a block's scales are read up to the 16-byte granule that holds the last row's
+    const int sa_cols = min(((M + 15) & ~15) - m0, BM), sb_cols = min(((N + 15) & ~15) - n0, BN);
+    const int ldsa = (int)args.ldsa, ldsb = (int)args.ldsb;
+
+    // a line past K reads nothing: zeros arrive
+    auto copy = [&](int line, Slot &slot, Scales &sc) __attribute__((always_inline)) {
+        const int nb = min(blocks - line * 8, 8);
+        const auto ra = rsrc(a_base + line * 128, nb > 0 ? a_end - line * 128 : 0);
+        const auto rb = rsrc(b_base + line * 128, nb > 0 ? b_end - line * 128 : 0);
+        const auto rsa = rsrc(args.SA + (int64_t)line * 8 * args.ldsa + m0, max((nb - 1) * ldsa + sa_cols, 0));
+        const auto rsb = rsrc(args.SB + (int64_t)line * 8 * args.ldsb + n0, max((nb - 1) * ldsb + sb_cols, 0));
+#pragma unroll
+        for (int j = 0; j < kDma; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(j < BM / 8 ? ra : rb, LDS_PTR(&slot.rows[j * 8][0]), 16, voff[j], 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            sc.a[q] = load_bytes<FM>(rsa, (4 * q + g) * ldsa + FM * r);
+            sc.b[q] = load_bytes<FN>(rsb, (4 * q + g) * ldsb + FN * r);
+        }
+    };
+
+    floatx4_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0, 0, 0, 0};
+
+    auto turn = [&](int line, Slot &slot, Scales &sc) __attribute__((always_inline)) {
+        // this line's copies have landed; the two lines' after it may be in flight
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kAll) : "memory");
+        uint4 fa[2][FM], fb[2][FN];
+        const uint32_t sa[2] = {sc.a[0], sc.a[1]}, sb[2] = {sc.b[0], sc.b[1]};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int ch = (4 * q + g) ^ swizzle16(r);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) fa[q][i] = slot.rows[16 * i + r][ch];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) fb[q][j] = slot.rows[BM + 16 * j + r][ch];
+        }
+        // the slot is read: it takes the line after the next two
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        copy(line + 3 * W, slot, sc);
+        if (line * 256 + 256 > K) {
+            // A's values at and beyond K become zeros: what is beside them in B is finite (e2m1
+            // holds nothing else), and scales past the last block are zero
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int n = K - (line * 256 + q * 128 + g * kBlock);
+                uint32_t m[4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const int left = n - 8 * d;
+                    m[d] = left >= 8 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (4 * left)) - 1u;
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    uint4 &v = fa[q][i];
+                    v = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            static_for<FM>([&](auto i_c) __attribute__((always_inline)) {
+                static_for<FN>([&](auto j_c) __attribute__((always_inline)) {
+                    constexpr int i = decltype(i_c)::value, j = decltype(j_c)::value;
+                    acc[i][j] = mfma_fp4<i, j>(fa[q][i], fb[q][j], acc[i][j], sa[q], sb[q]);
+                });
+            });
+    };
+    if (wave < lines) {
+        Scales c0, c1, c2;
+        copy(wave, s0[wave], c0);
+        copy(wave + W, s1[wave], c1);
+        copy(wave + 2 * W, s2[wave], c2);
+        for (int line = wave; line < lines; line += 3 * W) {
+            turn(line, s0[wave], c0);
+            if (line + W >= lines) break;
+            turn(line + W, s1[wave], c1);
+            if (line + 2 * W >= lines) break;
+            turn(line + 2 * W, s2[wave], c2);
+        }
+        // no copy may still be writing this workgroup's LDS when it exits
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    join_and_store<FM, FN, W, OT, sizeof(Slot) / 4, true>(acc, reinterpret_cast<float *>(&s0[0]), args, m0, n0, tid, lane, wave);
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
 // 16-bit activations times MXFP4 weights.  The codes become the 16-bit type exactly
 // (e2m1 values need two significant bits); an MFMA of 32 values of K covers one block,
 // and its result is scaled by the block's 2^(byte - 127) as it is added to the sum, in
 // binary32: with the scale in the 16-bit operand instead, an f16 weight below 2^-24
 // would vanish.
 template <int T>
-__device__ __forceinline__ floatx4_t mfma16(const uint4 &a, const uint4 &b) {
-    const floatx4_t zero = {0, 0, 0, 0};
+__device__ __forceinline__ floatx4_t mfma16(const uint4 &a, const uint4 &b, const floatx4_t &c) {
     if constexpr (T == kF16) {
         half8_t x, y;
         __builtin_memcpy(&x, &a, 16);
         __builtin_memcpy(&y, &b, 16);
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, zero, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
     } else {
         bf16x8_t x, y;
         __builtin_memcpy(&x, &a, 16);
         __builtin_memcpy(&y, &b, 16);
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, zero, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
     }
 }
 
-// the eight values of a dword of codes as the 16-bit type
-template <int T>
-__device__ __forceinline__ uint4 widen(uint32_t w) {
+// the eight values of a dword of codes, exact: as f16, or times a power of two as bf16
+__device__ __forceinline__ uint4 widen_f16(uint32_t w) {
     uint32_t x[4];
     static_for<4>([&](auto s_c) __attribute__((always_inline)) {
         constexpr int s = decltype(s_c)::value;
-        if constexpr (T == kF16) {
-            const half2_t h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, s);
-            x[s] = __builtin_bit_cast(uint32_t, h);
-        } else {
-            const bf16x2_t h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, s);
-            x[s] = __builtin_bit_cast(uint32_t, h);
-        }
+        const half2_t h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, s);
+        x[s] = __builtin_bit_cast(uint32_t, h);
+    });
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ uint4 widen_bf16(uint32_t w, float scale) {
+    uint32_t x[4];
+    static_for<4>([&](auto s_c) __attribute__((always_inline)) {
+        constexpr int s = decltype(s_c)::value;
+        const bf16x2_t h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, s);
+        x[s] = __builtin_bit_cast(uint32_t, h);
     });
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
@@ -954,42 +1001,75 @@ __device__ __forceinline__ float scale_or_nan(uint32_t byte) {
     return byte == 255 ? __builtin_nanf("") : scale_value(byte);
 }
 
-// Dword t of the chunks that the four 16-lane groups hold goes to group t: chunk g of
-// group g holds block g, and afterwards w[t] of group g is dword g of block t.
-__device__ __forceinline__ void transpose_groups(uint32_t (&w)[4]) {
-    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    w[0] = c[0];
-    w[1] = c[1];
-    w[2] = d[0];
-    w[3] = d[1];
-}
-
-// The same tile as mx_small_kernel, with A in 16 bits (T).
-template <int T, int FM, int FN, int W, int OT>
-__global__ __launch_bounds__(W *kWave) void a16_small_kernel(MxArgs args) {
+// Few rows of 16-bit activations: the scheme of mx_few_kernel in steps of 128 values of K,
+// 256 bytes (two lines) of a row of A and half a line of B; neighbouring waves take the two
+// halves of a line.  The operands' maps are those of the tile kernel below, with the step's
+// four blocks in place of two halves: bf16, lane group g holds block g, scaled as it is
+// widened, and MFMA u its values 8 u .. + 7; f16, MFMA u covers block u, of which group g
+// holds dword g, and its result is scaled as it is added.
+template <int T, int FM, int FN, int W, int S, int OT>
+__global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int BM = 16 * FM, BN = 16 * FN;
+    constexpr int kDmaA = BM / 4, kDmaB = BN / 16;      // copies of 1 KB (4 rows of A, 16 of B) per step
+    constexpr int kSc = T == kBF16 ? 1 : 4;             // loads of scales per step
+    constexpr int kAll = kDmaA + kDmaB + kSc;
+    static_assert(S == 2 || S == 3, "slots per wave");
+    static_assert((S - 1) * kAll <= 63, "vmcnt holds at most 63 outstanding loads");
+    struct Slot {
+        uint4 a[BM][16];   // chunk c of row r at c ^ swz_a(r)
+        uint4 b[BN][4];    // chunk c of row r at c ^ ((r / 4) % 4)
+    };
+    struct Scales {
+        uint32_t v[kSc];
+    };
+    __shared__ Slot s0[W], s1[W];
+    __shared__ typename std::conditional<(S > 2), Slot, char>::type s2[S > 2 ? W : 1];
+
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane & 15, g = lane >> 4;
     const int m0 = (blockIdx.x / args.tiles_n) * BM, n0 = (blockIdx.x % args.tiles_n) * BN;
     const int M = args.M, N = args.N, K = args.K;
     const int blocks = (K + kBlock - 1) / kBlock;
-    const int lines = (blocks + 7) / 8;
+    const int steps = (blocks + 3) / 4;
 
-    uint32_t va[FM], vb[FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) va[i] = row_offset(min(m0 + FM * r + i, M - 1) - m0, args.lda) + g * 16;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) vb[j] = row_offset(min(n0 + FN * r + j, N - 1) - n0, args.ldb) + g * 16;
     const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
     const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
-    const auto ra = rsrc(a_base, (int)((min(BM, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15));
-    const auto rb = rsrc(b_base, (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16);
-    const int sb_cols = min(((N + 15) & ~15) - n0, BN);
+    const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15);
+    const int b_end = (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16;
+    const int sb_cols = min(((N + 15) & ~15) - n0, BN), ldsb = (int)args.ldsb;
+    // positions of 256-byte rows are bank groups, and a phase of a read takes 8 rows at chunk c
+    // and at c ^ 8 (bf16) or c ^ 2 (f16): the 8 rows' terms differ outside that bit
+    auto swz_a = [](int row) __attribute__((always_inline)) {
+        return T == kBF16 ? row & 7 : (row & 1) | ((row & 6) << 1);
+    };
+    uint32_t va[kDmaA], vb[kDmaB];
+#pragma unroll
+    for (int j = 0; j < kDmaA; ++j) {
+        const int cr = j * 4 + (lane >> 4);
+        va[j] = row_offset(min(m0 + cr, M - 1) - m0, args.lda) + ((lane & 15) ^ swz_a(cr)) * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < kDmaB; ++j) {
+        const int cr = lane >> 2;   // column FN n + j at LDS row 16 j + n
+        vb[j] = row_offset(min(n0 + FN * cr + j, N - 1) - n0, args.ldb) + ((lane & 3) ^ ((cr >> 2) & 3)) * 16;
+    }
+    // a step past K reads nothing: zeros arrive
+    auto copy = [&](int step, Slot &slot, Scales &sc) __attribute__((always_inline)) {
+        const int nb = min(blocks - step * 4, 4);
+        const auto ra = rsrc(a_base + step * 256, nb > 0 ? a_end - step * 256 : 0);
+        const auto rb = rsrc(b_base + step * 64, nb > 0 ? b_end - step * 64 : 0);
+        const auto rs = rsrc(args.SB + (int64_t)step * 4 * args.ldsb + n0, max((nb - 1) * ldsb + sb_cols, 0));
+#pragma unroll
+        for (int j = 0; j < kDmaB; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_PTR(&slot.b[j * 16][0]), 16, vb[j], 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kDmaA; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_PTR(&slot.a[j * 4][0]), 16, va[j], 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < kSc; ++u) sc.v[u] = load_bytes<FN>(rs, (T == kBF16 ? g : u) * ldsb + FN * r);
+    };
 
     floatx4_t acc[FM][FN];
 #pragma unroll
@@ -997,62 +1077,84 @@ __global__ __launch_bounds__(W *kWave) void a16_small_kernel(MxArgs args) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0, 0, 0, 0};
 
-    for (int line = wave; line < lines; line += W) {
-        const int nb = min(blocks - line * 8, 8);
-        const auto rsb = rsrc(args.SB + (int64_t)line * 8 * args.ldsb + n0, (int)((nb - 1) * args.ldsb) + sb_cols);
-        uint4 fb[2][FN];
-        uint32_t sb[8];
+    auto turn = [&](int step, Slot &slot, Scales &sc) __attribute__((always_inline)) {
+        // this step's copies have landed; those of the S - 1 after it may be in flight
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * kAll) : "memory");
+        uint4 fa[4][FM], fb[FN];
+        const Scales s = sc;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) fb[q][j] = load16(rb, vb[j] + line * 128 + q * 64);
-#pragma unroll
-        for (int b = 0; b < 8; ++b) sb[b] = load_bytes<FN>(rsb, (uint32_t)(b * args.ldsb) + FN * r);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t w[FN][4];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                w[j][0] = fb[q][j].x;
-                w[j][1] = fb[q][j].y;
-                w[j][2] = fb[q][j].z;
-                w[j][3] = fb[q][j].w;
-                transpose_groups(w[j]);
+        for (int j = 0; j < FN; ++j) {
+            if constexpr (T == kBF16) {
+                fb[j] = slot.b[16 * j + r][g ^ ((r >> 2) & 3)];
+            } else {
+                const uint32_t *const row = reinterpret_cast<const uint32_t *>(&slot.b[16 * j + r][0]);
+                fb[j] = make_uint4(row[(0 ^ ((r >> 2) & 3)) * 4 + g], row[(1 ^ ((r >> 2) & 3)) * 4 + g],
+                                   row[(2 ^ ((r >> 2) & 3)) * 4 + g], row[(3 ^ ((r >> 2) & 3)) * 4 + g]);
             }
+        }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                uint4 fa[FM];
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int i = 0; i < FM; ++i) fa[i] = load16(ra, va[i] + line * 512 + (4 * q + t) * 64);
-                if (line * 256 + 256 > K) {
-                    // A's values at and beyond K may be anything, a NaN too: they become zeros
-                    const int n = K - (line * 256 + (4 * q + t) * kBlock + g * 8);
-                    uint32_t m[4];
+            for (int i = 0; i < FM; ++i) fa[u][i] = slot.a[16 * i + r][(T == kBF16 ? 4 * g + u : 4 * u + g) ^ swz_a(r)];
+        // the slot is read: it takes the step after the next S - 1
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        copy(step + S * W, slot, sc);
+        if (step * 128 + 128 > K) {
+            // A's values at and beyond K may be anything, a NaN too: they become zeros (B's codes
+            // beside them are finite, and scales past the last block are zero)
 #pragma unroll
-                    for (int d = 0; d < 4; ++d) m[d] = n >= 2 * d + 2 ? 0xFFFFFFFFu : n == 2 * d + 1 ? 0xFFFFu : 0u;
+            for (int u = 0; u < 4; ++u) {
+                const int n = K - step * 128 - 8 * (T == kBF16 ? 4 * g + u : 4 * u + g);
+                uint32_t m[4];
 #pragma unroll
-                    for (int i = 0; i < FM; ++i) {
-                        fa[i].x &= m[0];
-                        fa[i].y &= m[1];
-                        fa[i].z &= m[2];
-                        fa[i].w &= m[3];
-                    }
-                }
+                for (int d = 0; d < 4; ++d) m[d] = n >= 2 * d + 2 ? 0xFFFFFFFFu : n == 2 * d + 1 ? 0xFFFFu : 0u;
 #pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const uint4 b = widen<T>(w[j][t]);
-                    const float s = scale_or_nan((sb[4 * q + t] >> (8 * j)) & 255u);
-#pragma unroll
-                    for (int i = 0; i < FM; ++i) {
-                        const floatx4_t p = mfma16<T>(fa[i], b);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], s, acc[i][j][e]);
-                    }
+                for (int i = 0; i < FM; ++i) {
+                    uint4 &v = fa[u][i];
+                    v = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
                 }
             }
         }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t w = u == 0 ? fb[j].x : u == 1 ? fb[j].y : u == 2 ? fb[j].z : fb[j].w;
+                const uint32_t byte = (s.v[T == kBF16 ? 0 : u] >> (8 * j)) & 255u;
+                if constexpr (T == kBF16) {
+                    const uint4 b = widen_bf16(w, __builtin_bit_cast(float, byte << 23));
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) acc[i][j] = mfma16<T>(fa[u][i], b, acc[i][j]);
+                } else {
+                    const uint4 b = widen_f16(w);
+                    const float scale = scale_or_nan(byte);
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) {
+                        const floatx4_t p = mfma16<T>(fa[u][i], b, floatx4_t{0, 0, 0, 0});
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], scale, acc[i][j][e]);
+                    }
+                }
+            }
+    };
+    if (wave < steps) {
+        Scales c0, c1, c2;
+        copy(wave, s0[wave], c0);
+        copy(wave + W, s1[wave], c1);
+        if constexpr (S > 2) copy(wave + 2 * W, s2[wave], c2);
+        for (int step = wave; step < steps; step += S * W) {
+            turn(step, s0[wave], c0);
+            if (step + W >= steps) break;
+            turn(step + W, s1[wave], c1);
+            if constexpr (S > 2) {
+                if (step + 2 * W >= steps) break;
+                turn(step + 2 * W, s2[wave], c2);
+            }
+        }
+        // no copy may still be writing this workgroup's LDS when it exits
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    join_and_store<FM, FN, W, OT>(acc, args, m0, n0, tid, lane, wave);
+    join_and_store<FM, FN, W, OT, sizeof(Slot) / 4, false>(acc, reinterpret_cast<float *>(&s0[0]), args, m0, n0, tid, lane, wave);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1080,17 +1182,6 @@ template <> struct A16Map<kF16> {
     static __device__ __forceinline__ int chunk(int u, int g) { return 4 * u + g; }
     static __device__ __forceinline__ int swizzle(int r) { return ((r ^ (r >> 1)) & 1) | ((r >> 2) & 2) | (r & 4); }
 };
-
-// the eight values of a dword of codes times 2^(byte - 127), exact in bf16
-__device__ __forceinline__ uint4 widen_bf16(uint32_t w, float scale) {
-    uint32_t x[4];
-    static_for<4>([&](auto s_c) __attribute__((always_inline)) {
-        constexpr int s = decltype(s_c)::value;
-        const bf16x2_t h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, s);
-        x[s] = __builtin_bit_cast(uint32_t, h);
-    });
-    return make_uint4(x[0], x[1], x[2], x[3]);
-}
 
 template <int T, int BM, int BN, int WM, int WN, int OT>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_kernel(MxArgs args) {
@@ -1221,7 +1312,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
                 // the conversion reads the exponent alone: 0 is 2^-127 and 255 gives NaN
                 b.f[j] = widen_bf16(c.w[j][u], __builtin_bit_cast(float, byte << 23));
             } else {
-                b.f[j] = widen<T>(c.w[j][u]);
+                b.f[j] = widen_f16(c.w[j][u]);
                 b.s[j] = scale_or_nan(byte);
             }
         }
@@ -1239,12 +1330,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
             for (int j = 0; j < FN; ++j) {
                 floatx4_t &c = acc[half * FH + i][j];
                 if constexpr (T == kBF16) {
-                    bf16x8_t x, y;
-                    __builtin_memcpy(&x, &fa[i], 16);
-                    __builtin_memcpy(&y, &b.f[j], 16);
-                    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+                    c = mfma16<T>(fa[i], b.f[j], c);
                 } else {
-                    const floatx4_t p = mfma16<T>(fa[i], b.f[j]);
+                    const floatx4_t p = mfma16<T>(fa[i], b.f[j], floatx4_t{0, 0, 0, 0});
 #pragma unroll
                     for (int e = 0; e < 4; ++e) c[e] = __builtin_fmaf(p[e], b.s[j], c[e]);
                 }
@@ -1438,16 +1526,23 @@ int launch_quant(const QuantArgs &base, void *stream) {
                &args, stream);
 }
 
-template <int FM, int OT>
-const void *mx_small_ptr() {
-    return reinterpret_cast<const void *>(&mx_small_kernel<FM, 2, 8, FM == 4 ? 1 : 2, OT>);
-}
-
-struct MxConfig {
+struct Config {
     int bm, bn, threads;
 };
-constexpr MxConfig kMxConfigs[] = {{256, 256, 512}, {256, 128, 512}, {128, 128, 256}, {16, 32, 512}, {32, 32, 512}, {64, 32, 512}};
+
+constexpr Config kMxConfigs[] = {
+    {256, 256, 512}, {256, 128, 512}, {128, 128, 256},                   // 0-2: tiles
+    {64, 32, 256}, {64, 16, 256},                                        // 3-4: K split over 4 waves
+    {32, 64, 256}, {32, 32, 256}, {32, 16, 256},                         // 5-7
+    {16, 64, 256}, {16, 32, 256}, {16, 16, 256},                         // 8-10
+};
 constexpr int kNumMxConfigs = sizeof(kMxConfigs) / sizeof(kMxConfigs[0]);
+
+template <int C, int OT>
+const void *mx_few_ptr() {
+    constexpr Config c = kMxConfigs[C];
+    return reinterpret_cast<const void *>(&mx_few_kernel<c.bm / 16, c.bn / 16, 4, OT>);
+}
 
 template <int OT>
 const void *mx_ptr(int cfg) {
@@ -1455,27 +1550,42 @@ const void *mx_ptr(int cfg) {
     case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 256, 128, 64, 2, OT>);
     case 1: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 128, 64, 64, 3, OT>);
     case 2: return reinterpret_cast<const void *>(&mx_tile_kernel<128, 128, 64, 64, 2, OT>);
-    case 3: return mx_small_ptr<1, OT>();
-    case 4: return mx_small_ptr<2, OT>();
-    default: return mx_small_ptr<4, OT>();
+    case 3: return mx_few_ptr<3, OT>();
+    case 4: return mx_few_ptr<4, OT>();
+    case 5: return mx_few_ptr<5, OT>();
+    case 6: return mx_few_ptr<6, OT>();
+    case 7: return mx_few_ptr<7, OT>();
+    case 8: return mx_few_ptr<8, OT>();
+    case 9: return mx_few_ptr<9, OT>();
+    default: return mx_few_ptr<10, OT>();
     }
 }
 
-template <int T, int FM, int OT>
-const void *a16_small_ptr() {
-    return reinterpret_cast<const void *>(&a16_small_kernel<T, FM, 2, 8, OT>);
-}
-constexpr MxConfig kA16Configs[] = {{256, 256, 512}, {128, 128, 256}, {16, 32, 512}, {32, 32, 512}, {64, 32, 512}};
+constexpr Config kA16Configs[] = {
+    {256, 256, 512}, {128, 128, 256},                      // 0-1: tiles
+    {64, 32, 256}, {48, 64, 256}, {32, 64, 256},           // 2-4: K split over 4 waves
+    {32, 32, 256}, {16, 64, 256}, {16, 32, 256}, {16, 16, 256},   // 5-8
+};
 constexpr int kNumA16Configs = sizeof(kA16Configs) / sizeof(kA16Configs[0]);
+
+template <int T, int C, int S, int OT>
+const void *a16_few_ptr() {
+    constexpr Config c = kA16Configs[C];
+    return reinterpret_cast<const void *>(&a16_few_kernel<T, c.bm / 16, c.bn / 16, 4, S, OT>);
+}
 
 template <int T, int OT>
 const void *a16_ptr(int cfg) {
     switch (cfg) {
     case 0: return reinterpret_cast<const void *>(&a16_tile_kernel<T, 256, 256, 128, 64, OT>);
     case 1: return reinterpret_cast<const void *>(&a16_tile_kernel<T, 128, 128, 64, 64, OT>);
-    case 2: return a16_small_ptr<T, 1, OT>();
-    case 3: return a16_small_ptr<T, 2, OT>();
-    default: return a16_small_ptr<T, 4, OT>();
+    case 2: return a16_few_ptr<T, 2, 2, OT>();
+    case 3: return a16_few_ptr<T, 3, 2, OT>();
+    case 4: return a16_few_ptr<T, 4, 3, OT>();
+    case 5: return a16_few_ptr<T, 5, 3, OT>();
+    case 6: return a16_few_ptr<T, 6, 3, OT>();
+    case 7: return a16_few_ptr<T, 7, 3, OT>();
+    default: return a16_few_ptr<T, 8, 3, OT>();
     }
 }
 template <int T>
@@ -1484,7 +1594,7 @@ const void *a16_ptr(int cfg, int ot) {
 }
 
 int pick_mx(int64_t M, int64_t N, int64_t K) {
-    return M <= 16 ? 3 : M <= 32 ? 4 : M <= 64 ? 5 : 2;
+    return M <= 16 ? 8 : M <= 32 ? 5 : M <= 64 ? 3 : 2;
 }
 
 int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a,
@@ -1501,7 +1611,7 @@ int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_
     if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(B, ldb, scale_b, ldsb);
     if (rc != PDGEMM_OK) return rc;
     if (cfg < 0) cfg = pick_mx(M, N, K);
-    const MxConfig &c = kMxConfigs[cfg];
+    const Config &c = kMxConfigs[cfg];
     // with K = 0 no operand is read: the kernels form addresses from C instead
     const uint8_t *const p = static_cast<const uint8_t *>(C);
     MxArgs args = {K ? A : p, K ? scale_a : p, K ? B : p, K ? scale_b : p, C, K ? lda / 2 : 0, K ? ldb / 2 : 0,
@@ -1511,7 +1621,7 @@ int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_
 }
 
 int pick_a16(int64_t M, int64_t N, int64_t K) {
-    return M <= 16 ? 2 : M <= 32 ? 3 : M <= 64 ? 4 : cdiv(M, 256) * cdiv(N, 256) >= 192 ? 0 : 1;
+    return M <= 16 ? 6 : M <= 32 ? 4 : M <= 64 ? 2 : cdiv(M, 256) * cdiv(N, 256) >= 192 ? 0 : 1;
 }
 
 int launch_a16(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
@@ -1528,7 +1638,7 @@ int launch_a16(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t 
     if (rc == PDGEMM_OK && K > 0 && (lda % 8 || ((uintptr_t)A & 15))) rc = PDGEMM_EALIGN;
     if (rc != PDGEMM_OK) return rc;
     if (cfg < 0) cfg = pick_a16(M, N, K);
-    const MxConfig &c = kA16Configs[cfg];
+    const Config &c = kA16Configs[cfg];
     const uint8_t *const p = static_cast<const uint8_t *>(C);
     MxArgs args = {K ? static_cast<const uint8_t *>(A) : p, nullptr, K ? B : p, K ? scale_b : p, C, K ? 2 * lda : 0,
                    K ? ldb / 2 : 0, 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, c.bm), (int)cdiv(N, c.bn)};

@@ -438,8 +438,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int range)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, range, kRsrcWord3);
 }
 
-// byte offset of a tile's row: a row spans at most 4 MiB and a tile 256 rows
-__device__ __forceinline__ uint32_t row_offset(int row, int64_t ld) { return (uint32_t)row * (uint32_t)ld; }
+// Byte offset of row `row` of a tile (a row spans at most 4 MiB and a tile 256 rows) that
+// has `rows` rows; rows past them get an offset outside every range, so that zeros arrive and
+// no memory is read.
+constexpr uint32_t kOutside = 0x80000000u;
+__device__ __forceinline__ uint32_t row_offset(int row, int rows, int64_t ld) {
+    return row < rows ? (uint32_t)row * (uint32_t)ld : kOutside;
+}
 
 __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     const uintx4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
@@ -474,13 +479,13 @@ __device__ __forceinline__ void static_for(F &&f) {
 // Sum of the waves' partial tiles (each wave summed its own range of K) in wave order,
 // rounded once to C's type and stored.  acc[i][j] of a wave holds, in register e of lane
 // l, row FM * (4 (l / 16) + e) + i (with kMixed; else 16 i + 4 (l / 16) + e) and column
-// FN * (l % 16) + j of the tile.  `part` is LDS of kStride floats per wave, each wave's part
-// free for it to write.
-template <int FM, int FN, int W, int OT, int kStride, bool kMixed>
+// FN * (l % 16) + j of the tile, of which BM rows are stored.  `part` is LDS of kStride floats
+// per wave, each wave's part free for it to write.
+template <int FM, int FN, int W, int OT, int kStride, int BM, bool kMixed>
 __device__ __forceinline__ void join_and_store(floatx4_t (&acc)[FM][FN], float *part, const MxArgs &args, int m0, int n0,
                                                int tid, int lane, int wave) {
     using Out = typename ElemOf<OT>::type;
-    constexpr int BM = 16 * FM, BN = 16 * FN;
+    constexpr int BN = 16 * FN;
     static_assert(kStride >= FM * FN * 4 * kWave, "a wave's partial tile");
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -601,7 +606,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
     const int sa_cols = min(((M + 15) & ~15) - m0, BM), sb_cols = min(((N + 15) & ~15) - n0, BN);
 
     // copy j of this wave fills LDS rows (j NW + wave) 8 .. + 7, lane l chunk position l % 8
-    // of row l / 8; rows of the tile past M (N) repeat the last one, not stored
+    // of row l / 8
     uint32_t voff[kDma];
 #pragma unroll
     for (int j = 0; j < kDma; ++j) {
@@ -609,11 +614,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
         const int chunk = (lane & 7) ^ swizzle8(cr);
         if (j < kDmaA) {
             const int row = cr / WM * WM + FM * (cr % 32) + cr % WM / 32;
-            voff[j] = row_offset(min(m0 + row, M - 1) - m0, args.lda) + chunk * 16;
+            voff[j] = row_offset(row, M - m0, args.lda) + chunk * 16;
         } else {
             const int cb = cr - BM;
             const int row = cb / WN * WN + FN * (cb % 32) + cb % WN / 32;
-            voff[j] = row_offset(min(n0 + row, N - 1) - n0, args.ldb) + chunk * 16;
+            voff[j] = row_offset(row, N - n0, args.ldb) + chunk * 16;
         }
     }
     // scale copy `wave`, 16 rows of one block per lane.  The waves beyond copy nothing (an
@@ -862,9 +867,9 @@ __global__ __launch_bounds__(W *kWave) void mx_few_kernel(MxArgs args) {
         const int cr = j * 8 + (lane >> 3);
         const int chunk = (lane & 7) ^ swizzle16(cr);
         if (j < BM / 8)
-            voff[j] = row_offset(min(m0 + FM * (cr % 16) + cr / 16, M - 1) - m0, args.lda) + chunk * 16;
+            voff[j] = row_offset(FM * (cr % 16) + cr / 16, M - m0, args.lda) + chunk * 16;
         else
-            voff[j] = row_offset(min(n0 + FN * ((cr - BM) % 16) + (cr - BM) / 16, N - 1) - n0, args.ldb) + chunk * 16;
+            voff[j] = row_offset(FN * ((cr - BM) % 16) + (cr - BM) / 16, N - n0, args.ldb) + chunk * 16;
     }
     // a block's scales are read up to the 16-byte granule that holds the last row's
     const int sa_cols = min(((M + 15) & ~15) - m0, BM), sb_cols = min(((N + 15) & ~15) - n0, BN);
@@ -952,7 +957,7 @@ __global__ __launch_bounds__(W *kWave) void mx_few_kernel(MxArgs args) {
         // no copy may still be writing this workgroup's LDS when it exits
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    join_and_store<FM, FN, W, OT, sizeof(Slot) / 4, true>(acc, reinterpret_cast<float *>(&s0[0]), args, m0, n0, tid, lane, wave);
+    join_and_store<FM, FN, W, OT, sizeof(Slot) / 4, BM, true>(acc, reinterpret_cast<float *>(&s0[0]), args, m0, n0, tid, lane, wave);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1001,74 +1006,90 @@ __device__ __forceinline__ float scale_or_nan(uint32_t byte) {
     return byte == 255 ? __builtin_nanf("") : scale_value(byte);
 }
 
-// Few rows of 16-bit activations: the scheme of mx_few_kernel in steps of 128 values of K,
-// 256 bytes (two lines) of a row of A and half a line of B; neighbouring waves take the two
-// halves of a line.  The operands' maps are those of the tile kernel below, with the step's
-// four blocks in place of two halves: bf16, lane group g holds block g, scaled as it is
-// widened, and MFMA u its values 8 u .. + 7; f16, MFMA u covers block u, of which group g
-// holds dword g, and its result is scaled as it is added.
-template <int T, int FM, int FN, int W, int S, int OT>
+// How a step of 64 values of K (a line of a row of A, two blocks of B) is shared out over the
+// four lane groups g = l / 16 of two MFMAs u.
+//
+// bf16: its exponents reach the weights' (a code times 2^(byte - 127) is exact, subnormals
+// included, which the MFMA keeps), so the scale goes into the operand: group g takes half a
+// block, values 16 g .. + 15 of the step, and MFMA u its values 8 u .. + 7.
+// f16: group g takes dword g of a block, MFMA u covers block u alone, and its result is scaled
+// as it is added: 4 vector instructions per MFMA, as many cycles as it takes itself.
+template <int T> struct A16Map;
+template <> struct A16Map<kBF16> {
+    static __device__ __forceinline__ int chunk(int u, int g) { return 2 * g + u; }       // of A's 8
+    static __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 3; }
+};
+template <> struct A16Map<kF16> {
+    static __device__ __forceinline__ int chunk(int u, int g) { return 4 * u + g; }
+    static __device__ __forceinline__ int swizzle(int r) { return ((r ^ (r >> 1)) & 1) | ((r >> 2) & 2) | (r & 4); }
+};
+
+// Few rows of 16-bit activations: the scheme of mx_few_kernel in steps of a line of A, W
+// waves with S slots each (as many as LDS holds: what is on its way bounds the rate), so W
+// neighbouring waves share a line of B.  RA: the rows of A that are staged; with eight
+// (M <= 8) a fragment's rows repeat them and LDS holds more steps.
+template <int T, int RA, int FN, int W, int S, int OT>
 __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int BM = 16 * FM, BN = 16 * FN;
-    constexpr int kDmaA = BM / 4, kDmaB = BN / 16;      // copies of 1 KB (4 rows of A, 16 of B) per step
-    constexpr int kSc = T == kBF16 ? 1 : 4;             // loads of scales per step
+    using Map = A16Map<T>;
+    constexpr int FM = (RA + 15) / 16, BN = 16 * FN;
+    constexpr int kDmaA = RA / 8, kDmaB = (BN + 31) / 32;   // copies of 1 KB (8 rows of A, 32 of B) per step
+    constexpr int kSc = T == kBF16 ? 1 : 2;                 // loads of scales per step
     constexpr int kAll = kDmaA + kDmaB + kSc;
-    static_assert(S == 2 || S == 3, "slots per wave");
-    static_assert((S - 1) * kAll <= 63, "vmcnt holds at most 63 outstanding loads");
+    static_assert(RA == 8 || RA % 16 == 0, "rows of A");
+    static_assert(S >= 2 && S <= 6 && (S - 1) * kAll <= 63, "vmcnt holds at most 63 outstanding loads");
     struct Slot {
-        uint4 a[BM][16];   // chunk c of row r at c ^ swz_a(r)
-        uint4 b[BN][4];    // chunk c of row r at c ^ ((r / 4) % 4)
+        uint4 a[RA][8];             // chunk c of row r at c ^ Map::swizzle(r)
+        uint4 b[32 * kDmaB][2];     // chunk c of row r at c ^ ((r / 8) % 2)
     };
     struct Scales {
         uint32_t v[kSc];
     };
+    // separate objects: a read of one slot does not wait for the copies into the others
     __shared__ Slot s0[W], s1[W];
     __shared__ typename std::conditional<(S > 2), Slot, char>::type s2[S > 2 ? W : 1];
+    __shared__ typename std::conditional<(S > 3), Slot, char>::type s3[S > 3 ? W : 1];
+    __shared__ typename std::conditional<(S > 4), Slot, char>::type s4[S > 4 ? W : 1];
+    __shared__ typename std::conditional<(S > 5), Slot, char>::type s5[S > 5 ? W : 1];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane & 15, g = lane >> 4;
-    const int m0 = (blockIdx.x / args.tiles_n) * BM, n0 = (blockIdx.x % args.tiles_n) * BN;
+    const int m0 = (blockIdx.x / args.tiles_n) * RA, n0 = (blockIdx.x % args.tiles_n) * BN;
     const int M = args.M, N = args.N, K = args.K;
     const int blocks = (K + kBlock - 1) / kBlock;
-    const int steps = (blocks + 3) / 4;
+    const int steps = (blocks + 1) / 2;
 
     const uint8_t *const a_base = args.A + (int64_t)m0 * args.lda;
     const uint8_t *const b_base = args.B + (int64_t)n0 * args.ldb;
-    const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15);
+    const int a_end = (int)((min(RA, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15);
     const int b_end = (int)((min(BN, N - n0) - 1) * args.ldb) + blocks * 16;
     const int sb_cols = min(((N + 15) & ~15) - n0, BN), ldsb = (int)args.ldsb;
-    // positions of 256-byte rows are bank groups, and a phase of a read takes 8 rows at chunk c
-    // and at c ^ 8 (bf16) or c ^ 2 (f16): the 8 rows' terms differ outside that bit
-    auto swz_a = [](int row) __attribute__((always_inline)) {
-        return T == kBF16 ? row & 7 : (row & 1) | ((row & 6) << 1);
-    };
     uint32_t va[kDmaA], vb[kDmaB];
 #pragma unroll
     for (int j = 0; j < kDmaA; ++j) {
-        const int cr = j * 4 + (lane >> 4);
-        va[j] = row_offset(min(m0 + cr, M - 1) - m0, args.lda) + ((lane & 15) ^ swz_a(cr)) * 16;
+        const int cr = j * 8 + (lane >> 3);
+        va[j] = row_offset(cr, M - m0, args.lda) + ((lane & 7) ^ Map::swizzle(cr)) * 16;
     }
 #pragma unroll
     for (int j = 0; j < kDmaB; ++j) {
-        const int cr = lane >> 2;   // column FN n + j at LDS row 16 j + n
-        vb[j] = row_offset(min(n0 + FN * cr + j, N - 1) - n0, args.ldb) + ((lane & 3) ^ ((cr >> 2) & 3)) * 16;
+        const int cr = j * 32 + (lane >> 1);   // column FN n + j at LDS row 16 j + n
+        vb[j] = row_offset(FN * (cr % 16) + cr / 16, cr < BN ? N - n0 : 0, args.ldb) + ((lane & 1) ^ ((cr >> 3) & 1)) * 16;
     }
     // a step past K reads nothing: zeros arrive
     auto copy = [&](int step, Slot &slot, Scales &sc) __attribute__((always_inline)) {
-        const int nb = min(blocks - step * 4, 4);
-        const auto ra = rsrc(a_base + step * 256, nb > 0 ? a_end - step * 256 : 0);
-        const auto rb = rsrc(b_base + step * 64, nb > 0 ? b_end - step * 64 : 0);
-        const auto rs = rsrc(args.SB + (int64_t)step * 4 * args.ldsb + n0, max((nb - 1) * ldsb + sb_cols, 0));
+        const int nb = min(blocks - step * 2, 2);
+        const auto ra = rsrc(a_base + step * 128, nb > 0 ? a_end - step * 128 : 0);
+        const auto rb = rsrc(b_base + step * 32, nb > 0 ? b_end - step * 32 : 0);
+        const auto rs = rsrc(args.SB + (int64_t)step * 2 * args.ldsb + n0, max((nb - 1) * ldsb + sb_cols, 0));
 #pragma unroll
         for (int j = 0; j < kDmaB; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_PTR(&slot.b[j * 16][0]), 16, vb[j], 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_PTR(&slot.b[j * 32][0]), 16, vb[j], 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < kDmaA; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_PTR(&slot.a[j * 4][0]), 16, va[j], 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_PTR(&slot.a[j * 8][0]), 16, va[j], 0, 0, 0);
 #pragma unroll
-        for (int u = 0; u < kSc; ++u) sc.v[u] = load_bytes<FN>(rs, (T == kBF16 ? g : u) * ldsb + FN * r);
+        for (int u = 0; u < kSc; ++u) sc.v[u] = load_bytes<FN>(rs, (T == kBF16 ? g >> 1 : u) * ldsb + FN * r);
     };
 
     floatx4_t acc[FM][FN];
@@ -1080,31 +1101,45 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
     auto turn = [&](int step, Slot &slot, Scales &sc) __attribute__((always_inline)) {
         // this step's copies have landed; those of the S - 1 after it may be in flight
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * kAll) : "memory");
-        uint4 fa[4][FM], fb[FN];
-        const Scales s = sc;
+        uint4 fa[2][FM];
+        uint32_t w[FN][2];
+        const int ra = RA == 8 ? r & 7 : r, flip = (r >> 3) & 1;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
+            const uint32_t *const row = reinterpret_cast<const uint32_t *>(&slot.b[16 * j + r][0]);
             if constexpr (T == kBF16) {
-                fb[j] = slot.b[16 * j + r][g ^ ((r >> 2) & 3)];
+                w[j][0] = row[((g >> 1) ^ flip) * 4 + 2 * (g & 1)];
+                w[j][1] = row[((g >> 1) ^ flip) * 4 + 2 * (g & 1) + 1];
             } else {
-                const uint32_t *const row = reinterpret_cast<const uint32_t *>(&slot.b[16 * j + r][0]);
-                fb[j] = make_uint4(row[(0 ^ ((r >> 2) & 3)) * 4 + g], row[(1 ^ ((r >> 2) & 3)) * 4 + g],
-                                   row[(2 ^ ((r >> 2) & 3)) * 4 + g], row[(3 ^ ((r >> 2) & 3)) * 4 + g]);
+                w[j][0] = row[flip * 4 + g];
+                w[j][1] = row[(1 ^ flip) * 4 + g];
             }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < FM; ++i) fa[u][i] = slot.a[16 * i + r][(T == kBF16 ? 4 * g + u : 4 * u + g) ^ swz_a(r)];
+            for (int i = 0; i < FM; ++i) fa[u][i] = slot.a[16 * i + ra][Map::chunk(u, g) ^ Map::swizzle(ra)];
+        // (the scales leave the registers that the copy loads into, or the compiler would load
+        // into others and wait at once to move them)
+        float scale[kSc][FN];
+#pragma unroll
+        for (int u = 0; u < kSc; ++u)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const uint32_t byte = (sc.v[u] >> (8 * j)) & 255u;
+                // (the conversion of bf16 reads the exponent alone: 0 is 2^-127 and 255 gives NaN)
+                scale[u][j] = T == kBF16 ? __builtin_bit_cast(float, byte << 23) : scale_or_nan(byte);
+                asm volatile("" : "+v"(scale[u][j]));
+            }
         // the slot is read: it takes the step after the next S - 1
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         copy(step + S * W, slot, sc);
-        if (step * 128 + 128 > K) {
+        if (step * 64 + 64 > K) {
             // A's values at and beyond K may be anything, a NaN too: they become zeros (B's codes
             // beside them are finite, and scales past the last block are zero)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int n = K - step * 128 - 8 * (T == kBF16 ? 4 * g + u : 4 * u + g);
+            for (int u = 0; u < 2; ++u) {
+                const int n = K - step * 64 - 8 * Map::chunk(u, g);
                 uint32_t m[4];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) m[d] = n >= 2 * d + 2 ? 0xFFFFFFFFu : n == 2 * d + 1 ? 0xFFFFu : 0u;
@@ -1118,30 +1153,30 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t w = u == 0 ? fb[j].x : u == 1 ? fb[j].y : u == 2 ? fb[j].z : fb[j].w;
-                const uint32_t byte = (s.v[T == kBF16 ? 0 : u] >> (8 * j)) & 255u;
+            for (int u = 0; u < 2; ++u) {
                 if constexpr (T == kBF16) {
-                    const uint4 b = widen_bf16(w, __builtin_bit_cast(float, byte << 23));
+                    const uint4 b = widen_bf16(w[j][u], scale[0][j]);
 #pragma unroll
                     for (int i = 0; i < FM; ++i) acc[i][j] = mfma16<T>(fa[u][i], b, acc[i][j]);
                 } else {
-                    const uint4 b = widen_f16(w);
-                    const float scale = scale_or_nan(byte);
+                    const uint4 b = widen_f16(w[j][u]);
 #pragma unroll
                     for (int i = 0; i < FM; ++i) {
                         const floatx4_t p = mfma16<T>(fa[u][i], b, floatx4_t{0, 0, 0, 0});
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], scale, acc[i][j][e]);
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], scale[u][j], acc[i][j][e]);
                     }
                 }
             }
     };
     if (wave < steps) {
-        Scales c0, c1, c2;
+        Scales c0, c1, c2, c3, c4, c5;
         copy(wave, s0[wave], c0);
         copy(wave + W, s1[wave], c1);
         if constexpr (S > 2) copy(wave + 2 * W, s2[wave], c2);
+        if constexpr (S > 3) copy(wave + 3 * W, s3[wave], c3);
+        if constexpr (S > 4) copy(wave + 4 * W, s4[wave], c4);
+        if constexpr (S > 5) copy(wave + 5 * W, s5[wave], c5);
         for (int step = wave; step < steps; step += S * W) {
             turn(step, s0[wave], c0);
             if (step + W >= steps) break;
@@ -1150,11 +1185,27 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
                 if (step + 2 * W >= steps) break;
                 turn(step + 2 * W, s2[wave], c2);
             }
+            if constexpr (S > 3) {
+                if (step + 3 * W >= steps) break;
+                turn(step + 3 * W, s3[wave], c3);
+            }
+            if constexpr (S > 4) {
+                if (step + 4 * W >= steps) break;
+                turn(step + 4 * W, s4[wave], c4);
+            }
+            if constexpr (S > 5) {
+                if (step + 5 * W >= steps) break;
+                turn(step + 5 * W, s5[wave], c5);
+            }
         }
         // no copy may still be writing this workgroup's LDS when it exits
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    join_and_store<FM, FN, W, OT, sizeof(Slot) / 4, false>(acc, reinterpret_cast<float *>(&s0[0]), args, m0, n0, tid, lane, wave);
+    // a wave's partial tile takes its first slot where that is large enough
+    constexpr bool kFits = sizeof(Slot) >= FM * FN * 1024;
+    __shared__ float part[kFits ? 1 : W * FM * FN * 256];
+    join_and_store<FM, FN, W, OT, kFits ? sizeof(Slot) / 4 : FM * FN * 256, RA, false>(
+        acc, kFits ? reinterpret_cast<float *>(&s0[0]) : part, args, m0, n0, tid, lane, wave);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1164,25 +1215,8 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 // serves four steps of A and is copied a quarter per step.  The codes become the 16-bit
 // type in registers, once per wave and step.
 //
-// bf16: its exponents reach the weights' (a code times 2^(byte - 127) is exact, subnormals
-// included, which the MFMA keeps), so the scale goes into the operand: lane group g = l / 16
-// takes half a block, values 16 g .. + 15 of the step, and MFMA u its values 8 u .. + 7.
-// f16: group g takes dword g of a block, the MFMA covers one block and its result is scaled
-// as it is added (see mfma16 above): 4 vector instructions per MFMA, as many cycles as it
-// takes itself.
-//
 // Fragment j holds columns FN n + j (n = l % 16) of the wave's, so a lane's scales of its
 // fragments are one dword and its results neighbouring columns of C.
-template <int T> struct A16Map;
-template <> struct A16Map<kBF16> {
-    static __device__ __forceinline__ int chunk(int u, int g) { return 2 * g + u; }       // of A's 8
-    static __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 3; }
-};
-template <> struct A16Map<kF16> {
-    static __device__ __forceinline__ int chunk(int u, int g) { return 4 * u + g; }
-    static __device__ __forceinline__ int swizzle(int r) { return ((r ^ (r >> 1)) & 1) | ((r >> 2) & 2) | (r & 4); }
-};
-
 template <int T, int BM, int BN, int WM, int WN, int OT>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1226,13 +1260,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
 #pragma unroll
     for (int j = 0; j < kDmaA; ++j) {
         const int cr = (j * NW + wave) * 8 + (lane >> 3);
-        va[j] = row_offset(min(m0 + cr, M - 1) - m0, args.lda) + a_chunk;
+        va[j] = row_offset(cr, M - m0, args.lda) + a_chunk;
     }
 #pragma unroll
     for (int j = 0; j < 4 * kDmaB; ++j) {
         const int cr = (j * NW + wave) * 8 + (lane >> 3);
         const int col = cr / WN * WN + FN * (cr % 16) + cr % WN / 16;   // column FN n + j at LDS row 16 j + n
-        vb[j] = row_offset(min(n0 + col, N - 1) - n0, args.ldb) + ((lane & 7) ^ swizzle8(cr)) * 16;
+        vb[j] = row_offset(col, N - n0, args.ldb) + ((lane & 7) ^ swizzle8(cr)) * 16;
     }
     const bool sc_none = wave >= kSc;
     const int sd = wave * 64 + lane;
@@ -1246,7 +1280,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         const auto ra = rsrc(a_base + kb, max(a_end - kb, 0));
 #pragma unroll
         for (int j = 0; j < kDmaA; ++j) {
-            const uint32_t off = kb + a_chunk < whole16 ? va[j] : 0x80000000u;
+            const uint32_t off = kb + a_chunk < whole16 ? va[j] : kOutside;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_PTR(&buf[(j * NW + wave) * 8][0]), 16, off, 0, 0, 0);
         }
     };
@@ -1284,9 +1318,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         for (int j = 0; j < FN; ++j) {
             const uint32_t *const row = reinterpret_cast<const uint32_t *>(&buf.rows[wn0 + j * 16 + r][0]);
             if constexpr (T == kBF16) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(&row[((2 * t + (g >> 1)) ^ swizzle8(r)) * 4 + 2 * (g & 1)]);
-                c.w[j][0] = v.x;
-                c.w[j][1] = v.y;
+                const uint32_t *const half = &row[((2 * t + (g >> 1)) ^ swizzle8(r)) * 4 + 2 * (g & 1)];
+                c.w[j][0] = half[0];
+                c.w[j][1] = half[1];
             } else {
                 c.w[j][0] = row[((2 * t) ^ swizzle8(r)) * 4 + g];
                 c.w[j][1] = row[((2 * t + 1) ^ swizzle8(r)) * 4 + g];
@@ -1350,7 +1384,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         const uint32_t sc = load_bytes<4>(rs, wn0 + FN * r);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            c.w[j][0] = load_bytes<4>(rb, row_offset(min(n0 + wn0 + FN * r + j, N - 1) - n0, args.ldb) + kt / 2);
+            c.w[j][0] = load_bytes<4>(rb, row_offset(wn0 + FN * r + j, N - n0, args.ldb) + kt / 2);
         c.s[0] = sc;
         make_b(c, 0, b);
 #pragma unroll
@@ -1358,7 +1392,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
 #pragma unroll
             for (int i = 0; i < FH; ++i) {
                 const int row = wm0 + (half * FH + i) * 16 + r;
-                uint4 v = load16(ra, g == 0 ? row_offset(min(m0 + row, M - 1) - m0, args.lda) + 2 * kt : 0x80000000u);
+                uint4 v = load16(ra, g == 0 ? row_offset(row, M - m0, args.lda) + 2 * kt : kOutside);
                 uint32_t m[4];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) m[d] = K % 8 >= 2 * d + 2 ? 0xFFFFFFFFu : K % 8 == 2 * d + 1 ? 0xFFFFu : 0u;
@@ -1562,16 +1596,18 @@ const void *mx_ptr(int cfg) {
 }
 
 constexpr Config kA16Configs[] = {
-    {256, 256, 512}, {128, 128, 256},                      // 0-1: tiles
-    {64, 32, 256}, {48, 64, 256}, {32, 64, 256},           // 2-4: K split over 4 waves
-    {32, 32, 256}, {16, 64, 256}, {16, 32, 256}, {16, 16, 256},   // 5-8
+    {256, 256, 512}, {128, 128, 256},                         // 0-1: tiles
+    {64, 32, 256}, {48, 32, 256},                             // 2-3: K split over the waves
+    {32, 64, 256}, {32, 32, 512},                             // 4-5
+    {16, 64, 512}, {16, 32, 512}, {16, 16, 512},              // 6-8
+    {8, 64, 512}, {8, 32, 512}, {8, 16, 512},                 // 9-11
 };
 constexpr int kNumA16Configs = sizeof(kA16Configs) / sizeof(kA16Configs[0]);
 
 template <int T, int C, int S, int OT>
 const void *a16_few_ptr() {
     constexpr Config c = kA16Configs[C];
-    return reinterpret_cast<const void *>(&a16_few_kernel<T, c.bm / 16, c.bn / 16, 4, S, OT>);
+    return reinterpret_cast<const void *>(&a16_few_kernel<T, c.bm, c.bn / 16, c.threads / 64, S, OT>);
 }
 
 template <int T, int OT>
@@ -1579,13 +1615,16 @@ const void *a16_ptr(int cfg) {
     switch (cfg) {
     case 0: return reinterpret_cast<const void *>(&a16_tile_kernel<T, 256, 256, 128, 64, OT>);
     case 1: return reinterpret_cast<const void *>(&a16_tile_kernel<T, 128, 128, 64, 64, OT>);
-    case 2: return a16_few_ptr<T, 2, 2, OT>();
-    case 3: return a16_few_ptr<T, 3, 2, OT>();
-    case 4: return a16_few_ptr<T, 4, 3, OT>();
+    case 2: return a16_few_ptr<T, 2, 4, OT>();
+    case 3: return a16_few_ptr<T, 3, 5, OT>();
+    case 4: return a16_few_ptr<T, 4, 5, OT>();
     case 5: return a16_few_ptr<T, 5, 3, OT>();
-    case 6: return a16_few_ptr<T, 6, 3, OT>();
-    case 7: return a16_few_ptr<T, 7, 3, OT>();
-    default: return a16_few_ptr<T, 8, 3, OT>();
+    case 6: return a16_few_ptr<T, 6, 4, OT>();
+    case 7: return a16_few_ptr<T, 7, 5, OT>();
+    case 8: return a16_few_ptr<T, 8, 5, OT>();
+    case 9: return a16_few_ptr<T, 9, 5, OT>();
+    case 10: return a16_few_ptr<T, 10, 5, OT>();
+    default: return a16_few_ptr<T, 11, 5, OT>();
     }
 }
 template <int T>

@@ -378,7 +378,7 @@ def test_a16(pd, dev, shape, kind, a_kind):
 
 
 @pytest.mark.parametrize("a_kind", ["f16", "bf16"])
-@pytest.mark.parametrize("cfg", range(9))
+@pytest.mark.parametrize("cfg", range(12))
 @pytest.mark.parametrize("shape", TILE_SHAPES, ids=[f"{m}x{n}x{k}" for m, n, k in TILE_SHAPES])
 def test_a16_every_tile(pd, dev, shape, cfg, a_kind):
     M, N, K = shape

@@ -443,7 +443,7 @@ int pdgemm_a16_mxf4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A,
                         const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc,
                         int out_type, void *stream);
 int pdgemm_a16_mxf4_num_configs(void);
-int pdgemm_a16_mxf4_pick(int64_t M, int64_t N, int64_t K);
+int pdgemm_a16_mxf4_pick(int a_type, int64_t M, int64_t N, int64_t K);   /* -1 for another type */
 
 /* Static message for a return code (never NULL): the PDGEMM_E* codes above,
  * or hipGetErrorString() for a positive hipError_t.  Part of the error

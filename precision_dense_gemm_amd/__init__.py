@@ -129,7 +129,7 @@ lib.pdgemm_a16_mxf4_cfg.argtypes = [_i] + lib.gemm_a16_mxf4.argtypes
 lib.pdgemm_a16_mxf4_cfg.restype = _i
 lib.pdgemm_a16_mxf4_num_configs.argtypes = []
 lib.pdgemm_a16_mxf4_num_configs.restype = _i
-lib.pdgemm_a16_mxf4_pick.argtypes = [_i64, _i64, _i64]
+lib.pdgemm_a16_mxf4_pick.argtypes = [_i, _i64, _i64, _i64]
 lib.pdgemm_a16_mxf4_pick.restype = _i
 lib.pdgemm_strerror.argtypes = [_i]
 lib.pdgemm_strerror.restype = ctypes.c_char_p
@@ -778,9 +778,9 @@ def a16_mxf4_num_configs() -> int:
     return lib.pdgemm_a16_mxf4_num_configs()
 
 
-def a16_mxf4_pick(M: int, N: int, K: int) -> int:
-    """The tile configuration gemm_a16_mxf4 takes for a shape."""
-    return lib.pdgemm_a16_mxf4_pick(M, N, K)
+def a16_mxf4_pick(dtype: torch.dtype, M: int, N: int, K: int) -> int:
+    """The tile configuration gemm_a16_mxf4 takes for activations of `dtype` and a shape."""
+    return lib.pdgemm_a16_mxf4_pick(_MX_TYPES[dtype], M, N, K)
 
 
 def prepare(prec: str, A: torch.Tensor, Bt: torch.Tensor, out: torch.Tensor, K: int | None = None,

@@ -560,13 +560,13 @@ __device__ __forceinline__ int swizzle8(int r) { return (r & 7) ^ ((r >> 3) & 1)
 // 6.5 PFLOP/s, of the 16 x 16 form at 5.9).
 //
 // A stage is one 128-byte line (256 values) of K of the tile's BM rows of A and BN of B,
-// copied from memory straight into LDS, LS stages deep, and its scales.  Fragment i of a
+// copied from memory straight into LDS, two stages deep, and its scales.  Fragment i of a
 // wave holds rows FM r + i (r = 0 .. 31) of the wave's WM rows, which the copy places at
 // LDS rows 32 i + r: so a lane's scales of its FM fragments are neighbouring bytes of a
 // dword, which one MFMA operand register takes whole (the instruction picks the byte), and
 // a lane's results of FN fragments are neighbouring columns of C, stored together.  A
 // stage's scales are copied by the first waves, 16 rows of a block per lane.
-template <int BM, int BN, int WM, int WN, int LS, int OT>
+template <int BM, int BN, int WM, int WN, int OT>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using Out = typename ElemOf<OT>::type;
@@ -581,13 +581,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "a stage's rows split evenly over the waves");
     static_assert(BM % 128 == 0 && BN % 128 == 0 && kSc <= NW, "a wave copies scales of one operand");
     static_assert((FM == 1 || FM == 2 || FM == 4) && (FN == 1 || FN == 2 || FN == 4), "scales of a lane in one dword");
-    static_assert((LS - 1) * kAll <= 63, "vmcnt holds at most 63 outstanding loads");
     struct Stage {
         uint4 rows[kRows][8];
         uint4 sc[kRows / 2 + 64];   // bytes: [A: 8 blocks of BM rows | B: 8 blocks of BN rows | unused]
     };
     __shared__ Stage l0, l1;
-    __shared__ typename std::conditional<(LS > 2), Stage, char>::type l2;
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -705,7 +703,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
     uint4 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
     uint32_t sa[4], sb[4], sa_next[4], sb_next[4];
     // stage st (not the last) from `cur`, whose k-step 0 is in fa0 / fb0 and scales in sa / sb;
-    // refills `cur` with stage st + LS and reads the same of stage st + 1 from `nxt`
+    // refills `cur` with stage st + 2 and reads the same of stage st + 1 from `nxt`
     auto full_stage = [&](Stage &cur, const Stage &nxt, int st) __attribute__((always_inline)) {
         read_frags(cur, 1, fa1, fb1);
         mma(fa0, fb0, sa[0], sb[0]);
@@ -716,10 +714,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
         read_frags(cur, 3, fa1, fb1);
         mma(fa0, fb0, sa[2], sb[2]);
         interleave(kFrags{}, kNone{});
-        // this wave's copies of stage st + 1 have landed (later ones may be in flight) and its
-        // reads of `cur` are done; after the barrier the same holds for every wave
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((LS - 2) * kAll) : "memory");
-        stage(st + LS, cur);
+        // this wave's copies of stage st + 1 have landed and its reads of `cur` are done; after
+        // the barrier the same holds for every wave
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        stage(st + 2, cur);
         read_scales(nxt, sa_next, sb_next);
         read_frags(nxt, 0, fa0, fb0);
         mma(fa1, fb1, sa[3], sb[3]);
@@ -760,31 +758,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
     if (n_st > 0) {
         stage(0, l0);
         stage(1, l1);
-        if constexpr (LS > 2) stage(2, l2);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((LS - 1) * kAll) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kAll) : "memory");
         read_frags(l0, 0, fa0, fb0);
         read_scales(l0, sa, sb);
         int st = 0;
-        if constexpr (LS == 2) {
-            for (; st + 2 < n_st; st += 2) {
-                full_stage(l0, l1, st);
-                full_stage(l1, l0, st + 1);
-            }
-            if (st + 1 < n_st) full_stage(l0, l1, st++);
-            last_stage((st & 1) ? l1 : l0, st);
-        } else {
-            for (; st + 3 < n_st; st += 3) {
-                full_stage(l0, l1, st);
-                full_stage(l1, l2, st + 1);
-                full_stage(l2, l0, st + 2);
-            }
-            if (st + 1 < n_st) {
-                full_stage(l0, l1, st++);
-                if (st + 1 < n_st) full_stage(l1, l2, st++);
-            }
-            const int q = st % 3;
-            last_stage(q == 0 ? l0 : q == 1 ? l1 : l2, st);
+        for (; st + 2 < n_st; st += 2) {
+            full_stage(l0, l1, st);
+            full_stage(l1, l0, st + 1);
         }
+        if (st + 1 < n_st) full_stage(l0, l1, st++);
+        last_stage((st & 1) ? l1 : l0, st);
         // no copy may still be writing this workgroup's LDS when it exits
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
@@ -1565,42 +1548,41 @@ struct Config {
 };
 
 constexpr Config kMxConfigs[] = {
-    {256, 256, 512}, {256, 128, 512}, {128, 128, 256},                   // 0-2: tiles
-    {64, 32, 256}, {64, 16, 256},                                        // 3-4: K split over 4 waves
-    {32, 64, 256}, {32, 32, 256}, {32, 16, 256},                         // 5-7
-    {16, 64, 256}, {16, 32, 256}, {16, 16, 256},                         // 8-10
+    {256, 256, 512}, {128, 128, 256},                // 0-1: tiles
+    {64, 32, 256}, {64, 16, 256},                    // 2-3: K split over the waves
+    {32, 64, 256}, {32, 32, 256}, {32, 16, 256},     // 4-6
+    {16, 64, 256}, {16, 32, 256}, {16, 16, 256},     // 7-9
 };
 constexpr int kNumMxConfigs = sizeof(kMxConfigs) / sizeof(kMxConfigs[0]);
 
 template <int C, int OT>
 const void *mx_few_ptr() {
     constexpr Config c = kMxConfigs[C];
-    return reinterpret_cast<const void *>(&mx_few_kernel<c.bm / 16, c.bn / 16, 4, OT>);
+    return reinterpret_cast<const void *>(&mx_few_kernel<c.bm / 16, c.bn / 16, c.threads / 64, OT>);
 }
 
 template <int OT>
 const void *mx_ptr(int cfg) {
     switch (cfg) {
-    case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 256, 128, 64, 2, OT>);
-    case 1: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 128, 64, 64, 3, OT>);
-    case 2: return reinterpret_cast<const void *>(&mx_tile_kernel<128, 128, 64, 64, 2, OT>);
+    case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<256, 256, 128, 64, OT>);
+    case 1: return reinterpret_cast<const void *>(&mx_tile_kernel<128, 128, 64, 64, OT>);
+    case 2: return mx_few_ptr<2, OT>();
     case 3: return mx_few_ptr<3, OT>();
     case 4: return mx_few_ptr<4, OT>();
     case 5: return mx_few_ptr<5, OT>();
     case 6: return mx_few_ptr<6, OT>();
     case 7: return mx_few_ptr<7, OT>();
     case 8: return mx_few_ptr<8, OT>();
-    case 9: return mx_few_ptr<9, OT>();
-    default: return mx_few_ptr<10, OT>();
+    default: return mx_few_ptr<9, OT>();
     }
 }
 
 constexpr Config kA16Configs[] = {
     {256, 256, 512}, {128, 128, 256},                         // 0-1: tiles
-    {64, 32, 256}, {48, 32, 256},                             // 2-3: K split over the waves
+    {64, 32, 512}, {48, 32, 512},                             // 2-3: K split over the waves
     {32, 64, 256}, {32, 32, 512},                             // 4-5
     {16, 64, 512}, {16, 32, 512}, {16, 16, 512},              // 6-8
-    {8, 64, 512}, {8, 32, 512}, {8, 16, 512},                 // 9-11
+    {8, 64, 512}, {8, 32, 1024}, {8, 16, 512},                // 9-11
 };
 constexpr int kNumA16Configs = sizeof(kA16Configs) / sizeof(kA16Configs[0]);
 
@@ -1615,15 +1597,15 @@ const void *a16_ptr(int cfg) {
     switch (cfg) {
     case 0: return reinterpret_cast<const void *>(&a16_tile_kernel<T, 256, 256, 128, 64, OT>);
     case 1: return reinterpret_cast<const void *>(&a16_tile_kernel<T, 128, 128, 64, 64, OT>);
-    case 2: return a16_few_ptr<T, 2, 4, OT>();
-    case 3: return a16_few_ptr<T, 3, 5, OT>();
+    case 2: return a16_few_ptr<T, 2, 2, OT>();
+    case 3: return a16_few_ptr<T, 3, 2, OT>();
     case 4: return a16_few_ptr<T, 4, 5, OT>();
     case 5: return a16_few_ptr<T, 5, 3, OT>();
     case 6: return a16_few_ptr<T, 6, 4, OT>();
     case 7: return a16_few_ptr<T, 7, 5, OT>();
     case 8: return a16_few_ptr<T, 8, 5, OT>();
     case 9: return a16_few_ptr<T, 9, 5, OT>();
-    case 10: return a16_few_ptr<T, 10, 5, OT>();
+    case 10: return a16_few_ptr<T, 10, 4, OT>();
     default: return a16_few_ptr<T, 11, 5, OT>();
     }
 }
@@ -1632,8 +1614,41 @@ const void *a16_ptr(int cfg, int ot) {
     return ot == kF32 ? a16_ptr<T, kF32>(cfg) : ot == kF16 ? a16_ptr<T, kF16>(cfg) : a16_ptr<T, kBF16>(cfg);
 }
 
+// The tile of a product of many rows: 0 (256 x 256, one workgroup per CU) or 1 (128 x 128,
+// two).  A round of the CUs costs the tiles' area; a last round that is not full 0.35 + 0.65
+// of its share (fewer CUs clock higher and get more of the L2); and the area of 128 x 128
+// tiles costs `dearer` times that of 256 x 256 ones (twice the bytes through the L2 per
+// product).  Timed at 14 shapes from 1500^3 to 8192^3 the choice is the faster one at 13, and
+// 8% off at 7000 x 7000 x 2000: e.g. (MXFP4, us, 0 against 1) 8192^3 248 and 287,
+// 3000^3 24.6 and 28.0, 2500^3 20.7 and 15.4, 1024 x 8192 x 8192 40.8 and 35.6.
+int pick_tile(int64_t M, int64_t N, double dearer) {
+    auto rounds = [](int64_t tiles, int64_t slots) {
+        const double part = double(tiles % slots) / double(slots);
+        return double(tiles / slots) + (part > 0 ? 0.35 + 0.65 * part : 0.0);
+    };
+    const double large = rounds(cdiv(M, 256) * cdiv(N, 256), 256) * 256 * 256;
+    const double small = rounds(cdiv(M, 128) * cdiv(N, 128), 512) * 2 * 128 * 128 * dearer;
+    return large <= small ? 0 : 1;
+}
+
+// The column width (64, 32 or 16: 0, 1 or 2) of a tile of few rows: the widest that still
+// makes `least` workgroups.  A wider tile reads A less often; a CU without a workgroup reads
+// nothing.
+int pick_width(int64_t N, int64_t least) { return cdiv(N, 64) >= least ? 0 : cdiv(N, 32) >= least ? 1 : 2; }
+
+// gemm_mxf4.  To 32 rows a tile of 16 or 32 rows, whose work is short beside its start: 128
+// workgroups are enough where K is long (us by width 64 / 32 / 16: one row of
+// 8192 x 8192 7.5 / 8.6 / 11.5, 4096 x 14336 9.0 / 7.3 / 8.8, 4096 x 4096 4.2 / 3.5 / 3.1).
+// Above, 64 x 32 or 64 x 16 while one round of the CUs takes them all (256 x 1024 x 8192
+// 7.4 against 16.3 on 128 x 128 tiles), or two where 128 x 128 tiles would leave three CUs
+// of four without one over a long K (128 x 8192 x 8192 18.1 against 22.7); the chip once
+// filled, tiles read A less often (256 x 8192 x 8192 22.7 against 34.5).
 int pick_mx(int64_t M, int64_t N, int64_t K) {
-    return M <= 16 ? 8 : M <= 32 ? 5 : M <= 64 ? 3 : 2;
+    if (M <= 32) return (M <= 16 ? 7 : 4) + pick_width(N, K <= 4096 ? 256 : 128);
+    const int64_t few = cdiv(M, 64) * cdiv(N, 32);
+    if (few <= 128) return 3;
+    if (few <= 256 || (few <= 512 && K >= 8192 && cdiv(M, 128) * cdiv(N, 128) <= 64)) return 2;
+    return pick_tile(M, N, 1.15);
 }
 
 int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a,
@@ -1659,8 +1674,19 @@ int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_
     return run(fn, (int64_t)args.tiles_m * args.tiles_n, c.threads, &args, stream);
 }
 
-int pick_a16(int64_t M, int64_t N, int64_t K) {
-    return M <= 16 ? 6 : M <= 32 ? 4 : M <= 64 ? 2 : cdiv(M, 256) * cdiv(N, 256) >= 192 ? 0 : 1;
+// gemm_a16_mxf4.  The same, with A's 16-bit rows the larger part of what a tile of few rows
+// reads: 8, 16, 32, 48 or 64 rows, and one round of workgroups of the widest tile (one row,
+// us by width 64 / 32 / 16: 16384 x 4096 8.4 / 9.7 / 14.1, 8192 x 8192 11.2 / 9.3 / 12.9,
+// 4096 x 4096 6.0 / 5.1 / 4.7).  A round of 64 x 32 takes a third to a quarter of one of
+// 128 x 128 tiles (K = 8192: 18 us against 60 for bf16, 22 against 106 for f16, whose
+// products are scaled by vector instructions), so it is taken up to that many rounds
+// (128 x 8192 x 8192, two rounds, bf16 36 against 61; 128 x 16384 x 4096, four, 42 against 34).
+int pick_a16(int a_type, int64_t M, int64_t N, int64_t K) {
+    if (M <= 16) return (M <= 8 ? 9 : 6) + pick_width(N, 256);
+    if (M <= 32) return cdiv(N, 64) >= 256 ? 4 : 5;
+    if (cdiv(M, 64) * cdiv(N, 32) <= 256 * (a_type == kF16 ? 4 : 3))
+        return cdiv(M, 48) == cdiv(M, 64) ? 3 : 2;   // 48 rows where that takes no more tiles
+    return pick_tile(M, N, 1.23);
 }
 
 int launch_a16(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
@@ -1676,7 +1702,7 @@ int launch_a16(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t 
     if (rc == PDGEMM_OK && K > 0) rc = check_mx_memory(B, ldb, scale_b, ldsb);
     if (rc == PDGEMM_OK && K > 0 && (lda % 8 || ((uintptr_t)A & 15))) rc = PDGEMM_EALIGN;
     if (rc != PDGEMM_OK) return rc;
-    if (cfg < 0) cfg = pick_a16(M, N, K);
+    if (cfg < 0) cfg = pick_a16(a_type, M, N, K);
     const Config &c = kA16Configs[cfg];
     const uint8_t *const p = static_cast<const uint8_t *>(C);
     MxArgs args = {K ? static_cast<const uint8_t *>(A) : p, nullptr, K ? B : p, K ? scale_b : p, C, K ? 2 * lda : 0,
@@ -1760,6 +1786,9 @@ int pdgemm_a16_mxf4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A,
 
 int pdgemm_a16_mxf4_num_configs(void) { return kNumA16Configs; }
 
-int pdgemm_a16_mxf4_pick(int64_t M, int64_t N, int64_t K) { return pick_a16(M, N, K); }
+int pdgemm_a16_mxf4_pick(int a_type, int64_t M, int64_t N, int64_t K) {
+    if (a_type != kF16 && a_type != kBF16) return -1;
+    return pick_a16(a_type, M, N, K);
+}
 
 }  // extern "C"

@@ -1549,9 +1549,9 @@ struct Config {
 
 constexpr Config kMxConfigs[] = {
     {256, 256, 512}, {128, 128, 256},                // 0-1: tiles
-    {64, 32, 256}, {64, 16, 256},                    // 2-3: K split over the waves
-    {32, 64, 256}, {32, 32, 256}, {32, 16, 256},     // 4-6
-    {16, 64, 256}, {16, 32, 256}, {16, 16, 256},     // 7-9
+    {64, 32, 256},                                   // 2: K split over the waves
+    {32, 64, 256}, {32, 32, 256}, {32, 16, 256},     // 3-5
+    {16, 64, 256}, {16, 32, 256}, {16, 16, 256},     // 6-8
 };
 constexpr int kNumMxConfigs = sizeof(kMxConfigs) / sizeof(kMxConfigs[0]);
 
@@ -1572,8 +1572,7 @@ const void *mx_ptr(int cfg) {
     case 5: return mx_few_ptr<5, OT>();
     case 6: return mx_few_ptr<6, OT>();
     case 7: return mx_few_ptr<7, OT>();
-    case 8: return mx_few_ptr<8, OT>();
-    default: return mx_few_ptr<9, OT>();
+    default: return mx_few_ptr<8, OT>();
     }
 }
 
@@ -1631,23 +1630,22 @@ int pick_tile(int64_t M, int64_t N, double dearer) {
     return large <= small ? 0 : 1;
 }
 
-// The column width (64, 32 or 16: 0, 1 or 2) of a tile of few rows: the widest that still
-// makes `least` workgroups.  A wider tile reads A less often; a CU without a workgroup reads
-// nothing.
-int pick_width(int64_t N, int64_t least) { return cdiv(N, 64) >= least ? 0 : cdiv(N, 32) >= least ? 1 : 2; }
+int64_t tiles(const Config &c, int64_t M, int64_t N) { return cdiv(M, c.bm) * cdiv(N, c.bn); }
 
-// gemm_mxf4.  To 32 rows a tile of 16 or 32 rows, whose work is short beside its start: 128
-// workgroups are enough where K is long (us by width 64 / 32 / 16: one row of
-// 8192 x 8192 7.5 / 8.6 / 11.5, 4096 x 14336 9.0 / 7.3 / 8.8, 4096 x 4096 4.2 / 3.5 / 3.1).
-// Above, 64 x 32 or 64 x 16 while one round of the CUs takes them all (256 x 1024 x 8192
-// 7.4 against 16.3 on 128 x 128 tiles), or two where 128 x 128 tiles would leave three CUs
-// of four without one over a long K (128 x 8192 x 8192 18.1 against 22.7); the chip once
-// filled, tiles read A less often (256 x 8192 x 8192 22.7 against 34.5).
+// gemm_mxf4.  While one round of the CUs takes all of them, small tiles, whose workgroups read
+// the least (us: 251 x 90 x 2911 16 x 16 3.1, 64 x 16 4.5; 256 x 1024 x 8192 64 x 32 7.4,
+// 128 x 128 16.3); to 32 rows a wider tile over a long K, where 128 workgroups are enough
+// (one row by width 64 / 32 / 16: 8192 x 8192 7.5 / 8.6 / 11.5, 4096 x 14336 9.0 / 7.3 / 8.8,
+// 4096 x 4096 4.2 / 3.5 / 3.1).  Then 64 x 32 once more where 128 x 128 tiles would leave
+// three CUs of four without one over a long K (128 x 8192 x 8192 18.1 against 22.7).
 int pick_mx(int64_t M, int64_t N, int64_t K) {
-    if (M <= 32) return (M <= 16 ? 7 : 4) + pick_width(N, K <= 4096 ? 256 : 128);
-    const int64_t few = cdiv(M, 64) * cdiv(N, 32);
-    if (few <= 128) return 3;
-    if (few <= 256 || (few <= 512 && K >= 8192 && cdiv(M, 128) * cdiv(N, 128) <= 64)) return 2;
+    if (M <= 32) {
+        const int64_t least = K <= 4096 ? 256 : 128;
+        return (M <= 16 ? 6 : 3) + (cdiv(N, 64) >= least ? 0 : cdiv(N, 32) >= least ? 1 : 2);
+    }
+    for (int c : {8, 5, 7, 4, 2})
+        if (tiles(kMxConfigs[c], M, N) <= 256) return c;
+    if (K >= 8192 && tiles(kMxConfigs[2], M, N) <= 512 && tiles(kMxConfigs[1], M, N) <= 64) return 2;
     return pick_tile(M, N, 1.15);
 }
 
@@ -1674,17 +1672,19 @@ int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_
     return run(fn, (int64_t)args.tiles_m * args.tiles_n, c.threads, &args, stream);
 }
 
-// gemm_a16_mxf4.  The same, with A's 16-bit rows the larger part of what a tile of few rows
-// reads: 8, 16, 32, 48 or 64 rows, and one round of workgroups of the widest tile (one row,
-// us by width 64 / 32 / 16: 16384 x 4096 8.4 / 9.7 / 14.1, 8192 x 8192 11.2 / 9.3 / 12.9,
-// 4096 x 4096 6.0 / 5.1 / 4.7).  A round of 64 x 32 takes a third to a quarter of one of
-// 128 x 128 tiles (K = 8192: 18 us against 60 for bf16, 22 against 106 for f16, whose
-// products are scaled by vector instructions), so it is taken up to that many rounds
-// (128 x 8192 x 8192, two rounds, bf16 36 against 61; 128 x 16384 x 4096, four, 42 against 34).
+// gemm_a16_mxf4.  The same, with A's 16-bit rows four times as dear as B's: the tile that
+// reads the least and makes one round of workgroups (us: 152 x 68 x 4562 f16 8 x 16 5.5,
+// 64 x 32 13.0; one row by width 64 / 32 / 16 16384 x 4096 8.4 / 9.7 / 14.1, 8192 x 8192
+// 11.2 / 9.3 / 12.9, 4096 x 4096 6.0 / 5.1 / 4.7).  Past that, to 32 rows the widest.  A round of
+// 64 x 32 takes a third to a quarter of one of 128 x 128 tiles (K = 8192: 18 us against 60
+// for bf16, 22 against 106 for f16, whose products are scaled by vector instructions), so it
+// is taken up to that many rounds of a K that is not short (128 x 8192 x 8192, two, bf16 36
+// against 61; 128 x 16384 x 4096, four, 42 against 34; 1086 x 1004 x 456, three, 12.4 against 8.6).
 int pick_a16(int a_type, int64_t M, int64_t N, int64_t K) {
-    if (M <= 16) return (M <= 8 ? 9 : 6) + pick_width(N, 256);
-    if (M <= 32) return cdiv(N, 64) >= 256 ? 4 : 5;
-    if (cdiv(M, 64) * cdiv(N, 32) <= 256 * (a_type == kF16 ? 4 : 3))
+    for (int c : {11, 10, 8, 7, 9, 6, 5, 3, 4, 2})
+        if (tiles(kA16Configs[c], M, N) <= 256) return c;
+    if (M <= 32) return M <= 8 ? 9 : M <= 16 ? 6 : 4;
+    if (K >= 2048 && tiles(kA16Configs[2], M, N) <= 256 * (a_type == kF16 ? 4 : 3))
         return cdiv(M, 48) == cdiv(M, 64) ? 3 : 2;   // 48 rows where that takes no more tiles
     return pick_tile(M, N, 1.23);
 }

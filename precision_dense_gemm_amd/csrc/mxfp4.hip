@@ -478,30 +478,38 @@ __device__ __forceinline__ floatx4_t mfma_fp4(const uint4 &a, const uint4 &b, co
 // rounded once to C's type and stored.  acc[i][j] of a wave holds, in register e of lane
 // l, row FM * (4 (l / 16) + e) + i (with kMixed; else 16 i + 4 (l / 16) + e) and column
 // FN * (l % 16) + j of the tile, of which BM rows are stored.  `part` is LDS of kStride floats
-// per wave, each wave's part free for it to write.
+// per wave, each wave's part free for it to write; where it does not hold a wave's tile, the
+// column blocks j go through it in two halves.
 template <int FM, int FN, int W, int OT, int kStride, int BM, bool kMixed>
 __device__ __forceinline__ void join_and_store(floatx4_t (&acc)[FM][FN], float *part, const MxArgs &args, int m0, int n0,
                                                int tid, int lane, int wave) {
     using Out = typename ElemOf<OT>::type;
-    constexpr int BN = 16 * FN;
-    static_assert(kStride >= FM * FN * 4 * kWave, "a wave's partial tile");
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[wave * kStride + ((i * FN + j) * 4 + e) * kWave + lane] = acc[i][j][e];
-    __syncthreads();
+    constexpr int kTile = FM * FN * 4 * kWave;
+    constexpr int kParts = kStride >= kTile ? 1 : 2, FG = FN / kParts;
+    static_assert(kStride * kParts >= kTile && FN % kParts == 0, "a wave's tile, or half of it");
     Out *const C = static_cast<Out *>(args.C);
-    for (int x = tid; x < BM * BN; x += W * kWave) {
-        const int row = x / BN, col = x % BN;
-        if (m0 + row >= args.M || n0 + col >= args.N) continue;
-        const int i = kMixed ? row % FM : row / 16, rr = kMixed ? row / FM : row % 16;
-        const int at = ((i * FN + col % FN) * 4 + (rr & 3)) * kWave + (rr >> 2) * 16 + col / FN;
-        float sum = part[at];
 #pragma unroll
-        for (int w = 1; w < W; ++w) sum += part[w * kStride + at];
-        C[(int64_t)(m0 + row) * args.ldc + n0 + col] = (Out)sum;
+    for (int h = 0; h < kParts; ++h) {
+        if (h > 0) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FG; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    part[wave * kStride + ((i * FG + j) * 4 + e) * kWave + lane] = acc[i][h * FG + j][e];
+        __syncthreads();
+        for (int x = tid; x < BM * 16 * FG; x += W * kWave) {
+            const int row = x / (16 * FG), n = x % (16 * FG) / FG, j = x % FG;
+            const int col = FN * n + h * FG + j;
+            if (m0 + row >= args.M || n0 + col >= args.N) continue;
+            const int i = kMixed ? row % FM : row / 16, rr = kMixed ? row / FM : row % 16;
+            const int at = ((i * FG + j) * 4 + (rr & 3)) * kWave + (rr >> 2) * 16 + n;
+            float sum = part[at];
+#pragma unroll
+            for (int w = 1; w < W; ++w) sum += part[w * kStride + at];
+            C[(int64_t)(m0 + row) * args.ldc + n0 + col] = (Out)sum;
+        }
     }
 }
 
@@ -1182,11 +1190,7 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
         // no copy may still be writing this workgroup's LDS when it exits
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    // a wave's partial tile takes its first slot where that is large enough
-    constexpr bool kFits = sizeof(Slot) >= FM * FN * 1024;
-    __shared__ float part[kFits ? 1 : W * FM * FN * 256];
-    join_and_store<FM, FN, W, OT, kFits ? sizeof(Slot) / 4 : FM * FN * 256, RA, false>(
-        acc, kFits ? reinterpret_cast<float *>(&s0[0]) : part, args, m0, n0, tid, lane, wave);
+    join_and_store<FM, FN, W, OT, sizeof(Slot) / 4, RA, false>(acc, reinterpret_cast<float *>(&s0[0]), args, m0, n0, tid, lane, wave);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1547,9 +1551,9 @@ struct Config {
 
 constexpr Config kMxConfigs[] = {
     {256, 256, 512}, {128, 128, 256},                // 0-1: tiles
-    {64, 32, 256},                                   // 2: K split over the waves
-    {32, 64, 256}, {32, 32, 256}, {32, 16, 256},     // 3-5
-    {16, 64, 256}, {16, 32, 256}, {16, 16, 256},     // 6-8
+    {64, 64, 192}, {64, 32, 256},                    // 2-3: K split over the waves
+    {32, 64, 256}, {32, 32, 256}, {32, 16, 256},     // 4-6
+    {16, 64, 256}, {16, 32, 256}, {16, 16, 256},     // 7-9
 };
 constexpr int kNumMxConfigs = sizeof(kMxConfigs) / sizeof(kMxConfigs[0]);
 
@@ -1570,7 +1574,8 @@ const void *mx_ptr(int cfg) {
     case 5: return mx_few_ptr<5, OT>();
     case 6: return mx_few_ptr<6, OT>();
     case 7: return mx_few_ptr<7, OT>();
-    default: return mx_few_ptr<8, OT>();
+    case 8: return mx_few_ptr<8, OT>();
+    default: return mx_few_ptr<9, OT>();
     }
 }
 
@@ -1580,6 +1585,7 @@ constexpr Config kA16Configs[] = {
     {32, 64, 256}, {32, 32, 512},                             // 4-5
     {16, 64, 512}, {16, 32, 512}, {16, 16, 512},              // 6-8
     {8, 64, 512}, {8, 32, 1024}, {8, 16, 512},                // 9-11
+    {64, 64, 512},                                            // 12
 };
 constexpr int kNumA16Configs = sizeof(kA16Configs) / sizeof(kA16Configs[0]);
 
@@ -1603,7 +1609,8 @@ const void *a16_ptr(int cfg) {
     case 8: return a16_few_ptr<T, 8, 5, OT>();
     case 9: return a16_few_ptr<T, 9, 5, OT>();
     case 10: return a16_few_ptr<T, 10, 4, OT>();
-    default: return a16_few_ptr<T, 11, 5, OT>();
+    case 11: return a16_few_ptr<T, 11, 5, OT>();
+    default: return a16_few_ptr<T, 12, 2, OT>();
     }
 }
 template <int T>
@@ -1631,19 +1638,19 @@ int pick_tile(int64_t M, int64_t N, double dearer) {
 int64_t tiles(const Config &c, int64_t M, int64_t N) { return cdiv(M, c.bm) * cdiv(N, c.bn); }
 
 // gemm_mxf4.  While one round of the CUs takes all of them, small tiles, whose workgroups read
-// the least (us: 251 x 90 x 2911 16 x 16 3.1, 64 x 16 4.5; 256 x 1024 x 8192 64 x 32 7.4,
-// 128 x 128 16.3); to 32 rows a wider tile over a long K, where 128 workgroups are enough
-// (one row by width 64 / 32 / 16: 8192 x 8192 7.5 / 8.6 / 11.5, 4096 x 14336 9.0 / 7.3 / 8.8,
-// 4096 x 4096 4.2 / 3.5 / 3.1).  Then 64 x 32 once more where 128 x 128 tiles would leave
-// three CUs of four without one over a long K (128 x 8192 x 8192 18.1 against 22.7).
+// the least (us: 251 x 90 x 2911 16 x 16 3.1, 64 x 32 4.5; 256 x 1024 x 8192 64 x 32 7.4,
+// 128 x 128 16.3), 64 x 64 where K is long enough to pay for its start (256 x 4096 x 8192
+// 13.4 against 16.9 on 128 x 128 tiles, at K = 2048 8.2 against 6.6); to 32 rows a wider tile
+// over a long K, where 128 workgroups are enough (one row by width 64 / 32 / 16: 8192 x 8192
+// 7.5 / 8.6 / 11.5, 4096 x 14336 9.0 / 7.3 / 8.8, 4096 x 4096 4.2 / 3.5 / 3.1).
 int pick_mx(int64_t M, int64_t N, int64_t K) {
     if (M <= 32) {
         const int64_t least = K <= 4096 ? 256 : 128;
-        return (M <= 16 ? 6 : 3) + (cdiv(N, 64) >= least ? 0 : cdiv(N, 32) >= least ? 1 : 2);
+        return (M <= 16 ? 7 : 4) + (cdiv(N, 64) >= least ? 0 : cdiv(N, 32) >= least ? 1 : 2);
     }
-    for (int c : {8, 5, 7, 4, 2})
+    for (int c : {9, 6, 8, 5, 3})
         if (tiles(kMxConfigs[c], M, N) <= 256) return c;
-    if (K >= 8192 && tiles(kMxConfigs[2], M, N) <= 512 && tiles(kMxConfigs[1], M, N) <= 64) return 2;
+    if (K > 4096 && tiles(kMxConfigs[2], M, N) <= 256) return 2;
     return pick_tile(M, N, 1.15);
 }
 
@@ -1673,17 +1680,15 @@ int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_
 // gemm_a16_mxf4.  The same, with A's 16-bit rows four times as dear as B's: the tile that
 // reads the least and makes one round of workgroups (us: 152 x 68 x 4562 f16 8 x 16 5.5,
 // 64 x 32 13.0; one row by width 64 / 32 / 16 16384 x 4096 8.4 / 9.7 / 14.1, 8192 x 8192
-// 11.2 / 9.3 / 12.9, 4096 x 4096 6.0 / 5.1 / 4.7).  Past that, to 32 rows the widest.  A round of
-// 64 x 32 takes a third to a quarter of one of 128 x 128 tiles (K = 8192: 18 us against 60
-// for bf16, 22 against 106 for f16, whose products are scaled by vector instructions), so it
-// is taken up to that many rounds of a K that is not short (128 x 8192 x 8192, two, bf16 36
-// against 61; 128 x 16384 x 4096, four, 42 against 34; 1086 x 1004 x 456, three, 12.4 against 8.6).
+// 11.2 / 9.3 / 12.9, 4096 x 4096 6.0 / 5.1 / 4.7).  Past that, to 32 rows the widest.  A round
+// of 64 x 64 takes two fifths of one of 128 x 128 tiles, a third for f16, whose products are
+// scaled by vector instructions (K = 8192: 24 us against 61, 32 against 106), so it is taken
+// for so many rounds of a K that is not short (1086 x 1004 x 456 12.4 against 8.6).
 int pick_a16(int a_type, int64_t M, int64_t N, int64_t K) {
-    for (int c : {11, 10, 8, 7, 9, 6, 5, 3, 4, 2})
+    for (int c : {11, 10, 8, 7, 9, 6, 5, 3, 4, 2, 12})
         if (tiles(kA16Configs[c], M, N) <= 256) return c;
     if (M <= 32) return M <= 8 ? 9 : M <= 16 ? 6 : 4;
-    if (K >= 2048 && tiles(kA16Configs[2], M, N) <= 256 * (a_type == kF16 ? 4 : 3))
-        return cdiv(M, 48) == cdiv(M, 64) ? 3 : 2;   // 48 rows where that takes no more tiles
+    if (K >= 2048 && tiles(kA16Configs[12], M, N) <= 256 * (a_type == kF16 ? 3 : 2)) return 12;
     return pick_tile(M, N, 1.23);
 }
 

@@ -288,7 +288,7 @@ TILE_SHAPES = [(1, 1, 1), (33, 65, 256), (65, 63, 513), (255, 257, 1030), (260, 
                (300, 520, 8191), (129, 300, 300)]
 
 
-@pytest.mark.parametrize("cfg", range(9))
+@pytest.mark.parametrize("cfg", range(10))
 @pytest.mark.parametrize("shape", TILE_SHAPES, ids=[f"{m}x{n}x{k}" for m, n, k in TILE_SHAPES])
 def test_product_every_tile(pd, dev, shape, cfg):
     M, N, K = shape
@@ -378,7 +378,7 @@ def test_a16(pd, dev, shape, kind, a_kind):
 
 
 @pytest.mark.parametrize("a_kind", ["f16", "bf16"])
-@pytest.mark.parametrize("cfg", range(12))
+@pytest.mark.parametrize("cfg", range(13))
 @pytest.mark.parametrize("shape", TILE_SHAPES, ids=[f"{m}x{n}x{k}" for m, n, k in TILE_SHAPES])
 def test_a16_every_tile(pd, dev, shape, cfg, a_kind):
     M, N, K = shape

@@ -102,14 +102,26 @@ __device__ __forceinline__ uint32_t codes32(uint32_t old, float x, float y, floa
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, x, y, scale, kSel);
 }
 
-// maximum over groups of 4, 8 or 16 lanes (in every lane); every lane is active
+// maximum over groups of 4 or 8 lanes (in every lane); every lane is active
 template <int kLanes>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
     v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));                            // quad_perm 1 0 3 2
     v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));                            // quad_perm 2 3 0 1
     if constexpr (kLanes >= 8) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));   // row_half_mirror
-    if constexpr (kLanes >= 16) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));  // row_mirror
     return v;
+}
+
+// One exchange of a maximum over lanes: of 2 n values v, the lanes without `kBit` keep the
+// first n and the others the last n, each with what its partner (DPP control kDpp, which
+// flips that bit) has there.
+template <int n, int kBit, int kDpp>
+__device__ __forceinline__ void halve(uint32_t (&v)[32], int lane) {
+    const bool upper = lane & kBit;
+#pragma unroll
+    for (int p = 0; p < n; ++p) {
+        const uint32_t keep = upper ? v[p + n] : v[p], give = upper ? v[p] : v[p + n];
+        v[p] = max(keep, (uint32_t)__builtin_amdgcn_mov_dpp((int)give, kDpp, 0xF, 0xF, true));
+    }
 }
 
 struct QuantArgs {
@@ -229,7 +241,7 @@ __global__ __launch_bounds__(512) void mx_quant_cols_kernel(QuantArgs args) {
     __shared__ uint4 lqt[kCols][8];               // chunk w of column c at w ^ ((c / 2) % 8)
     __shared__ __align__(16) uint8_t lq[kBoth ? kRows : 1][64];
     __shared__ uint8_t sct[8][kCols];
-    __shared__ uint8_t scr[4][kBoth ? kRows : 1];
+    __shared__ __align__(16) uint8_t scr[4][kBoth ? kRows : 16];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -256,22 +268,40 @@ __global__ __launch_bounds__(512) void mx_quant_cols_kernel(QuantArgs args) {
     }
 
     if constexpr (kBoth) {
+        // The 32 rows' largest magnitudes over 16 lanes: each exchange leaves a lane half of its
+        // rows, so that lane l ends with rows 2 (l % 16) and + 1 of its block, and one lane
+        // makes a row's scale for all 16.
+        uint32_t a[32];
 #pragma unroll
         for (int r = 0; r < 32; ++r) {
-            uint32_t a;
             if constexpr (T == kF32)
-                a = group_max<16>(max(v[r][0] & 0x7FFFFFFFu, v[r][1] & 0x7FFFFFFFu));
+                a[r] = max(v[r][0] & 0x7FFFFFFFu, v[r][1] & 0x7FFFFFFFu);
             else
-                a = magnitude_bits<T>(group_max<16>(max(v[r][0] & 0x7FFFu, (v[r][0] >> 16) & 0x7FFFu)));
-            const uint32_t byte = scale_byte(a, args.bias);
+                a[r] = max(v[r][0] & 0x7FFFu, (v[r][0] >> 16) & 0x7FFFu);
+        }
+        halve<16, 8, 0x140>(a, lane);   // row_mirror: lane 15 - l
+        halve<8, 4, 0x141>(a, lane);    // row_half_mirror: 7 - l
+        halve<4, 2, 0x4E>(a, lane);     // quad_perm 2 3 0 1
+        halve<2, 1, 0xB1>(a, lane);     // quad_perm 1 0 3 2
+        uint32_t b[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) b[x] = scale_byte(T == kF32 ? a[x] : magnitude_bits<T>(a[x]), args.bias);
+        uint8_t *const sr = &scr[lane / 16][wave * 32];
+        *reinterpret_cast<uint16_t *>(sr + 2 * (lane & 15)) = (uint16_t)(b[0] | b[1] << 8);
+        const bool special = __builtin_amdgcn_ballot_w64(max(b[0], b[1]) == 255u) != 0;   // of any block of the wave
+        uint32_t w[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) w[x] = reinterpret_cast<const uint32_t *>(sr)[x];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            const uint32_t byte = (w[r / 4] >> (8 * (r & 3))) & 255u;
             const float scale = scale_value(byte);
             uint32_t c;
             if constexpr (T == kF32)
                 c = codes32<0>(0, __builtin_bit_cast(float, v[r][0]), __builtin_bit_cast(float, v[r][1]), scale);
             else
                 c = codes16<T, 0>(0, v[r][0], scale);
-            lq[wave * 32 + r][lane] = byte == 255 ? 0 : (uint8_t)c;
-            if (lane % 16 == 0) scr[lane / 16][wave * 32 + r] = (uint8_t)byte;
+            lq[wave * 32 + r][lane] = special && byte == 255 ? 0 : (uint8_t)c;
         }
     }
 

@@ -653,6 +653,10 @@ def _mx_form(out, rows: int, K: int, device, stream, name: str):
         r, _, ld, lds = _mx_operand(codes, scales, K, name)
         if r != rows:
             raise ValueError(f"{name} must have {rows} rows")
+        # the last row's last chunk is written whole: 16 bytes a block, wherever the view ends
+        end = codes.storage_offset() + (rows - 1) * (ld // 2) + 16 * ((K + MX_BLOCK - 1) // MX_BLOCK)
+        if rows and codes.untyped_storage().nbytes() < end:
+            raise ValueError(f"{name}'s codes must have room for whole 16-byte blocks in every row")
         return (codes, scales), (codes.data_ptr(), ld, scales.data_ptr(), lds)
     blocks = (K + MX_BLOCK - 1) // MX_BLOCK
     lds = _round_up(rows, 16)

@@ -570,3 +570,104 @@ def test_another_stream(pd, dev):
     side.synchronize()
     assert_close(C, R, S, -(-K // 64), "f32", "side stream")
     assert np.array_equal(v.cpu().double().numpy(), mx.values(*mx.quantize(x), K))
+
+
+# ---- large sizes, long rows ----
+
+@pytest.mark.parametrize("a_kind", [None, "f16", "bf16"], ids=["mxf4", "a16-f16", "a16-bf16"])
+@pytest.mark.parametrize("shape", [(4096, 4096, 256), (8192, 4096, 96), (2560, 2304, 520), (1024, 8192, 320)],
+                         ids=["one-window", "two-windows", "bands", "wide"])
+def test_many_tiles(pd, dev, shape, a_kind):
+    """Grids of whole 16 x 16 windows of tiles, and of bands: every element, against the
+    product in 64 bits of the oracle's values."""
+    M, N, K = shape
+    gu.note(f"[case] many tiles {shape} {a_kind}")
+    b = random_operand(N, K, 82, 124, 130)
+    vb = torch.from_numpy(mx.values(*b, K)).to(dev)
+    if a_kind is None:
+        a = random_operand(M, K, 81, 124, 130)
+        va = torch.from_numpy(mx.values(*a, K)).to(dev)
+        C = pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K)
+    else:
+        t, x = to_type(spread(M, K, 83), a_kind)
+        va = torch.from_numpy(x).to(dev)
+        C = pd.gemm_a16_mxf4(source(t, dev, gu.round_up(K, 8) - K + 8), *stored(*b, K, dev))
+    R, S = va @ vb.t(), va.abs() @ vb.t().abs()
+    bad = (C.double() - R).abs() > (-(-K // 64) + 1) * 2.0 ** -22 * S
+    assert not bool(bad.any()), f"{int(bad.sum())} off, first at {torch.nonzero(bad)[0].tolist()}"
+
+
+@pytest.mark.parametrize("cfg", [0, 1, 2, 3, 9])
+def test_rows_of_4_mib(pd, dev, cfg):
+    """The longest rows the library takes: codes, scales, activations and C 4 MiB apart."""
+    M, N, K = (260, 70, 300) if cfg < 2 else (70, 40, 300)
+    gu.note(f"[case] rows of 4 MiB cfg={cfg}")
+    row = 1 << 22
+    a, b, R, S = operands(M, N, K, 91)
+
+    def far(host):
+        buf = torch.empty((host.shape[0], row), dtype=torch.uint8, device=dev)
+        buf[:, :host.shape[1]] = torch.from_numpy(host).to(dev)
+        return buf[:, :host.shape[1]]
+
+    A, sa, B, sb = far(a[0]), far(a[1]), far(b[0]), far(b[1])
+    out = torch.empty((M, row // 4), device=dev)[:, :N]
+    pd.gemm_mxf4(A, sa, B, sb, K, out=out, cfg=cfg)
+    assert_close(out, R, S, -(-K // 64), "f32", f"4 MiB cfg {cfg}")
+    t, x = to_type(spread(M, K, 92), "bf16")
+    x16 = torch.empty((M, row // 2), dtype=torch.bfloat16, device=dev)[:, :K]
+    x16.copy_(t)
+    R, S = mx.product(x, mx.values(*b, K))
+    pd.gemm_a16_mxf4(x16, B, sb, out=out, cfg=cfg)
+    assert_close(out, R, S, -(-K // 64) + 1, "f32", f"4 MiB a16 cfg {cfg}")
+
+
+def test_offsets_past_32_bits(pd, dev):
+    """A tensor of more than 2^31 elements (and bytes past 2^32): its last rows, and rows in
+    between, quantise and read back as those rows alone do."""
+    rows, K = 33000, 65600
+    gu.note(f"[case] past 32 bits {rows}x{K}")
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device=dev)
+    part = torch.from_numpy(spread(96, K, 97)).to(torch.bfloat16).to(dev)
+    for first in range(0, rows, 96):
+        x[first:first + 96] = part[:min(96, rows - first)] * 2.0 ** (first % 7)
+    (q, s), (qt, st) = pd.mxf4_quantize_both(x)
+    for first in (0, 16384, rows - 96):
+        alone, scales = pd.mxf4_quantize(x[first:first + 96])
+        assert torch.equal(q[first:first + 96], alone) and torch.equal(s[:, first:first + 96], scales)
+        v = pd.mxf4_dequantize(q[first:first + 96], s[:, first:first + 112][:, :96].contiguous(), K)
+        assert torch.equal(v, pd.mxf4_dequantize(alone, scales, K))
+    last = rows // 32 * 32 - 64
+    alone, scales = pd.mxf4_quantize(x[last:].contiguous(), transpose=True)
+    assert torch.equal(qt[:, last // 2:], alone) and torch.equal(st[last // 32:], scales)
+    v = pd.mxf4_dequantize(q, s, K, out_dtype=torch.bfloat16)
+    assert torch.equal(v[-5:], pd.mxf4_dequantize(*pd.mxf4_quantize(x[-5:]), K, out_dtype=torch.bfloat16))
+
+
+def test_out_needs_room_for_whole_blocks(pd, dev):
+    gu.note("[case] out without room")
+    x = torch.randn((1, 40), device=dev)
+    scales = torch.empty((2, 16), dtype=torch.uint8, device=dev)[:, :1]
+    with pytest.raises(ValueError):
+        pd.mxf4_quantize(x, out=(torch.empty((1, 20), dtype=torch.uint8, device=dev), scales))
+    codes = torch.empty((1, 32), dtype=torch.uint8, device=dev)[:, :20]
+    pd.mxf4_quantize(x, out=(codes, scales))
+    want = mx.quantize(x.cpu().double().numpy())
+    assert np.array_equal(codes.cpu().numpy(), want[0][:, :20]) and np.array_equal(scales.cpu().numpy(), want[1])
+
+
+def test_two_streams_at_once(pd, dev):
+    gu.note("[case] two streams at once")
+    M, N, K = 300, 400, 2000
+    cases = [operands(M, N, K, 51 + n) for n in range(2)]
+    devs = [(stored(*a, K, dev), stored(*b, K, dev)) for a, b, _, _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for n, st in enumerate(streams):
+            outs[n].append(pd.gemm_mxf4(*devs[n][0], *devs[n][1], K, stream=st))
+    torch.cuda.synchronize()
+    for n, (_, _, R, S) in enumerate(cases):
+        assert_close(outs[n][0], R, S, -(-K // 64), "f32", f"stream {n}")
+        assert all(torch.equal(o, outs[n][0]) for o in outs[n])

@@ -1036,7 +1036,7 @@ __device__ __forceinline__ float scale_or_nan(uint32_t byte) {
 template <int T> struct A16Map;
 template <> struct A16Map<kBF16> {
     static __device__ __forceinline__ int chunk(int u, int g) { return 2 * g + u; }       // of A's 8
-    static __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 3; }
+    static __device__ __forceinline__ int swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 };
 template <> struct A16Map<kF16> {
     static __device__ __forceinline__ int chunk(int u, int g) { return 4 * u + g; }

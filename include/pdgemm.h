@@ -407,8 +407,8 @@ int pdgemm_mxf4_quantize(int64_t rows, int64_t K, const void *src, int64_t ld, i
                          uint8_t *scales_t, int64_t ldst, int scale_rule, void *stream);
 
 /* The values of an MXFP4 operand, to a dense row-major dst of dst_type: exact
- * in binary32 (a magnitude of 2^128 and above, which the quantiser never makes,
- * is infinite), rounded to nearest even for the 16-bit types (binary16:
+ * in binary32 (a magnitude of 2^128 and above is infinite; of finite values the
+ * quantiser makes one only by FIT, from magnitudes of 1.75 * 2^127 and above), rounded to nearest even for the 16-bit types (binary16:
  * overflow gives infinity). */
 int pdgemm_mxf4_dequantize(int64_t rows, int64_t K, const uint8_t *q, int64_t ldq, const uint8_t *scales,
                            int64_t lds, void *dst, int64_t ldd, int dst_type, void *stream);
@@ -434,7 +434,7 @@ int pdgemm_mxf4_pick(int64_t M, int64_t N, int64_t K);
 /* C = A * B of 16-bit A (a_type PDGEMM_F16 or PDGEMM_BF16, row-major, rows of a
  * multiple of 16 bytes, 16-byte aligned) and MXFP4 B: weights kept in 4 bits
  * under activations that are not quantised.  B's values enter exactly (those of
- * 2^128 and above, which the quantiser never makes, may be infinite); sums and
+ * 2^128 and above may be infinite); sums and
  * rounding as in gemm_mxf4, explicit tiles as pdgemm_mxf4_cfg. */
 int gemm_a16_mxf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                   int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type,

@@ -1154,8 +1154,9 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         copy(step + S * W, slot, sc);
         if (step * 64 + 64 > K) {
-            // A's values at and beyond K may be anything, a NaN too: they become zeros (B's codes
-            // beside them are finite, and scales past the last block are zero)
+            // A's values at and beyond K may be anything, a NaN too: they become zeros, and in bf16,
+            // where a code times a scale of 2^126 or 2^127 may be infinite, B's codes too (scales
+            // past the last block are zero)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int n = K - step * 64 - 8 * Map::chunk(u, g);
@@ -1166,6 +1167,10 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
                 for (int i = 0; i < FM; ++i) {
                     uint4 &v = fa[u][i];
                     v = make_uint4(v.x & m[0], v.y & m[1], v.z & m[2], v.w & m[3]);
+                }
+                if constexpr (T == kBF16) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) w[j][u] &= n >= 8 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (4 * n)) - 1u;
                 }
             }
         }
@@ -1353,10 +1358,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         uint4 f[FN];
         float s[T == kBF16 ? 1 : FN];
     };
-    auto make_b = [&](const Codes &c, int u, FragB &b) __attribute__((always_inline)) {
+    // (bf16: where A's chunk has been zeroed, `live` is false and the scale is 2^-127, or a code
+    // times 2^126 or 2^127 could be infinite there)
+    auto make_b = [&](const Codes &c, int u, bool live, FragB &b) __attribute__((always_inline)) {
+        const uint32_t sc = T != kBF16 ? c.s[u] : live ? c.s[0] : 0;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const uint32_t byte = (c.s[T == kBF16 ? 0 : u] >> (8 * j)) & 255u;
+            const uint32_t byte = (sc >> (8 * j)) & 255u;
             if constexpr (T == kBF16) {
                 // the conversion reads the exponent alone: 0 is 2^-127 and 255 gives NaN
                 b.f[j] = widen_bf16(c.w[j][u], __builtin_bit_cast(float, byte << 23));
@@ -1397,11 +1405,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         FragB b;
         uint4 fa[FH];
         const uint32_t sc = load_bytes<4>(rs, wn0 + FN * r);
+        const uint32_t inside = g == 0 ? (1u << (4 * (K % 8))) - 1u : 0u;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            c.w[j][0] = load_bytes<4>(rb, row_offset(wn0 + FN * r + j, N - n0, args.ldb) + kt / 2);
+            c.w[j][0] = load_bytes<4>(rb, row_offset(wn0 + FN * r + j, N - n0, args.ldb) + kt / 2) & inside;
         c.s[0] = sc;
-        make_b(c, 0, b);
+        make_b(c, 0, true, b);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -1420,6 +1429,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         }
     }
 
+    // whether this lane's half of MFMA u of the step `step` lies before K & ~7
+    auto live = [&](int step, int u) __attribute__((always_inline)) { return (K & ~7) - step * 64 - 8 * u > 16 * g; };
     uint4 fl[FH], fu[FH];
     Codes codes;
     FragB b0, b1;
@@ -1433,7 +1444,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         read_a(cur, 0, 1, fu);
         mma(0, fl, b0);
         __builtin_amdgcn_sched_barrier(0);
-        make_b(codes, 1, b1);
+        make_b(codes, 1, live(4 * ln + t, 1), b1);
         read_a(cur, 1, 0, fl);
         mma(1, fu, b0);
         __builtin_amdgcn_sched_barrier(0);
@@ -1450,7 +1461,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         read_a(nxt, 0, 0, fl);
         read_b(t < 3 ? line : other, (t + 1) & 3, codes);
         mma(1, fu, b1);
-        make_b(codes, 0, b0);
+        make_b(codes, 0, live(4 * ln + t + 1, 0), b0);
         __builtin_amdgcn_sched_barrier(0);
     };
     auto whole_line = [&](LineB &line, LineB &other, int ln) __attribute__((always_inline)) {
@@ -1467,7 +1478,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
         read_a(la0, 0, 0, fl);
         read_b(lb0, 0, codes);
-        make_b(codes, 0, b0);
+        make_b(codes, 0, live(0, 0), b0);
         int ln = 0;
         for (; ln + 1 < n_ln; ln += 2) {
             whole_line(lb0, lb1, ln);

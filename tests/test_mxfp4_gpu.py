@@ -671,3 +671,34 @@ def test_two_streams_at_once(pd, dev):
     for n, (_, _, R, S) in enumerate(cases):
         assert_close(outs[n][0], R, S, -(-K // 64), "f32", f"stream {n}")
         assert all(torch.equal(o, outs[n][0]) for o in outs[n])
+
+
+@pytest.mark.parametrize("a_kind", ["f16", "bf16"])
+@pytest.mark.parametrize("cfg", range(13))
+@pytest.mark.parametrize("K", [1, 41, 300])
+def test_a16_largest_scales_beside_the_operand(pd, dev, K, cfg, a_kind):
+    """Codes of 6 right after the last value, in a block whose scale makes them 2^129: a column's
+    result holds only the values inside, +-2^126."""
+    M, N = 20, 37
+    gu.note(f"[case] gemm_a16_mxf4 largest scales K={K} cfg={cfg} {a_kind}")
+    rng = np.random.default_rng(K)
+    t, x = to_type(rng.standard_normal((M, K)) * 2.0 ** -10, a_kind)
+    codes = np.where(rng.integers(0, 2, (N, 16 * mx.blocks_of(K))) == 1, 0x91, 0x19).astype(np.uint8)
+    b = codes, np.full((mx.blocks_of(K), N), 254, np.uint8)
+    R, S = mx.product(x, mx.values(*b, K))
+    C = pd.gemm_a16_mxf4(source(t, dev, gu.round_up(K, 8) - K + 8), *stored(*b, K, dev), cfg=cfg)
+    assert_close(C, R, S, -(-K // 64) + 1, "f32", f"K={K} cfg {cfg} {a_kind}")
+
+
+@pytest.mark.parametrize("cfg", range(10))
+@pytest.mark.parametrize("K", [41, 300])
+def test_product_of_zeros_at_the_largest_scales(pd, dev, K, cfg):
+    M, N = 20, 37
+    gu.note(f"[case] gemm_mxf4 zeros at the largest scales K={K} cfg={cfg}")
+    a = random_operand(M, K, 1)
+    a[0][:, 16:], a[1][1:] = 0, 254               # zero codes from the second block on
+    b = random_operand(N, K, 2)
+    b[1][1:] = 254
+    R, S = mx.product(mx.values(*a, K), mx.values(*b, K))
+    C = pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K, cfg=cfg)
+    assert_close(C, R, S, -(-K // 64), "f32", f"K={K} cfg {cfg}")

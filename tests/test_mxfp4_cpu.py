@@ -197,3 +197,16 @@ def test_binding_refusals():
         pd.gemm_mxf4(x, u, u, u)
     with pytest.raises(TypeError):
         pd.mxf4_dequantize(u, x)
+
+
+@pytest.mark.parametrize("K, width, agree", [(32, 16, True), (33, 17, True), (33, 32, True), (64, 33, False),
+                                             (32, 32, False), (33, 16, False), (0, 1, False)])
+def test_a16_refuses_another_length(K, width, agree):
+    """Weights of another K than the activations' are refused by name, not cut to fit; those that
+    agree come as far as the check that wants tensors on a GPU."""
+    torch = pytest.importorskip("torch")
+    import precision_dense_gemm_amd as pd
+    a, codes = torch.zeros((4, K), dtype=torch.float16), torch.zeros((8, width), dtype=torch.uint8)
+    scales = torch.zeros((4, 16), dtype=torch.uint8)[:, :8]
+    with pytest.raises(ValueError, match="GPU" if agree else "disagree on K|fewer than K"):
+        pd.gemm_a16_mxf4(a, codes, scales)

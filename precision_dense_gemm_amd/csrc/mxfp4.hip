@@ -393,8 +393,11 @@ struct DequantArgs {
 // Values back from codes and scales.  A lane makes 16 bytes of a row (4 or 8 values), so every
 // store of a wave is a run of 1 KB; a workgroup of 4 waves takes 4 * kRpw rows of that span,
 // whose scales it first reads into LDS, a run of rows per block.  The stores are non-temporal
-// (8192 x 8192 to bf16 25 us and not 35).
-template <int T, int kRpw>
+// where they fill whole lines (8192 x 8192 to f16 24.8 us and not 25.6, 3000 x 5120 to fp32
+// 11.1 and not 11.7); rows that start inside a line share it, and such pieces are left to the L2
+// to join (2999 x 5003 to fp32 12.9 and not 16.8, to bf16 8.3 and not 9.0).
+// (kLines: dst's rows start on 128-byte lines.)
+template <int T, int kRpw, bool kLines>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(DequantArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using Elem = typename ElemOf<T>::type;
@@ -440,7 +443,10 @@ __global__ __launch_bounds__(256) void mx_dequant_kernel(DequantArgs args) {
             typedef vec_t packed_t __attribute__((aligned(sizeof(Elem))));   // the element's alignment only
             vec_t v;
             __builtin_memcpy(&v, e, 16);
-            __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
+            if constexpr (kLines)
+                __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
+            else
+                *reinterpret_cast<packed_t *>(p) = v;
         } else {
 #pragma unroll
             for (int x = 0; x < kVals; ++x)
@@ -1586,6 +1592,12 @@ int launch_quant(const QuantArgs &base, void *stream) {
                stream);
 }
 
+template <int T>
+const void *dequant_ptr(bool lines) {
+    return lines ? reinterpret_cast<const void *>(&mx_dequant_kernel<T, 4, true>)
+                 : reinterpret_cast<const void *>(&mx_dequant_kernel<T, 4, false>);
+}
+
 struct Config {
     int bm, bn, threads;
 };
@@ -1792,10 +1804,12 @@ int pdgemm_mxf4_dequantize(int64_t rows, int64_t K, const uint8_t *q, int64_t ld
     rc = check_mx_memory(q, ldq, scales, lds);
     if (rc == PDGEMM_OK) rc = check_plain(dst, ldd, dst_type);
     if (rc != PDGEMM_OK) return rc;
-    DequantArgs args = {q, scales, dst, ldq / 2, lds, ldd, (int)rows, (int)K, (int)cdiv(K, 64 * 16 / elem_size(dst_type))};
-    const void *fn = dst_type == kF32   ? reinterpret_cast<const void *>(&mx_dequant_kernel<kF32, 4>)
-                     : dst_type == kF16 ? reinterpret_cast<const void *>(&mx_dequant_kernel<kF16, 4>)
-                                        : reinterpret_cast<const void *>(&mx_dequant_kernel<kBF16, 4>);
+    const int size = elem_size(dst_type);
+    DequantArgs args = {q, scales, dst, ldq / 2, lds, ldd, (int)rows, (int)K, (int)cdiv(K, 64 * 16 / size)};
+    const bool lines = (ldd * size) % 128 == 0 && ((uintptr_t)dst & 127) == 0;
+    const void *fn = dst_type == kF32   ? dequant_ptr<kF32>(lines)
+                     : dst_type == kF16 ? dequant_ptr<kF16>(lines)
+                                        : dequant_ptr<kBF16>(lines);
     return run(fn, cdiv(rows, 16) * args.tiles_k, 256, &args, stream);
 }
 

@@ -475,6 +475,7 @@ struct MxArgs {
     int64_t ldc;         // elements
     int M, N, K;
     int tiles_m, tiles_n;
+    bool plain;          // C through the L2 (the tile kernels; see plain_stores)
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int range) {
@@ -814,7 +815,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
 
-    // C, non-temporal.  Register e of lane l in block (i, j): row FM (8 (e / 4) + 4 h + e % 4)
+    // C.  Register e of lane l in block (i, j): row FM (8 (e / 4) + 4 h + e % 4)
     // + i, column FN (l % 32) + j of the wave's tile, so a store of a lane's FN columns by 32
     // lanes is a run of WN columns of one row.
     typedef Out vec_t __attribute__((ext_vector_type(FN)));
@@ -822,8 +823,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
     const int row0 = m0 + wm0 + FM * 4 * h, col0 = n0 + wn0 + FN * r;
     Out *const c_lane = static_cast<Out *>(args.C) + (int64_t)row0 * args.ldc + col0;
     const int rows_left = M - row0, cols_left = N - col0;
-    auto store_all = [&](auto interior_c) __attribute__((always_inline)) {
-        constexpr bool kInterior = decltype(interior_c)::value;
+    auto store_all = [&](auto interior_c, auto plain_c) __attribute__((always_inline)) {
+        constexpr bool kInterior = decltype(interior_c)::value, kPlain = decltype(plain_c)::value;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
 #pragma unroll
@@ -834,7 +835,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
 #pragma unroll
                 for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
                 if (kInterior || (row < rows_left && FN <= cols_left)) {
-                    __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
+                    if constexpr (kPlain)
+                        *reinterpret_cast<packed_t *>(p) = v;
+                    else
+                        __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
                 } else if (row < rows_left) {
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
@@ -842,10 +846,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
                 }
             }
     };
-    if (m0 + BM <= M && n0 + BN <= N)
-        store_all(std::true_type{});
-    else
-        store_all(std::false_type{});
+    if (args.plain) {
+        // (the markers keep the compiler from joining these stores with the others')
+        asm volatile("; C through the L2" ::: "memory");
+        store_all(std::false_type{}, std::true_type{});
+        asm volatile("; C through the L2, end" ::: "memory");
+    } else if (m0 + BM <= M && n0 + BN <= N) {
+        store_all(std::true_type{}, std::false_type{});
+    } else {
+        store_all(std::false_type{}, std::false_type{});
+    }
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1495,15 +1505,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
 
-    // C, non-temporal.  Register e of lane l in block (i, j): row 16 i + 4 (l / 16) + e, column
+    // C.  Register e of lane l in block (i, j): row 16 i + 4 (l / 16) + e, column
     // FN (l % 16) + j of the wave's tile: a store writes runs of WN columns of four rows
     typedef Out vec_t __attribute__((ext_vector_type(FN)));
     typedef vec_t packed_t __attribute__((aligned(sizeof(Out))));
     const int row0 = m0 + wm0 + 4 * g, col0 = n0 + wn0 + FN * r;
     Out *const c_lane = static_cast<Out *>(args.C) + (int64_t)row0 * args.ldc + col0;
     const int rows_left = M - row0, cols_left = N - col0;
-    auto store_all = [&](auto interior_c) __attribute__((always_inline)) {
-        constexpr bool kInterior = decltype(interior_c)::value;
+    auto store_all = [&](auto interior_c, auto plain_c) __attribute__((always_inline)) {
+        constexpr bool kInterior = decltype(interior_c)::value, kPlain = decltype(plain_c)::value;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -1514,7 +1524,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
 #pragma unroll
                 for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
                 if (kInterior || (row < rows_left && FN <= cols_left)) {
-                    __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
+                    if constexpr (kPlain)
+                        *reinterpret_cast<packed_t *>(p) = v;
+                    else
+                        __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
                 } else if (row < rows_left) {
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
@@ -1522,10 +1535,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
                 }
             }
     };
-    if (m0 + BM <= M && n0 + BN <= N)
-        store_all(std::true_type{});
-    else
-        store_all(std::false_type{});
+    if (args.plain) {
+        // (the markers keep the compiler from joining these stores with the others')
+        asm volatile("; C through the L2" ::: "memory");
+        store_all(std::false_type{}, std::true_type{});
+        asm volatile("; C through the L2, end" ::: "memory");
+    } else if (m0 + BM <= M && n0 + BN <= N) {
+        store_all(std::true_type{}, std::false_type{});
+    } else {
+        store_all(std::false_type{}, std::false_type{});
+    }
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1688,6 +1707,17 @@ int pick_tile(int64_t M, int64_t N, double dearer) {
     return large <= small ? 0 : 1;
 }
 
+// How the tile kernels store C.  Non-temporal stores leave the L2 to A and B (4096^3 to bf16
+// 33.8 us and not 34.3) and are not held up in it at the kernel's end.  Rows that share lines
+// make them pieces of lines, which cost more the more there are: past 28 MB of C, about what the
+// L2s hold, such rows go through the L2, which joins them (us, plain against non-temporal:
+// 2000 x 4001 x 4096 to fp32, 32 MB, 24.1 and 26.3; 7000 x 7001 x 2000 to fp32 90 and 110; but
+// 2500^3 to fp32, 25 MB, 18.0 and 16.9).
+bool plain_stores(const void *C, int64_t M, int64_t N, int64_t ldc, int type) {
+    const bool lines = ldc * elem_size(type) % 128 == 0 && ((uintptr_t)C & 127) == 0;
+    return !lines && M * N * elem_size(type) > 28'000'000;
+}
+
 int64_t tiles(const Config &c, int64_t M, int64_t N) { return cdiv(M, c.bm) * cdiv(N, c.bn); }
 
 // gemm_mxf4.  While one round of the CUs takes all of them, small tiles, whose workgroups read
@@ -1725,7 +1755,8 @@ int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_
     // with K = 0 no operand is read: the kernels form addresses from C instead
     const uint8_t *const p = static_cast<const uint8_t *>(C);
     MxArgs args = {K ? A : p, K ? scale_a : p, K ? B : p, K ? scale_b : p, C, K ? lda / 2 : 0, K ? ldb / 2 : 0,
-                   K ? ldsa : 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, c.bm), (int)cdiv(N, c.bn)};
+                   K ? ldsa : 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, c.bm), (int)cdiv(N, c.bn),
+                   plain_stores(C, M, N, ldc, out_type)};
     const void *fn = out_type == kF32 ? mx_ptr<kF32>(cfg) : out_type == kF16 ? mx_ptr<kF16>(cfg) : mx_ptr<kBF16>(cfg);
     return run(fn, (int64_t)args.tiles_m * args.tiles_n, c.threads, &args, stream);
 }
@@ -1762,7 +1793,8 @@ int launch_a16(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t 
     const Config &c = kA16Configs[cfg];
     const uint8_t *const p = static_cast<const uint8_t *>(C);
     MxArgs args = {K ? static_cast<const uint8_t *>(A) : p, nullptr, K ? B : p, K ? scale_b : p, C, K ? 2 * lda : 0,
-                   K ? ldb / 2 : 0, 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, c.bm), (int)cdiv(N, c.bn)};
+                   K ? ldb / 2 : 0, 0, K ? ldsb : 0, ldc, (int)M, (int)N, (int)K, (int)cdiv(M, c.bm), (int)cdiv(N, c.bn),
+                   plain_stores(C, M, N, ldc, out_type)};
     const void *fn = a_type == kF16 ? a16_ptr<kF16>(cfg, out_type) : a16_ptr<kBF16>(cfg, out_type);
     return run(fn, (int64_t)args.tiles_m * args.tiles_n, c.threads, &args, stream);
 }

@@ -702,3 +702,23 @@ def test_product_of_zeros_at_the_largest_scales(pd, dev, K, cfg):
     R, S = mx.product(mx.values(*a, K), mx.values(*b, K))
     C = pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K, cfg=cfg)
     assert_close(C, R, S, -(-K // 64), "f32", f"K={K} cfg {cfg}")
+
+
+@pytest.mark.parametrize("a_kind", ["mxf4", "f16", "bf16"])
+@pytest.mark.parametrize("cfg", [0, 1])
+def test_large_outputs_whose_rows_share_lines(pd, dev, cfg, a_kind):
+    """More than 28 MB of C with an odd row stride: stored through the L2."""
+    M, N, K = 2700, 2701, 40
+    gu.note(f"[case] large C {M}x{N}x{K} cfg={cfg} {a_kind}")
+    a, b, R, S = operands(M, N, K, 60 + cfg)
+    buf, out = guarded(M, N, "f32", dev)
+    assert out.stride(0) % 32 and M * N * 4 > 28_000_000
+    if a_kind == "mxf4":
+        pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K, out=out, cfg=cfg)
+    else:
+        t, x = to_type(spread(M, K, 61), a_kind)
+        R, S = mx.product(x, mx.values(*b, K))
+        pd.gemm_a16_mxf4(source(t, dev, 8), *stored(*b, K, dev), out=out, cfg=cfg)
+    torch.cuda.synchronize()
+    check_rest(buf, M, N)
+    assert_close(out, R, S, -(-K // 64) + 1, "f32", f"{a_kind} cfg {cfg}")

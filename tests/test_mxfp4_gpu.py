@@ -722,3 +722,18 @@ def test_large_outputs_whose_rows_share_lines(pd, dev, cfg, a_kind):
     torch.cuda.synchronize()
     check_rest(buf, M, N)
     assert_close(out, R, S, -(-K // 64) + 1, "f32", f"{a_kind} cfg {cfg}")
+
+
+@pytest.mark.parametrize("K, stride", [(40, 32), (2048, 1024), (2080, 1152), (2500, 1280)])
+def test_strides_of_new_operands(pd, dev, K, stride):
+    """Rows of more than 1 KB of codes start on whole lines; the values are the same."""
+    gu.note(f"[case] new operand K={K}")
+    x = torch.randn((40, K), device=dev)
+    want = mx.quantize(x.cpu().double().numpy())
+    (codes, scales), (codes_t, _) = pd.mxf4_quantize_both(x)
+    assert codes.shape == (40, (K + 1) // 2) and codes.stride() == (stride, 1) and codes_t.stride() == (32, 1)
+    assert np.array_equal(codes.cpu().numpy(), want[0][:, :(K + 1) // 2]) and np.array_equal(scales.cpu().numpy(), want[1])
+    v = pd.mxf4_dequantize(codes, scales, K)
+    assert np.array_equal(v.cpu().double().numpy(), mx.values(*want, K))
+    R, S = mx.product(mx.values(*want, K), mx.values(*want, K))
+    assert_close(pd.gemm_mxf4(codes, scales, codes, scales, K), R, S, -(-K // 64), "f32", f"K={K}")

@@ -1036,9 +1036,15 @@ __device__ __forceinline__ uint4 widen_bf16(uint32_t w, float scale) {
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// binary32 of a scale byte, 255 included (NaN)
-__device__ __forceinline__ float scale_or_nan(uint32_t byte) {
-    return byte == 255 ? __builtin_nanf("") : scale_value(byte);
+// Byte j of v moved to where a binary32 has its exponent, which is all that the conversions read
+// of a scale (0 is 2^-127 there and 255 gives NaN): what is left beside it does not matter.
+__device__ __forceinline__ float scale_bits(uint32_t v, int j) {
+    return __builtin_bit_cast(float, j < 3 ? v << (23 - 8 * j) : v >> 1);
+}
+
+// binary32 of that scale, NaN included: a code of 1.0 converted with it
+__device__ __forceinline__ float scale_f32(float bits) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(0x22u, bits, 0)[0];
 }
 
 // How a step of 64 values of K (a line of a row of A, two blocks of B) is shared out over the
@@ -1156,16 +1162,12 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
             for (int i = 0; i < FM; ++i) fa[u][i] = slot.a[16 * i + ra][Map::chunk(u, g) ^ Map::swizzle(ra)];
         // (the scales leave the registers that the copy loads into, or the compiler would load
         // into others and wait at once to move them)
-        float scale[kSc][FN];
+        uint32_t sb[kSc];
 #pragma unroll
-        for (int u = 0; u < kSc; ++u)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const uint32_t byte = (sc.v[u] >> (8 * j)) & 255u;
-                // (the conversion of bf16 reads the exponent alone: 0 is 2^-127 and 255 gives NaN)
-                scale[u][j] = T == kBF16 ? __builtin_bit_cast(float, byte << 23) : scale_or_nan(byte);
-                asm volatile("" : "+v"(scale[u][j]));
-            }
+        for (int u = 0; u < kSc; ++u) {
+            sb[u] = sc.v[u];
+            asm volatile("" : "+v"(sb[u]));
+        }
         // the slot is read: it takes the step after the next S - 1
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         copy(step + S * W, slot, sc);
@@ -1195,16 +1197,17 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 if constexpr (T == kBF16) {
-                    const uint4 b = widen_bf16(w[j][u], scale[0][j]);
+                    const uint4 b = widen_bf16(w[j][u], scale_bits(sb[0], j));
 #pragma unroll
                     for (int i = 0; i < FM; ++i) acc[i][j] = mfma16<T>(fa[u][i], b, acc[i][j]);
                 } else {
                     const uint4 b = widen_f16(w[j][u]);
+                    const float scale = scale_f32(scale_bits(sb[u], j));
 #pragma unroll
                     for (int i = 0; i < FM; ++i) {
                         const floatx4_t p = mfma16<T>(fa[u][i], b, floatx4_t{0, 0, 0, 0});
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], scale[u][j], acc[i][j][e]);
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], scale, acc[i][j][e]);
                     }
                 }
             }
@@ -1380,13 +1383,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
         const uint32_t sc = T != kBF16 ? c.s[u] : live ? c.s[0] : 0;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const uint32_t byte = (sc >> (8 * j)) & 255u;
             if constexpr (T == kBF16) {
-                // the conversion reads the exponent alone: 0 is 2^-127 and 255 gives NaN
-                b.f[j] = widen_bf16(c.w[j][u], __builtin_bit_cast(float, byte << 23));
+                b.f[j] = widen_bf16(c.w[j][u], scale_bits(sc, j));
             } else {
                 b.f[j] = widen_f16(c.w[j][u]);
-                b.s[j] = scale_or_nan(byte);
+                b.s[j] = scale_f32(scale_bits(sc, j));
             }
         }
     };
@@ -1766,7 +1767,7 @@ int launch_mx(int cfg, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_
 // 64 x 32 13.0; one row by width 64 / 32 / 16 16384 x 4096 8.4 / 9.7 / 14.1, 8192 x 8192
 // 11.2 / 9.3 / 12.9, 4096 x 4096 6.0 / 5.1 / 4.7).  Past that, to 32 rows the widest.  A round
 // of 64 x 64 takes two fifths of one of 128 x 128 tiles, a third for f16, whose products are
-// scaled by vector instructions (K = 8192: 24 us against 61, 32 against 106), so it is taken
+// scaled by vector instructions (K = 8192: 24 us against 61, 31 against 106), so it is taken
 // for so many rounds of a K that is not short (1086 x 1004 x 456 12.4 against 8.6).
 int pick_a16(int a_type, int64_t M, int64_t N, int64_t K) {
     for (int c : {11, 10, 8, 7, 9, 6, 5, 3, 4, 2, 12})

@@ -144,6 +144,8 @@ struct QuantArgs {
 // so every load instruction reads 1 KB of one row, and a block is 4 (fp32: 8)
 // neighbouring lanes.  A workgroup of 4 waves takes 4 * kRpw rows of one span; the
 // scales go through LDS so that a block's scales of those rows are written as one run.
+// Bound by memory: 8192 x 8192 takes 24.2 us from f16 (7.0 TB/s of reads and writes) and
+// 46.4 us from fp32 (6.6); a copy of as many bytes runs at 5 to 8.5.
 template <int T, int kRpw>
 __global__ __launch_bounds__(256) void mx_quant_rows_kernel(QuantArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -231,7 +233,9 @@ __global__ __launch_bounds__(256) void mx_quant_rows_kernel(QuantArgs args) {
 // columns of one row; a column's block is in one lane's registers and a row's block in
 // 16 neighbouring lanes.  A workgroup of 8 waves takes 256 rows x 128 columns, and the
 // codes (4 bits a value) go through LDS so that both forms are written in runs of whole
-// chunks: 128 bytes per column, 64 bytes per row.
+// chunks: 128 bytes per column, 64 bytes per row.  Both forms of 4096 x 8192 bf16 take 18.2 us
+// (5.6 TB/s), the transpose alone 14.4: bound by memory and, for both, by the conversions, two
+// for every value.
 template <int T, bool kBoth>
 __global__ __launch_bounds__(512) void mx_quant_cols_kernel(QuantArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -609,6 +613,11 @@ __device__ __forceinline__ int swizzle8(int r) { return (r & 7) ^ ((r >> 3) & 1)
 // dword, which one MFMA operand register takes whole (the instruction picks the byte), and
 // a lane's results of FN fragments are neighbouring columns of C, stored together.  A
 // stage's scales are copied by the first waves, 16 rows of a block per lane.
+//
+// 8192^3 to fp32 takes 242 to 252 us by GPU (4.4 to 4.5 PFLOP/s), 1024 x 8192 x 8192 34 to 36.
+// Counters of the former: MFMAs busy 58% of the cycles, LDS 25%, no bank conflicts, operands
+// fetched past the L2s 6 times (428 MB), C written once; the clock falls to 1.7 GHz under
+// the MFMAs' load, and the stores of C at each tile's end are a tenth of the time.
 template <int BM, int BN, int WM, int WN, int OT>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -866,7 +875,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
 // registers it touches 16 lines per instruction, at about 16 bytes a clock per CU; copied in
 // whole lines, 8 lanes each, and read from LDS, 64 x 8192 x 8192 took 9.5 us and not 14.3,
 // 1 x 8192 x 8192 7.5 and not 7.7.)  Fragment i holds rows FM r + i (r = 0 .. 15), so that a lane's scales of
-// its fragments are neighbouring bytes.
+// its fragments are neighbouring bytes.  One row is bound by reading B (4.7 TB/s, a launch's
+// start and end included); 333 x 2081 x 4133, 11.6 us on 64 x 64 tiles, by the copies into LDS,
+// which read each operand once per tile of the other.
 template <int FM, int FN, int W, int OT>
 __global__ __launch_bounds__(W *kWave) void mx_few_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1068,7 +1079,10 @@ template <> struct A16Map<kF16> {
 // Few rows of 16-bit activations: the scheme of mx_few_kernel in steps of a line of A, W
 // waves with S slots each (as many as LDS holds: what is on its way bounds the rate), so W
 // neighbouring waves share a line of B.  RA: the rows of A that are staged; with eight
-// (M <= 8) a fragment's rows repeat them and LDS holds more steps.
+// (M <= 8) a fragment's rows repeat them and LDS holds more steps.  One row is bound by reading
+// B (8192 x 8192 9.3 us, 3.8 TB/s; steps of a whole line of B, 128 bytes a row, took 9.9 there,
+// 4.0 instead of 4.7 for 4096 x 4096, and 20 instead of 12.4 for 37 rows of f16); 37 x 4096 x
+// 8192 by the copies into LDS in bf16 (9.8 us) and by the vector instructions in f16 (12.4).
 template <int T, int RA, int FN, int W, int S, int OT>
 __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1256,6 +1270,10 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 //
 // Fragment j holds columns FN n + j (n = l % 16) of the wave's, so a lane's scales of its
 // fragments are one dword and its results neighbouring columns of C.
+//
+// 2048 x 8192 x 8192 takes 172 to 178 us by GPU in bf16 (1.55 to 1.6 PFLOP/s; the FP16 GEMM of
+// this library reaches 1.24 at 8192^3) and 262 to 275 in f16 (1.0).  Counters: MFMAs busy 72% of
+// the cycles in bf16, at 1.9 GHz, the waves waiting 28% of theirs, and 43% in f16, whose scaled sums cost as many cycles of vector instructions as of MFMAs.
 template <int T, int BM, int BN, int WM, int WN, int OT>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1695,9 +1713,9 @@ const void *a16_ptr(int cfg, int ot) {
 // two).  A round of the CUs costs the tiles' area; a last round that is not full 0.35 + 0.65
 // of its share (fewer CUs clock higher and get more of the L2); and the area of 128 x 128
 // tiles costs `dearer` times that of 256 x 256 ones (twice the bytes through the L2 per
-// product).  Timed at 14 shapes from 1500^3 to 8192^3 the choice is the faster one at 13, and
-// 8% off at 7000 x 7000 x 2000: e.g. (MXFP4, us, 0 against 1) 8192^3 248 and 287,
-// 3000^3 24.6 and 28.0, 2500^3 20.7 and 15.4, 1024 x 8192 x 8192 40.8 and 35.6.
+// product).  Timed at 14 shapes from 1500^3 to 8192^3 the choice is the faster one: e.g. (MXFP4,
+// us, 0 against 1) 8192^3 248 and 287, 7000 x 7001 x 2000 86 and 88, 3000^3 24.6 and 28.0,
+// 2500^3 20.7 and 15.4, 1024 x 8192 x 8192 40.8 and 35.6.
 int pick_tile(int64_t M, int64_t N, double dearer) {
     auto rounds = [](int64_t tiles, int64_t slots) {
         const double part = double(tiles % slots) / double(slots);

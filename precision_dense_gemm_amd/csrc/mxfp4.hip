@@ -834,6 +834,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
     const int rows_left = M - row0, cols_left = N - col0;
     auto store_all = [&](auto interior_c, auto plain_c) __attribute__((always_inline)) {
         constexpr bool kInterior = decltype(interior_c)::value, kPlain = decltype(plain_c)::value;
+        const int whole = FN <= cols_left ? rows_left : 0;   // rows that this lane stores FN columns of
 #pragma unroll
         for (int e = 0; e < 16; ++e)
 #pragma unroll
@@ -843,17 +844,27 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
                 vec_t v;
 #pragma unroll
                 for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
-                if (kInterior || (row < rows_left && FN <= cols_left)) {
+                if (kInterior || row < whole) {
                     if constexpr (kPlain)
                         *reinterpret_cast<packed_t *>(p) = v;
                     else
                         __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
-                } else if (row < rows_left) {
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        if (j < cols_left) p[j] = v[j];
                 }
             }
+        // a lane that holds C's last columns and some beyond: one by one, in a pass of their own
+        // (tested at every store they cost each edge tile 2 us)
+        const bool some = cols_left > 0 && cols_left < FN;
+        if (!kInterior && __builtin_amdgcn_ballot_w64(some) != 0) {
+#pragma unroll
+            for (int j = 0; j < FN - 1; ++j) {
+                const int last = some && j < cols_left ? rows_left : 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+                        if (FM * (8 * (e >> 2) + (e & 3)) + i < last) c_lane[(FM * (8 * (e >> 2) + (e & 3)) + i) * args.ldc + j] = (Out)acc[i][j][e];
+            }
+        }
     };
     if (args.plain) {
         // (the markers keep the compiler from joining these stores with the others')
@@ -1533,6 +1544,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
     const int rows_left = M - row0, cols_left = N - col0;
     auto store_all = [&](auto interior_c, auto plain_c) __attribute__((always_inline)) {
         constexpr bool kInterior = decltype(interior_c)::value, kPlain = decltype(plain_c)::value;
+        const int whole = FN <= cols_left ? rows_left : 0;   // rows that this lane stores FN columns of
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -1542,17 +1554,27 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
                 vec_t v;
 #pragma unroll
                 for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
-                if (kInterior || (row < rows_left && FN <= cols_left)) {
+                if (kInterior || row < whole) {
                     if constexpr (kPlain)
                         *reinterpret_cast<packed_t *>(p) = v;
                     else
                         __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
-                } else if (row < rows_left) {
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        if (j < cols_left) p[j] = v[j];
                 }
             }
+        // a lane that holds C's last columns and some beyond: one by one, in a pass of their own
+        // (tested at every store they cost each edge tile 2 us)
+        const bool some = cols_left > 0 && cols_left < FN;
+        if (!kInterior && __builtin_amdgcn_ballot_w64(some) != 0) {
+#pragma unroll
+            for (int j = 0; j < FN - 1; ++j) {
+                const int last = some && j < cols_left ? rows_left : 0;
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (16 * i + e < last) c_lane[(16 * i + e) * args.ldc + j] = (Out)acc[i][j][e];
+            }
+        }
     };
     if (args.plain) {
         // (the markers keep the compiler from joining these stores with the others')

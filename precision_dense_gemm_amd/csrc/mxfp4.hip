@@ -29,6 +29,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float floatx2_t __attribute__((ext_vector_type(2)));
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
 typedef int intx8_t __attribute__((ext_vector_type(8)));
+typedef unsigned int uintx2_t __attribute__((ext_vector_type(2)));
 typedef unsigned int uintx4_t __attribute__((ext_vector_type(4)));
 typedef unsigned short ushortx2_t __attribute__((ext_vector_type(2)));
 
@@ -499,6 +500,15 @@ __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) 
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// v at byte offset off, not stored where that is outside the range; kAux: cache control
+template <int kAux, typename V>
+__device__ __forceinline__ void store_bytes(__amdgpu_buffer_rsrc_t r, uint32_t off, const V &v) {
+    if constexpr (sizeof(V) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, kAux);
+    if constexpr (sizeof(V) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, kAux);
+    if constexpr (sizeof(V) == 8) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2_t, v), r, off, 0, kAux);
+    if constexpr (sizeof(V) == 16) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4_t, v), r, off, 0, kAux);
+}
+
 // n (1, 2 or 4) bytes, zero-extended
 template <int n>
 __device__ __forceinline__ uint32_t load_bytes(__amdgpu_buffer_rsrc_t r, uint32_t off) {
@@ -831,50 +841,56 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
     typedef vec_t packed_t __attribute__((aligned(sizeof(Out))));
     const int row0 = m0 + wm0 + FM * 4 * h, col0 = n0 + wn0 + FN * r;
     Out *const c_lane = static_cast<Out *>(args.C) + (int64_t)row0 * args.ldc + col0;
-    const int rows_left = M - row0, cols_left = N - col0;
-    auto store_all = [&](auto interior_c, auto plain_c) __attribute__((always_inline)) {
-        constexpr bool kInterior = decltype(interior_c)::value, kPlain = decltype(plain_c)::value;
-        const int whole = FN <= cols_left ? rows_left : 0;   // rows that this lane stores FN columns of
+    const int cols_left = N - col0;
+    if (!args.plain && m0 + BM <= M && n0 + BN <= N) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
-                const int row = FM * (8 * (e >> 2) + (e & 3)) + i;   // wave-uniform part of the row
-                Out *const p = c_lane + row * args.ldc;
                 vec_t v;
 #pragma unroll
                 for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
-                if (kInterior || row < whole) {
-                    if constexpr (kPlain)
-                        *reinterpret_cast<packed_t *>(p) = v;
-                    else
-                        __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
+                __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(c_lane + (FM * (8 * (e >> 2) + (e & 3)) + i) * args.ldc));
+            }
+    } else {
+        // An edge tile (or stores through the L2): offsets from the tile's first element, of which
+        // those past row M are outside the range, and lanes without whole FN columns are sent
+        // there.  (Tests at every store cost each such tile 1 to 2 us: 768 x 1000 x 1024 5.9 us, not
+        // 5.5, 768 x 1001 x 1024 7.2, not 5.9.)  A lane that holds C's last columns and some beyond
+        // stores them one by one afterwards.
+        constexpr int kSize = sizeof(Out), kNonTemporal = 2;
+        const auto rc = rsrc(static_cast<Out *>(args.C) + (int64_t)m0 * args.ldc + n0,
+                             (int)(((min(BM, M - m0) - 1) * args.ldc + min(BN, N - n0)) * kSize));
+        const uint32_t ldc = (uint32_t)args.ldc * kSize;
+        const uint32_t off = (uint32_t)(row0 - m0) * ldc + (uint32_t)(col0 - n0) * kSize;
+        const uint32_t whole = FN <= cols_left ? off : kOutside;
+        const auto store_edge = [&](auto aux_c) __attribute__((always_inline)) {
+            constexpr int kAux = decltype(aux_c)::value;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    vec_t v;
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
+                    store_bytes<kAux>(rc, whole + (FM * (8 * (e >> 2) + (e & 3)) + i) * ldc, v);
+                }
+            const bool some = cols_left > 0 && cols_left < FN;
+            if (__builtin_amdgcn_ballot_w64(some) != 0) {
+#pragma unroll
+                for (int j = 0; j < FN - 1; ++j) {
+                    const uint32_t one = some && j < cols_left ? off + j * kSize : kOutside;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+#pragma unroll
+                        for (int i = 0; i < FM; ++i) store_bytes<kAux>(rc, one + (FM * (8 * (e >> 2) + (e & 3)) + i) * ldc, (Out)acc[i][j][e]);
                 }
             }
-        // a lane that holds C's last columns and some beyond: one by one, in a pass of their own
-        // (tested at every store they cost each edge tile 2 us)
-        const bool some = cols_left > 0 && cols_left < FN;
-        if (!kInterior && __builtin_amdgcn_ballot_w64(some) != 0) {
-#pragma unroll
-            for (int j = 0; j < FN - 1; ++j) {
-                const int last = some && j < cols_left ? rows_left : 0;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-                        if (FM * (8 * (e >> 2) + (e & 3)) + i < last) c_lane[(FM * (8 * (e >> 2) + (e & 3)) + i) * args.ldc + j] = (Out)acc[i][j][e];
-            }
-        }
-    };
-    if (args.plain) {
-        // (the markers keep the compiler from joining these stores with the others')
-        asm volatile("; C through the L2" ::: "memory");
-        store_all(std::false_type{}, std::true_type{});
-        asm volatile("; C through the L2, end" ::: "memory");
-    } else if (m0 + BM <= M && n0 + BN <= N) {
-        store_all(std::true_type{}, std::false_type{});
-    } else {
-        store_all(std::false_type{}, std::false_type{});
+        };
+        if (args.plain)
+            store_edge(std::integral_constant<int, 0>{});
+        else
+            store_edge(std::integral_constant<int, kNonTemporal>{});
     }
 #endif  // __HIP_DEVICE_COMPILE__
 }
@@ -1562,7 +1578,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_ker
                 }
             }
         // a lane that holds C's last columns and some beyond: one by one, in a pass of their own
-        // (tested at every store they cost each edge tile 2 us)
+        // (tested at every store they cost each edge tile 1 us more; the offsets of mx_tile_kernel
+        // need more registers than the 256 x 256 tile has left: 2048 x 8192 x 8192 bf16 190 us, not
+        // 178)
         const bool some = cols_left > 0 && cols_left < FN;
         if (!kInterior && __builtin_amdgcn_ballot_w64(some) != 0) {
 #pragma unroll

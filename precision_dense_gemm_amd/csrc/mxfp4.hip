@@ -503,10 +503,10 @@ __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) 
 // v at byte offset off, not stored where that is outside the range; kAux: cache control
 template <int kAux, typename V>
 __device__ __forceinline__ void store_bytes(__amdgpu_buffer_rsrc_t r, uint32_t off, const V &v) {
+    static_assert(sizeof(V) == 2 || sizeof(V) == 4 || sizeof(V) == 8, "an element of C, or two");
     if constexpr (sizeof(V) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, kAux);
     if constexpr (sizeof(V) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, kAux);
     if constexpr (sizeof(V) == 8) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2_t, v), r, off, 0, kAux);
-    if constexpr (sizeof(V) == 16) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4_t, v), r, off, 0, kAux);
 }
 
 // n (1, 2 or 4) bytes, zero-extended
@@ -850,7 +850,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
                 vec_t v;
 #pragma unroll
                 for (int j = 0; j < FN; ++j) v[j] = (Out)acc[i][j][e];
-                __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(c_lane + (FM * (8 * (e >> 2) + (e & 3)) + i) * args.ldc));
+                Out *const p = c_lane + (FM * (8 * (e >> 2) + (e & 3)) + i) * args.ldc;
+                __builtin_nontemporal_store(v, reinterpret_cast<packed_t *>(p));
             }
     } else {
         // An edge tile (or stores through the L2): offsets from the tile's first element, of which
@@ -883,7 +884,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
 #pragma unroll
-                        for (int i = 0; i < FM; ++i) store_bytes<kAux>(rc, one + (FM * (8 * (e >> 2) + (e & 3)) + i) * ldc, (Out)acc[i][j][e]);
+                        for (int i = 0; i < FM; ++i)
+                            store_bytes<kAux>(rc, one + (FM * (8 * (e >> 2) + (e & 3)) + i) * ldc, (Out)acc[i][j][e]);
                 }
             }
         };

@@ -637,13 +637,24 @@ def _mx_call(fn, args, tensors, stream):
         raise PdgemmError(rc)
 
 
-def _mx_empty(shape, dtype, device, stream):
+def _mx_empty(rows, cols, dtype, device, stream):
     """A new tensor of the stream that will write it, so that its memory is not handed out
     again before that stream is done with it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(rows, cols, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+
+
+def _mx_new_form(rows, width, row, blocks, lds, device):
+    """New codes (rows, width) in rows of `row` bytes, and scales (blocks, rows) in rows of
+    `lds`: made with their strides, which costs less than half of making and slicing them.
+    The codes' memory holds their last row whole, as the quantiser writes it; of the scales the
+    last 16 bytes are only read whole, and an allocation is of whole 16-byte granules."""
+    codes = torch.empty(rows, row, dtype=torch.uint8, device=device)
+    if row != width:
+        codes = codes.as_strided((rows, width), (row, 1))
+    return codes, torch.empty_strided((blocks, rows), (lds, 1), dtype=torch.uint8, device=device)
 
 
 def _mx_form(out, rows: int, K: int, device, stream, name: str):
@@ -665,14 +676,12 @@ def _mx_form(out, rows: int, K: int, device, stream, name: str):
     if row > 1024:
         # whole 128-byte lines, which the products copy: 2000 x 5000 x 7000 46 us and not 52
         row = _round_up(row, 128)
-    codes = _mx_empty((rows, row), torch.uint8, device, stream)
-    scales = _mx_empty((blocks, lds), torch.uint8, device, stream)
-    args = (codes.data_ptr(), 2 * row, scales.data_ptr(), lds)
-    if row != width:
-        codes = codes[:, :width]
-    if rows != lds:
-        scales = scales[:, :rows]
-    return (codes, scales), args
+    if stream is None:
+        codes, scales = _mx_new_form(rows, width, row, blocks, lds, device)
+    else:
+        with torch.cuda.stream(stream):
+            codes, scales = _mx_new_form(rows, width, row, blocks, lds, device)
+    return (codes, scales), (codes.data_ptr(), 2 * row, scales.data_ptr(), lds)
 
 
 _MX_NO_FORM = (None, 0, None, 0)
@@ -719,7 +728,7 @@ def _mx_dense_out(out, rows, cols, out_dtype, device, stream):
     """(out or a new tensor, its row stride, its type)."""
     kind = _mx_type(out_dtype if out is None else out.dtype, "the output")
     if out is None:
-        return _mx_empty((rows, cols), out_dtype, device, stream), cols, kind
+        return _mx_empty(rows, cols, out_dtype, device, stream), cols, kind
     r, c, ld = _mx_rows(out, "out")
     if (r, c) != (rows, cols):
         raise ValueError(f"out must have shape {(rows, cols)}")

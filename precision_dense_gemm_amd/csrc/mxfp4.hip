@@ -624,7 +624,7 @@ __device__ __forceinline__ int swizzle8(int r) { return (r & 7) ^ ((r >> 3) & 1)
 // a lane's results of FN fragments are neighbouring columns of C, stored together.  A
 // stage's scales are copied by the first waves, 16 rows of a block per lane.
 //
-// 8192^3 to fp32 takes 242 to 252 us by GPU (4.4 to 4.5 PFLOP/s), 1024 x 8192 x 8192 34 to 36.
+// 8192^3 to fp32 takes 242 to 260 us by GPU (4.2 to 4.5 PFLOP/s), 1024 x 8192 x 8192 34 to 37.
 // Counters of the former: MFMAs busy 58% of the cycles, LDS 25%, no bank conflicts, operands
 // fetched past the L2s 6 times (428 MB), C written once; the clock falls to 1.7 GHz under
 // the MFMAs' load, and the stores of C at each tile's end are a tenth of the time.
@@ -1300,7 +1300,7 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 // Fragment j holds columns FN n + j (n = l % 16) of the wave's, so a lane's scales of its
 // fragments are one dword and its results neighbouring columns of C.
 //
-// 2048 x 8192 x 8192 takes 172 to 178 us by GPU in bf16 (1.55 to 1.6 PFLOP/s; the FP16 GEMM of
+// 2048 x 8192 x 8192 takes 172 to 182 us by GPU in bf16 (1.5 to 1.6 PFLOP/s; the FP16 GEMM of
 // this library reaches 1.24 at 8192^3) and 262 to 275 in f16 (1.0).  Counters: MFMAs busy 72% of
 // the cycles in bf16, at 1.9 GHz, the waves waiting 28% of theirs, and 43% in f16, whose scaled sums cost as many cycles of vector instructions as of MFMAs.
 template <int T, int BM, int BN, int WM, int WN, int OT>

@@ -112,6 +112,15 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
     return v;
 }
 
+// Orders a wave's LDS accesses before and after it, across its lanes.  The LDS serves one wave's
+// accesses in the order they are issued, so this costs no instruction: it keeps the compiler,
+// which sees one lane alone, from moving a read above the other lanes' store.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // One exchange of a maximum over lanes: of 2 n values v, the lanes without `kBit` keep the
 // first n and the others the last n, each with what its partner (DPP control kDpp, which
 // flips that bit) has there.
@@ -291,12 +300,15 @@ __global__ __launch_bounds__(512) void mx_quant_cols_kernel(QuantArgs args) {
         uint32_t b[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) b[x] = scale_byte(T == kF32 ? a[x] : magnitude_bits<T>(a[x]), args.bias);
-        uint8_t *const sr = &scr[lane / 16][wave * 32];
-        *reinterpret_cast<uint16_t *>(sr + 2 * (lane & 15)) = (uint16_t)(b[0] | b[1] << 8);
+        // (copied as bytes both ways: a 16-bit store and a 32-bit read of it would be taken not to
+        // overlap)
+        uint8_t *const sr = static_cast<uint8_t *>(__builtin_assume_aligned(&scr[lane / 16][wave * 32], 16));
+        const uint16_t pair_of_scales = (uint16_t)(b[0] | b[1] << 8);
+        __builtin_memcpy(__builtin_assume_aligned(sr + 2 * (lane & 15), 2), &pair_of_scales, 2);
+        wave_lds_order();   // the block's 32 scales come from its 16 lanes
         const bool special = __builtin_amdgcn_ballot_w64(max(b[0], b[1]) == 255u) != 0;   // of any block of the wave
         uint32_t w[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) w[x] = reinterpret_cast<const uint32_t *>(sr)[x];
+        __builtin_memcpy(w, sr, 32);
 #pragma unroll
         for (int r = 0; r < 32; ++r) {
             const uint32_t byte = (w[r / 4] >> (8 * (r & 3))) & 255u;

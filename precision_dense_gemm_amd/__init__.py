@@ -581,7 +581,9 @@ def _mx_type(dtype, name: str) -> int:
 # the current stream's handle without a Stream object around it.
 
 def _mx_rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
-    """(rows, columns, row stride) of a 2-D tensor with contiguous rows."""
+    """(rows, columns, row stride) of a 2-D tensor with contiguous rows.  A single row's stride
+    says nothing (the last token of a sequence, h[:, -1, :], has the whole sequence's) and may pass
+    the longest row the library takes, so its length stands for it."""
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
@@ -589,12 +591,12 @@ def _mx_rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
-    return rows, cols, (ld if rows > 1 or ld > cols else cols)
+    return rows, cols, (ld if rows > 1 else cols)
 
 
 def _mx_operand(codes: torch.Tensor, scales: torch.Tensor, K: int | None, name: str):
-    """(rows, K, ld in values, scale row stride) of an MXFP4 operand.  An array of a single
-    row has no stride to speak of: it takes the next multiple the library accepts."""
+    """(rows, K, ld in values, scale row stride) of an MXFP4 operand.  The stride of a single
+    row is its length, up to the next multiple the library accepts."""
     if not isinstance(codes, torch.Tensor) or codes.dtype is not torch.uint8:
         raise TypeError(f"{name}'s codes must be a uint8 tensor")
     if not isinstance(scales, torch.Tensor) or scales.dtype is not torch.uint8:

@@ -210,3 +210,41 @@ def test_a16_refuses_another_length(K, width, agree):
     scales = torch.zeros((4, 16), dtype=torch.uint8)[:, :8]
     with pytest.raises(ValueError, match="GPU" if agree else "disagree on K|fewer than K"):
         pd.gemm_a16_mxf4(a, codes, scales)
+
+
+def test_a_single_row_has_no_stride(monkeypatch):
+    """The last token of a sequence, h[:, -1, :], is one row that torch strides by the whole
+    sequence (and calls contiguous, so that a copy would not mend it).  The library takes rows of
+    at most 4 MiB, so the stride of a single row is not passed on."""
+    torch = pytest.importorskip("torch")
+    import precision_dense_gemm_amd as pd
+    called = []
+    monkeypatch.setattr(pd, "_mx_call", lambda fn, args, tensors, stream: called.append(args))
+
+    def row(n, dtype):
+        t = torch.empty_strided((1, n), ((1 << 24) + 1, 1), dtype=dtype)
+        assert t.is_contiguous()
+        return t
+
+    K, N = 90, 50
+    x, x16 = row(K, torch.float32), row(K, torch.float16)
+    codes, scales = row(45, torch.uint8), torch.zeros((3, 16), dtype=torch.uint8)[:, :1]
+    one_block = row(N, torch.uint8)                      # scales of a K of one block
+    wide = torch.zeros((N, 48), dtype=torch.uint8)[:, :45], torch.zeros((3, 64), dtype=torch.uint8)[:, :N]
+    out = row(N, torch.float32)
+    room = torch.as_strided(torch.zeros(48, dtype=torch.uint8), (1, 45), (1 << 24, 1))
+    pd.mxf4_quantize(x, out=(room, scales))
+    assert called.pop()[3] == K                          # (rows, K, src, ld, type, q, ldq, ...)
+    pd.mxf4_quantize(x, out=(room, scales))
+    assert called.pop()[6] == 96
+    pd.mxf4_dequantize(codes, scales, K, out=row(K, torch.float32))
+    args = called.pop()                                  # (rows, K, q, ldq, scales, lds, dst, ldd, type)
+    assert (args[3], args[5], args[7]) == (96, 16, K)
+    pd.gemm_mxf4(codes, scales, *wide, K, out=out)
+    args = called.pop()                                  # (M, N, K, A, lda, sa, ldsa, B, ldb, sb, ldsb, C, ldc, type)
+    assert (args[4], args[6], args[8], args[10], args[12]) == (96, 16, 96, 64, N)
+    pd.gemm_a16_mxf4(x16, *wide, out=out)
+    args = called.pop()                                  # (M, N, K, A, lda, type, B, ldb, sb, ldsb, C, ldc, type)
+    assert (args[4], args[7], args[9], args[11]) == (96, 96, 64, N)
+    pd.mxf4_dequantize(torch.zeros((N, 16), dtype=torch.uint8), one_block, 32)
+    assert called.pop()[5] == 64

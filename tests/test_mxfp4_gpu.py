@@ -737,3 +737,34 @@ def test_strides_of_new_operands(pd, dev, K, stride):
     assert np.array_equal(v.cpu().double().numpy(), mx.values(*want, K))
     R, S = mx.product(mx.values(*want, K), mx.values(*want, K))
     assert_close(pd.gemm_mxf4(codes, scales, codes, scales, K), R, S, -(-K // 64), "f32", f"K={K}")
+
+
+def test_one_row_of_a_long_tensor(pd, dev):
+    """h[:, -1, :] of one sequence: one row, strided by the whole sequence, as every operand."""
+    gu.note("[case] one row of a long tensor")
+    K, N, far = 1030, 300, (1 << 22) + 16
+
+    def put(host):
+        buf = torch.full((2, far), 0, dtype=host.dtype, device=dev)
+        buf[1, :host.shape[1]] = host[0].to(dev)
+        return buf.view(1, 2, far)[:, -1, :host.shape[1]]
+
+    t, x = to_type(spread(1, K, 5), "bf16")
+    xd = put(t)
+    assert xd.stride(0) * xd.element_size() > 1 << 22 and xd.is_contiguous()
+    want = mx.quantize(x)
+    out = put(torch.zeros((1, (K + 1) // 2), dtype=torch.uint8)), torch.zeros((33, 16), dtype=torch.uint8, device=dev)[:, :1]
+    q, s = pd.mxf4_quantize(xd, out=out)
+    (b, sb), (bt, sbt) = pd.mxf4_quantize_both(xd)
+    for codes, scales in ((q, s), (b, sb)):
+        assert np.array_equal(codes.cpu().numpy(), want[0][:, :(K + 1) // 2])
+        assert np.array_equal(scales.cpu().numpy(), want[1])
+    want_t = mx.quantize(x.T)
+    assert np.array_equal(bt.cpu().numpy(), want_t[0][:, :1]) and np.array_equal(sbt.cpu().numpy(), want_t[1])
+    v = pd.mxf4_dequantize(q, s, K, out=put(torch.zeros((1, K))))
+    assert np.array_equal(v.cpu().double().numpy(), mx.values(*want, K))
+    w = random_operand(N, K, 6)
+    W = stored(*w, K, dev)
+    for got, a in ((pd.gemm_mxf4(q, s, *W, K, out=put(torch.zeros((1, N)))), mx.values(*want, K)),
+                   (pd.gemm_a16_mxf4(xd, *W, out=put(torch.zeros((1, N)))), x)):
+        assert_close(got, *mx.product(a, mx.values(*w, K)), -(-K // 64) + 1, "f32", "one row")

@@ -608,6 +608,8 @@ def _mx_operand(codes: torch.Tensor, scales: torch.Tensor, K: int | None, name: 
     elif K < 0 or 2 * width < K:
         raise ValueError(f"{name} holds fewer than K values per row")
     blocks = (K + MX_BLOCK - 1) // MX_BLOCK
+    if width > blocks * (MX_BLOCK // 2):   # (bytes that only fill the last block may be part of it)
+        raise ValueError(f"{name}'s codes and the call disagree on K")
     if have < blocks or cols < rows:
         raise ValueError(f"{name}'s scales must hold {blocks} blocks of {rows} rows")
     if rows <= 1:
@@ -786,8 +788,6 @@ def gemm_a16_mxf4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, out:
     if M <= 1:
         lda = _round_up(lda, 8)
     N, K, ldb, ldsb = _mx_operand(Bt, scale_b, K, "Bt")
-    if Bt.shape[1] > (K + MX_BLOCK - 1) // MX_BLOCK * (MX_BLOCK // 2):
-        raise ValueError("A and Bt disagree on K")   # (bytes that only fill the last block may be part of it)
     out, ldc, kind = _mx_dense_out(out, M, N, out_dtype, A.device, stream)
     args = (M, N, K, A.data_ptr(), lda, _MX_TYPES[A.dtype], Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb,
             out.data_ptr(), ldc, kind)

@@ -248,3 +248,25 @@ def test_a_single_row_has_no_stride(monkeypatch):
     assert (args[4], args[7], args[9], args[11]) == (96, 96, 64, N)
     pd.mxf4_dequantize(torch.zeros((N, 16), dtype=torch.uint8), one_block, 32)
     assert called.pop()[5] == 64
+
+
+@pytest.mark.parametrize("K, width, agree", [(32, 16, True), (33, 17, True), (33, 32, True), (64, 33, False),
+                                             (32, 32, False), (33, 16, False), (0, 1, False)])
+def test_every_operand_refuses_another_length(K, width, agree):
+    """Codes of another K than the call's (in a layer step M, N and K each stand in for another)
+    are refused by name by every call that is told K, not cut to fit."""
+    torch = pytest.importorskip("torch")
+    import precision_dense_gemm_amd as pd
+    fits = -(-K // 32) * 16
+    blocks = torch.zeros((4, 16), dtype=torch.uint8)
+    good, bad = (torch.zeros((8, w), dtype=torch.uint8) for w in (fits, width))
+    scales = blocks[:, :8]
+    calls = [lambda: pd.gemm_mxf4(bad, scales, good, scales, K), lambda: pd.gemm_mxf4(good, scales, bad, scales, K)]
+    if K:                                                # (nothing to read back or to quantise: no call to the library)
+        calls += [lambda: pd.mxf4_dequantize(bad, scales, K),
+                  lambda: pd.mxf4_quantize(torch.zeros((8, K)), out=(torch.zeros((9, 64), dtype=torch.uint8)[:8, :width], scales)),
+                  lambda: pd.mxf4_quantize(torch.zeros((K, 8)), transpose=True,
+                                           out=(torch.zeros((9, 64), dtype=torch.uint8)[:8, :width], scales))]
+    for call in calls:
+        with pytest.raises(ValueError, match="GPU" if agree else "disagree on K|fewer than K"):
+            call()

@@ -357,8 +357,8 @@ int pdgemm_config_info(int cfg, int *block_m, int *block_n, int *wave_m, int *wa
  *   scales  one byte per block of 32 consecutive k of a row, 2^(byte - 127),
  *           byte 255 = NaN (the whole block).  They are stored by block: the
  *           scale of block b = k / 32 of row i at scales[b * lds + i], lds >=
- *           rows, ceil(K / 32) blocks.  (Checkpoints that keep them by row need
- *           one transposition.)
+ *           rows, ceil(K / 32) blocks.  (Scales that a checkpoint keeps by row
+ *           are transposed once, into rows of a multiple of 16 bytes.)
  * The value of element (i, k) is e2m1(code) * 2^(byte - 127).  This is the
  * MXFP4 of the OCP Microscaling Formats (MX) Specification v1.0.  K is any
  * length: the last block of a row may be short.  The pages stop at integer

@@ -27,9 +27,12 @@ scale_b[j] as float32, or rounded to float16.
 MXFP4 operands (microscaled 4-bit floating point) are a pair of uint8 tensors:
 packed codes (rows, ceil(K/2)), two e2m1 values per byte with the even k in the
 low nibble, and scales (ceil(K/32), rows), the e8m0 byte of each block of 32
-values stored by block (a checkpoint's scales, (rows, K/32), are transposed).
-Rows of both start on multiples of 16 bytes; mxf4_quantize allocates them so, and
-rows of more than 1 KB of codes on multiples of 128 bytes, the faster stride.
+values stored by block.  Rows of both start on multiples of 16 bytes; mxf4_quantize
+allocates them so, and rows of more than 1 KB of codes on multiples of 128 bytes,
+the faster stride.  Scales that a checkpoint keeps by row, (rows, K/32), are
+transposed once into such rows:
+    scales = torch.empty(K // 32, (rows + 15) // 16 * 16, dtype=torch.uint8, device="cuda")[:, :rows]
+    scales.copy_(by_row.t())
 """
 from __future__ import annotations
 

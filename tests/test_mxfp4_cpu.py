@@ -270,3 +270,12 @@ def test_every_operand_refuses_another_length(K, width, agree):
     for call in calls:
         with pytest.raises(ValueError, match="GPU" if agree else "disagree on K|fewer than K"):
             call()
+
+
+@built
+def test_alignment_message_names_the_operands():
+    # scales of 4 bits' blocks have a stricter rule than the dequantizing epilogue's
+    L = ctypes.CDLL(LIB)
+    L.pdgemm_strerror.restype = ctypes.c_char_p
+    message = L.pdgemm_strerror(codes()["PDGEMM_EALIGN"]).decode()
+    assert "MXFP4 codes and scales" in message and "rows of a multiple of 16 bytes" in message

@@ -768,3 +768,22 @@ def test_one_row_of_a_long_tensor(pd, dev):
     for got, a in ((pd.gemm_mxf4(q, s, *W, K, out=put(torch.zeros((1, N)))), mx.values(*want, K)),
                    (pd.gemm_a16_mxf4(xd, *W, out=put(torch.zeros((1, N)))), x)):
         assert_close(got, *mx.product(a, mx.values(*w, K)), -(-K // 64) + 1, "f32", "one row")
+
+
+@pytest.mark.parametrize("N", [48, 50])
+def test_scales_of_a_checkpoint(pd, dev, N):
+    """Scales kept by row, (N, K / 32): their transpose, in rows of a multiple of 16 bytes.  As
+    it comes, packed, it is refused where N is not such a multiple."""
+    M, K = 20, 320
+    gu.note(f"[case] scales of a checkpoint N={N}")
+    t, x = to_type(spread(M, K, 5), "bf16")
+    codes, by_block = random_operand(N, K, 6)
+    B, by_row = torch.from_numpy(codes).to(dev), torch.from_numpy(by_block.T.copy()).to(dev)
+    packed = by_row.t().contiguous()
+    if N % 16:
+        with pytest.raises(pd.PdgemmError, match="MXFP4 codes and scales .* 16"):
+            pd.gemm_a16_mxf4(t.to(dev), B, packed)
+    scales = torch.empty((K // 32, gu.round_up(N, 16)), dtype=torch.uint8, device=dev)[:, :N]
+    scales.copy_(by_row.t())
+    R, S = mx.product(x, mx.values(codes, by_block, K))
+    assert_close(pd.gemm_a16_mxf4(t.to(dev), B, scales), R, S, -(-K // 64) + 1, "f32", f"N={N}")

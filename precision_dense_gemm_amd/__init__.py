@@ -33,6 +33,10 @@ the faster stride.  Scales that a checkpoint keeps by row, (rows, K/32), are
 transposed once into such rows:
     scales = torch.empty(K // 32, (rows + 15) // 16 * 16, dtype=torch.uint8, device="cuda")[:, :rows]
     scales.copy_(by_row.t())
+
+No call here records a graph: a result carries no gradient, whatever its inputs ask for.
+A layer that trains computes dX and dW by calls of its own (see mxf4_quantize_both), for
+example from a torch.autograd.Function.
 """
 from __future__ import annotations
 
@@ -726,7 +730,10 @@ def mxf4_quantize(x: torch.Tensor, transpose: bool = False, scale_rule: str = "f
 
 def mxf4_quantize_both(x: torch.Tensor, scale_rule: str = "floor", out=None, stream=None):
     """((codes, scales), (codes_t, scales_t)): mxf4_quantize of x and of its transpose, from one
-    read of x.  out: a pair of such pairs to write."""
+    read of x.  out: a pair of such pairs to write.
+
+    A linear layer Y = X W^T takes both forms of X, W and G = dL/dY: Y contracts X and W along K,
+    dX = G W takes G's rows and W's transpose, dW = G^T X both transposes."""
     first, second = (None, None) if out is None else out
     return _mx_quantize(x, True, True, scale_rule, first, second, stream)
 

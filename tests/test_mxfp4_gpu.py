@@ -787,3 +787,14 @@ def test_scales_of_a_checkpoint(pd, dev, N):
     scales.copy_(by_row.t())
     R, S = mx.product(x, mx.values(codes, by_block, K))
     assert_close(pd.gemm_a16_mxf4(t.to(dev), B, scales), R, S, -(-K // 64) + 1, "f32", f"N={N}")
+
+
+def test_results_carry_no_graph(pd, dev):
+    """The calls are not differentiable operations: results of tensors that require gradients do
+    not, and the documentation says so."""
+    gu.note("[case] no graph")
+    x = torch.randn((20, 64), device=dev, dtype=torch.float16, requires_grad=True)
+    q, s = pd.mxf4_quantize(x)
+    for out in (pd.mxf4_dequantize(q, s, 64), pd.gemm_mxf4(q, s, q, s, 64), pd.gemm_a16_mxf4(x, q, s)):
+        assert not out.requires_grad and out.grad_fn is None
+    assert "gradient" in pd.__doc__

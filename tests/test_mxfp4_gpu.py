@@ -798,3 +798,28 @@ def test_results_carry_no_graph(pd, dev):
     for out in (pd.mxf4_dequantize(q, s, 64), pd.gemm_mxf4(q, s, q, s, 64), pd.gemm_a16_mxf4(x, q, s)):
         assert not out.requires_grad and out.grad_fn is None
     assert "gradient" in pd.__doc__
+
+
+@pytest.mark.parametrize("rule", ["floor", "fit"])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_quantize_every_16_bit_value(pd, dev, kind, rule):
+    """Every value of a 16-bit type under scales from one end of its range to the other: in
+    each row the first value sets the scale, and the 31 others run over all that are not larger."""
+    bits = np.arange(0, 0x7C00 if kind == "f16" else 0x7F80, dtype=np.uint16)
+    vals = torch.from_numpy(bits.view(np.int16)).view(TYPES[kind]).double().numpy()
+    rows = []
+    for top in vals[[1, 5, len(vals) // 5, len(vals) // 3, len(vals) // 2, 3 * len(vals) // 4, -700, -200, -1]]:
+        below = vals[vals <= top]
+        below = np.concatenate([below, np.full(-len(below) % 31, top)]).reshape(-1, 31)
+        rows.append(np.hstack([np.full((len(below), 1), top), below]))
+    rows = np.vstack(rows)
+    t = torch.from_numpy(rows * np.where(np.random.default_rng(4).random(rows.shape) < 0.5, -1, 1)).to(TYPES[kind])
+    gu.note(f"[case] quantize every 16-bit value {kind} {rule} {tuple(t.shape)}")
+    want = mx.quantize(t.double().numpy(), rule)
+    assert set(np.unique(np.concatenate([want[0] & 15, want[0] >> 4]))) == set(range(16))
+    q, s = pd.mxf4_quantize(t.to(dev), scale_rule=rule)
+    qt, st = pd.mxf4_quantize(t.t().contiguous().to(dev), transpose=True, scale_rule=rule)
+    (b, sb), _ = pd.mxf4_quantize_both(t.to(dev), scale_rule=rule)
+    for name, codes, scales in (("rows", q, s), ("transpose", qt, st), ("both", b, sb)):
+        assert np.array_equal(scales.cpu().numpy(), want[1]), name
+        assert np.array_equal(codes.cpu().numpy(), want[0]), name

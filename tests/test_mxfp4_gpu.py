@@ -823,3 +823,169 @@ def test_quantize_every_16_bit_value(pd, dev, kind, rule):
     for name, codes, scales in (("rows", q, s), ("transpose", qt, st), ("both", b, sb)):
         assert np.array_equal(scales.cpu().numpy(), want[1]), name
         assert np.array_equal(codes.cpu().numpy(), want[0]), name
+
+
+# ---- the corners of what the header allows ----
+
+def off_by_one(rows, cols, kind, dev, value=7.0):
+    """A view whose first element has only its own alignment, in rows of an odd stride."""
+    ld = cols + 3 + (cols % 2)                       # odd
+    flat = torch.full((rows * ld + ld + 1,), value, dtype=TYPES[kind], device=dev)
+    return flat, torch.as_strided(flat, (rows, cols), (ld, 1), 1)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_elements_aligned_sources_and_results(pd, dev, kind):
+    """Dense arrays need only their element's alignment, the first element's too."""
+    gu.note(f"[case] element alignment {kind}")
+    rows, K = 300, 1029
+    t, x = to_type(spread(rows, K, 21), kind)
+    _, src = off_by_one(rows, K, kind, dev, float("nan"))
+    src.copy_(t)
+    assert src.data_ptr() % 16 == TYPES[kind].itemsize
+    want, want_t = mx.quantize(x), mx.quantize(x.T)
+    (q, s), (qt, st) = pd.mxf4_quantize_both(src)
+    q1, s1 = pd.mxf4_quantize(src)
+    for codes, scales, ref in ((q, s, want), (q1, s1, want), (qt, st, want_t)):
+        assert np.array_equal(codes.cpu().numpy(), ref[0][:, :codes.shape[1]])
+        assert np.array_equal(scales.cpu().numpy(), ref[1])
+    flat, out = off_by_one(rows, K, kind, dev)
+    pd.mxf4_dequantize(q, s, K, out=out)
+    # (a value of few bits is exact in each type; spread's are far from the types' ends)
+    assert np.array_equal(out.cpu().double().numpy(), mx.values(*want, K))
+    out.fill_(7.0)
+    assert bool((flat == 7.0).all())
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("cfg", range(13))
+def test_elements_aligned_products(pd, dev, cfg, kind):
+    M, N, K = 261, 135, 328
+    gu.note(f"[case] element-aligned C cfg={cfg} {kind}")
+    a, b, R, S = operands(M, N, K, 22)
+    for what, steps in (("mxf4", -(-K // 64)), ("f16", -(-K // 64) + 1), ("bf16", -(-K // 64) + 1)):
+        flat, out = off_by_one(M, N, kind, dev)
+        if what == "mxf4":
+            if cfg >= pd.mxf4_num_configs():
+                continue
+            pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K, out=out, cfg=cfg)
+        else:
+            t, x = to_type(spread(M, K, 23), what)
+            R, S = mx.product(x, mx.values(*b, K))
+            pd.gemm_a16_mxf4(source(t, dev, 8), *stored(*b, K, dev), out=out, cfg=cfg)
+        assert_close(out, R, S, steps, kind, f"{what} cfg {cfg}")
+        out.fill_(7.0)
+        assert bool((flat == 7.0).all()), "stores outside the M x N block"
+
+
+def on_gpu(codes, scales, K, dev):
+    """float64 values on the GPU of codes and scales there (no NaN scales)."""
+    table = torch.tensor(list(mx.E2M1) + [-v for v in mx.E2M1], dtype=torch.float64, device=dev)
+    nib = torch.stack((codes & 15, codes >> 4), dim=2).view(codes.shape[0], -1)[:, :K]
+    scale = ((scales.t().to(torch.int64) - 127 + 1023) << 52).view(torch.float64)
+    return table[nib.to(torch.int64)] * scale.repeat_interleave(32, dim=1)[:, :K]
+
+
+def random_on_gpu(rows, K, seed, dev):
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    nb = mx.blocks_of(K)
+    codes = torch.randint(0, 256, (rows, 16 * nb), dtype=torch.uint8, device=dev, generator=g)
+    scales = torch.randint(122, 132, (nb, gu.round_up(rows, 16)), dtype=torch.uint8, device=dev, generator=g)
+    return codes, scales[:, :rows]
+
+
+def assert_close_on_gpu(C, va, vb, steps, what):
+    R, S = va @ vb.t(), va.abs() @ vb.abs().t()
+    bad = ~((C.double() - R).abs() <= steps * 2.0 ** -22 * S)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} off, first at {torch.nonzero(bad)[0].tolist()}"
+
+
+@pytest.mark.parametrize("M, N", [((1 << 22), 5), (9, 1 << 20)], ids=["rows", "columns"])
+def test_most_rows(pd, dev, M, N):
+    """Operands of 4 Mi rows (their scales' rows are 4 MiB) and C's rows of 4 MiB."""
+    K = 40
+    gu.note(f"[case] most rows {M}x{N}x{K}")
+    a, b = random_on_gpu(M, K, 1, dev), random_on_gpu(N, K, 2, dev)
+    va, vb = on_gpu(*a, K, dev), on_gpu(*b, K, dev)
+    assert_close_on_gpu(pd.gemm_mxf4(a[0], a[1], b[0], b[1], K), va, vb, 1, "mxf4")
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device=dev).copy_(va)      # (two significant bits: exact)
+    assert_close_on_gpu(pd.gemm_a16_mxf4(x, *b), va, vb, 2, "a16")
+    with pytest.raises(pd.PdgemmError):
+        pd.mxf4_quantize(torch.zeros(((1 << 22) + 1, 1), device=dev))        # scales' rows past 4 MiB
+
+
+def test_more_rows_of_activations(pd, dev):
+    """16-bit activations have no scales: more rows than an MXFP4 operand may have."""
+    M, N, K = 5_000_001, 3, 8
+    gu.note(f"[case] more rows of activations {M}x{N}x{K}")
+    g = torch.Generator(device=dev)
+    g.manual_seed(4)
+    x = torch.randn((M, K), device=dev, generator=g).half()
+    b = random_on_gpu(N, K, 3, dev)
+    assert_close_on_gpu(pd.gemm_a16_mxf4(x, *b), x.double(), on_gpu(*b, K, dev), 2, "a16")
+
+
+def test_tallest_transpose(pd, dev):
+    """8 Mi rows quantised along themselves: a row of the transpose is 4 MiB of codes."""
+    rows, K = 1 << 23, 3
+    gu.note(f"[case] tallest transpose {rows}x{K}")
+    g = torch.Generator(device=dev)
+    g.manual_seed(5)
+    x = torch.randn((rows, K), device=dev, generator=g).bfloat16()
+    qt, st = pd.mxf4_quantize(x, transpose=True)
+    assert qt.shape == (K, rows // 2)
+    # a row along K of the copied transpose, in pieces of 2 MiB of values, which are rows of their own
+    pieces = x.t().contiguous().view(4 * K, rows // 4)
+    q, s = pd.mxf4_quantize(pieces)
+    assert torch.equal(qt.reshape(4 * K, rows // 8), q)
+    blocks = rows // 32
+    assert torch.equal(st.t().reshape(K, 4, blocks // 4), s.t().reshape(K, 4, blocks // 4))
+    v = pd.mxf4_dequantize(qt[:, :rows // 16], st[:rows // 256], rows // 8, out_dtype=torch.bfloat16)
+    assert torch.equal(v, pd.mxf4_dequantize(q, s, rows // 4, out_dtype=torch.bfloat16)[::4, :rows // 8])
+
+
+@pytest.mark.parametrize("cfg", [None, 0, 1, 2])
+def test_longest_rows(pd, dev, cfg):
+    """Rows of 4 MiB: 8 Mi values of K in MXFP4, 2 Mi of 16-bit activations."""
+    M, N, K = 3, 5, 1 << 23
+    gu.note(f"[case] longest rows {M}x{N}x{K} cfg={cfg}")
+    a, b = random_on_gpu(M, K, 6, dev), random_on_gpu(N, K, 7, dev)
+    assert_close_on_gpu(pd.gemm_mxf4(*a, *b, K, cfg=cfg), on_gpu(*a, K, dev), on_gpu(*b, K, dev), K // 64, "mxf4")
+    K = 1 << 21
+    b = random_on_gpu(N, K, 7, dev)
+    g = torch.Generator(device=dev)
+    g.manual_seed(8)
+    for dtype in (torch.float16, torch.bfloat16):
+        x = torch.randn((M, K), device=dev, generator=g).to(dtype)
+        assert_close_on_gpu(pd.gemm_a16_mxf4(x, *b, cfg=cfg), x.double(), on_gpu(*b, K, dev), K // 64 + 1, f"a16 {dtype}")
+
+
+@pytest.mark.parametrize("a_kind", ["mxf4", "f16", "bf16"])
+@pytest.mark.parametrize("cfg", range(13))
+def test_nan_and_infinity_stay_in_their_rows(pd, dev, cfg, a_kind):
+    """On every tile: NaN blocks and non-finite activations reach their row or column of C, and
+    the rest is as without them."""
+    M, N, K = 70, 75, 300
+    gu.note(f"[case] NaN on every tile cfg={cfg} {a_kind}")
+    a, b, _, _ = operands(M, N, K, 33)
+    b[1][0, 3] = b[1][-1, N - 1] = b[1][4, 40] = 255
+    b[0][3, :16] = 0                                 # a NaN scale over zero codes is NaN too
+    vb = mx.values(*b, K)
+    if a_kind == "mxf4":
+        if cfg >= pd.mxf4_num_configs():
+            return
+        a[1][0, 1] = a[1][-1, M - 1] = 255
+        va = mx.values(*a, K)
+        C = pd.gemm_mxf4(*stored(*a, K, dev), *stored(*b, K, dev), K, cfg=cfg)
+    else:
+        x = spread(M, K, 34)
+        x[1, 2], x[M - 1, K - 1], x[17, 130] = np.nan, np.inf, -np.inf
+        t, va = to_type(x, a_kind)
+        C = pd.gemm_a16_mxf4(source(t, dev, gu.round_up(K, 8) - K + 8), *stored(*b, K, dev), cfg=cfg)
+    got = C.cpu().double().numpy()
+    rows, cols = ~np.isfinite(va).all(axis=1), np.isnan(vb).any(axis=1)
+    assert not np.isfinite(got[rows]).any() and np.isnan(got[:, cols]).all()
+    R, S = mx.product(va[~rows], vb[~cols])
+    tol = (-(-K // 64) + 1) * 2.0 ** -22 * S
+    assert (np.abs(got[~rows][:, ~cols] - R) <= tol).all()

@@ -369,7 +369,8 @@ int pdgemm_config_info(int cfg, int *block_m, int *block_n, int *wave_m, int *wa
  * Alignment: codes and scales 16-byte aligned, ld a multiple of 32 (16 bytes),
  * lds a multiple of 16.  Dense arrays (the source of the quantiser, the result
  * of the dequantiser, C) need only their element's alignment and any ld >= the
- * row.  A row of any array spans at most 4 MiB.  As elsewhere, the 16-byte
+ * row.  A row of any array spans at most 4 MiB, a row of scales too: an operand
+ * has at most 4194304 rows.  As elsewhere, the 16-byte
  * granule that holds the last element of a row (of codes or of scales) may be
  * read whole, and values outside the operand never reach a stored result,
  * whatever their bits.
@@ -408,8 +409,9 @@ int pdgemm_mxf4_quantize(int64_t rows, int64_t K, const void *src, int64_t ld, i
 
 /* The values of an MXFP4 operand, to a dense row-major dst of dst_type: exact
  * in binary32 (a magnitude of 2^128 and above is infinite; of finite values the
- * quantiser makes one only by FIT, from magnitudes of 1.75 * 2^127 and above), rounded to nearest even for the 16-bit types (binary16:
- * overflow gives infinity). */
+ * quantiser makes one only by FIT, from magnitudes of 1.75 * 2^127 and above),
+ * rounded to nearest even for the 16-bit types (binary16: overflow gives
+ * infinity). */
 int pdgemm_mxf4_dequantize(int64_t rows, int64_t K, const uint8_t *q, int64_t ldq, const uint8_t *scales,
                            int64_t lds, void *dst, int64_t ldd, int dst_type, void *stream);
 
@@ -433,9 +435,11 @@ int pdgemm_mxf4_pick(int64_t M, int64_t N, int64_t K);
 
 /* C = A * B of 16-bit A (a_type PDGEMM_F16 or PDGEMM_BF16, row-major, rows of a
  * multiple of 16 bytes, 16-byte aligned) and MXFP4 B: weights kept in 4 bits
- * under activations that are not quantised.  B's values enter exactly (those of
- * 2^128 and above may be infinite); sums and
- * rounding as in gemm_mxf4, explicit tiles as pdgemm_mxf4_cfg. */
+ * under activations that are not quantised.  A has no scales, so the row limit
+ * of MXFP4 operands is not A's.  B's values enter exactly (those of 2^128 and
+ * above may be infinite); sums and rounding as in gemm_mxf4, with
+ * ceil(K / 64) + 1 in place of ceil(K / 64) (the values past the last multiple
+ * of 8 are added by a step of their own); explicit tiles as pdgemm_mxf4_cfg. */
 int gemm_a16_mxf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                   int64_t ldb, const uint8_t *scale_b, int64_t ldsb, void *C, int64_t ldc, int out_type,
                   void *stream);

@@ -917,8 +917,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void mx_tile_kern
 // whole lines, 8 lanes each, and read from LDS, 64 x 8192 x 8192 took 9.5 us and not 14.3,
 // 1 x 8192 x 8192 7.5 and not 7.7.)  Fragment i holds rows FM r + i (r = 0 .. 15), so that a lane's scales of
 // its fragments are neighbouring bytes.  One row is bound by reading B (4.7 TB/s, a launch's
-// start and end included); 333 x 2081 x 4133, 11.6 us on 64 x 64 tiles, by the copies into LDS,
-// which read each operand once per tile of the other.
+// start and end included).  333 x 2081 x 4133 takes 11.6 us on 64 x 64 tiles, 198 workgroups that
+// copy 278 KB each, every operand once per tile of the other; its counters show no unit near its
+// rate (MFMAs busy 6% of the SIMD cycles, LDS 8%, the waves waiting 32% of theirs): three waves
+// a CU, each with its own chain of copies.
 template <int FM, int FN, int W, int OT>
 __global__ __launch_bounds__(W *kWave) void mx_few_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1051,8 +1053,9 @@ __global__ __launch_bounds__(W *kWave) void mx_few_kernel(MxArgs args) {
 // 16-bit activations times MXFP4 weights.  The codes become the 16-bit type exactly
 // (e2m1 values need two significant bits); an MFMA of 32 values of K covers one block,
 // and its result is scaled by the block's 2^(byte - 127) as it is added to the sum, in
-// binary32: with the scale in the 16-bit operand instead, an f16 weight below 2^-24
-// would vanish.
+// binary32.  (With the scale in an f16 operand instead, weights are exact for scales of
+// 2^-23 .. 2^13, bytes 104 .. 140, only: half of 2^-23 is f16's least value, and 6 * 2^14 is
+// above its largest.  The kernels take any byte and have one path.)
 template <int T>
 __device__ __forceinline__ floatx4_t mfma16(const uint4 &a, const uint4 &b, const floatx4_t &c) {
     if constexpr (T == kF16) {
@@ -1122,8 +1125,10 @@ template <> struct A16Map<kF16> {
 // neighbouring waves share a line of B.  RA: the rows of A that are staged; with eight
 // (M <= 8) a fragment's rows repeat them and LDS holds more steps.  One row is bound by reading
 // B (8192 x 8192 9.3 us, 3.8 TB/s; steps of a whole line of B, 128 bytes a row, took 9.9 there,
-// 4.0 instead of 4.7 for 4096 x 4096, and 20 instead of 12.4 for 37 rows of f16); 37 x 4096 x
-// 8192 by the copies into LDS in bf16 (9.8 us) and by the vector instructions in f16 (12.4).
+// 4.0 instead of 4.7 for 4096 x 4096, and 20 instead of 12.4 for 37 rows of f16).  37 x 4096 x
+// 8192 takes 9.8 us in bf16 and 12.4 in f16, whose widening and scaling need 1.8 times the vector
+// instructions; B is copied three times, once per tile of 16 rows, and the waves wait 37 and 41%
+// of their cycles.
 template <int T, int RA, int FN, int W, int S, int OT>
 __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1314,7 +1319,10 @@ __global__ __launch_bounds__(W *kWave) void a16_few_kernel(MxArgs args) {
 //
 // 2048 x 8192 x 8192 takes 172 to 182 us by GPU in bf16 (1.5 to 1.6 PFLOP/s; the FP16 GEMM of
 // this library reaches 1.24 at 8192^3) and 262 to 275 in f16 (1.0).  Counters: MFMAs busy 72% of
-// the cycles in bf16, at 1.9 GHz, the waves waiting 28% of theirs, and 43% in f16, whose scaled sums cost as many cycles of vector instructions as of MFMAs.
+// the cycles in bf16, at 1.9 GHz, the waves waiting 28% of theirs, and 43% in f16, whose scaled
+// sums cost as many cycles of vector instructions as of MFMAs.  Both spend 0.8 cycles per LDS
+// instruction on bank conflicts; another swizzle of B's lines did not move them.  A loop of
+// nothing but these MFMAs on normal values runs at 1.70 PFLOP/s in bf16 and 1.60 in f16.
 template <int T, int BM, int BN, int WM, int WN, int OT>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void a16_tile_kernel(MxArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)

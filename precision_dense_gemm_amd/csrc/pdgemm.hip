@@ -2906,7 +2906,7 @@ const char *pdgemm_strerror(int code) {
     case PDGEMM_EINVAL_LD: return "leading dimension smaller than the row length, or a row above 4 MiB";
     case PDGEMM_ENULL: return "null pointer for an operand with nonzero extent";
     case PDGEMM_EINVAL_I4: return "INT4 K, lda and ldb must be even";
-    case PDGEMM_EALIGN: 
+    case PDGEMM_EALIGN:
         return "A and B must be 16-byte aligned, A and B rows must span a multiple of 16 bytes, C and the epilogue's "
                "scales must be element-aligned; MXFP4 codes and scales must be 16-byte aligned, in rows of a multiple of "
                "16 bytes";

@@ -449,6 +449,51 @@ int pdgemm_a16_mxf4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A,
 int pdgemm_a16_mxf4_num_configs(void);
 int pdgemm_a16_mxf4_pick(int a_type, int64_t M, int64_t N, int64_t K);   /* -1 for another type */
 
+/* ---------------------------------------------------------------------------
+ * Around the products of a quantised model: the root-mean-square norm, with the
+ * residual's addition before it and the INT8 products' operand after it, and
+ * its gradients.  The pages have no such step; it is what a decoder layer does
+ * between two products ("Hand-Written PTX Tensor-Core GEMM Kernels ...",
+ * Section VI, leaves quantisation out).
+ *
+ * Every matrix is dense, row-major, with only its element's alignment and any
+ * ld >= cols; a row has at most 32768 values.  type (PDGEMM_F32, _F16 or _BF16)
+ * is that of x, residual and sum; the weight, of cols values, and the result
+ * have types of their own.  Errors, streams and ownership are those of the
+ * other entry points; an unknown type, or an eps that is negative or not
+ * finite, returns PDGEMM_EINVAL_CFG. */
+#define PDGEMM_I8 3
+
+/* h = x + residual, in binary32, rounded to `type` and written to sum (residual
+ * and sum both NULL: h = x), then with r = (mean of the row's h^2 + eps)^(-1/2)
+ *   out_type F32, F16, BF16: out = h * r * weight, rounded once (scale is not
+ *     looked at);
+ *   out_type I8: with t = h * weight in binary32 and m the row's largest |t|,
+ *     out = t * (127 * (1 / m)), each step in binary32, rounded to nearest even, and
+ *     scale[i] = m * r / 127: the A and scale_a of gemm_i8_dequant where ldo is
+ *     a multiple of 16.  A row of zeros takes zero codes and scale 0, one with an
+ *     infinity or a NaN in t zero codes and scale NaN.
+ * Squares and their sum may leave binary32's range.  sum may be residual or x
+ * itself, and out x (or sum) itself where they have one type and ld. */
+int pdgemm_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual,
+                    int64_t ldr, void *sum, int64_t lds, const void *weight, int weight_type, float eps, void *out,
+                    int64_t ldo, int out_type, float *scale, void *stream);
+
+/* The gradients of y = norm(h): with n = h * r and g = dy * weight,
+ *   dx = r * (g - n * mean of the row's g * n) + dh,
+ * rounded once to `type` (that of dy, h, dh and dx): the gradient of x and of
+ * residual alike, dh being the gradient that h has from elsewhere (NULL: none);
+ *   dweight = sum over the rows of dy * n, binary32, cols values.
+ * The sums run in a fixed order.  dx may be dy or dh itself (same ld).  With
+ * rows = 0, dweight is set to zeros.  The workspace (16-byte aligned, contents
+ * undefined on return, not shared by calls that overlap) may be NULL where the
+ * size is 0. */
+int64_t pdgemm_rms_norm_backward_workspace_size(int64_t rows, int64_t cols);
+int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t lddy, const void *h, int64_t ldh,
+                             const void *dh, int64_t lddh, int type, const void *weight, int weight_type, float eps,
+                             void *dx, int64_t lddx, float *dweight, void *workspace, int64_t workspace_bytes,
+                             void *stream);
+
 /* Static message for a return code (never NULL): the PDGEMM_E* codes above,
  * or hipGetErrorString() for a positive hipError_t.  Part of the error
  * convention of "Chapter 5 · The Toolchain", Section 5.3 (every error made

@@ -139,6 +139,14 @@ lib.pdgemm_a16_mxf4_num_configs.argtypes = []
 lib.pdgemm_a16_mxf4_num_configs.restype = _i
 lib.pdgemm_a16_mxf4_pick.argtypes = [_i, _i64, _i64, _i64]
 lib.pdgemm_a16_mxf4_pick.restype = _i
+lib.pdgemm_rms_norm.argtypes = [_i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _p, _i, ctypes.c_float, _p, _i64, _i,
+                                _p, _p]
+lib.pdgemm_rms_norm.restype = _i
+lib.pdgemm_rms_norm_backward_workspace_size.argtypes = [_i64, _i64]
+lib.pdgemm_rms_norm_backward_workspace_size.restype = _i64
+lib.pdgemm_rms_norm_backward.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _i, ctypes.c_float, _p,
+                                         _i64, _p, _p, _i64, _p]
+lib.pdgemm_rms_norm_backward.restype = _i
 lib.pdgemm_strerror.argtypes = [_i]
 lib.pdgemm_strerror.restype = ctypes.c_char_p
 lib.pdgemm_version.argtypes = []
@@ -813,6 +821,121 @@ def a16_mxf4_num_configs() -> int:
 def a16_mxf4_pick(dtype: torch.dtype, M: int, N: int, K: int) -> int:
     """The tile configuration gemm_a16_mxf4 takes for activations of `dtype` and a shape."""
     return lib.pdgemm_a16_mxf4_pick(_MX_TYPES[dtype], M, N, K)
+
+
+# ---- norms ----
+
+_I8 = 3
+
+
+def _like_x(t, x, name: str):
+    """The row stride of a tensor of x's shape and type."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not x.dtype:
+        raise TypeError(f"{name} must be a tensor of x's type")
+    rows, cols, ld = _mx_rows(t, name)
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must have shape {tuple(x.shape)}")
+    return ld
+
+
+def _norm_weight(weight, cols: int) -> int:
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a tensor")
+    kind = _mx_type(weight.dtype, "weight")
+    if weight.dim() != 1 or weight.shape[0] != cols:
+        raise ValueError(f"weight must hold {cols} values")
+    if cols > 1 and weight.stride(0) != 1:
+        raise ValueError("weight must be contiguous")
+    return kind
+
+
+def _new_like(t, stream):
+    rows, cols = t.shape
+    return _mx_empty(rows, cols, t.dtype, t.device, stream)
+
+
+def _rms_norm(x, weight, eps, residual, sum_out, out, out_kind, scale, stream):
+    kind = _mx_type(x.dtype, "x")
+    rows, cols, ldx = _mx_rows(x, "x")
+    wkind = _norm_weight(weight, cols)
+    tensors = (x, weight, out) if scale is None else (x, weight, out, scale)
+    add = (None, 0, None, 0)
+    if residual is not None:
+        ldr = _like_x(residual, x, "residual")
+        if sum_out is None:
+            sum_out = _new_like(x, stream)
+        add = (residual.data_ptr(), ldr, sum_out.data_ptr(), _like_x(sum_out, x, "sum_out"))
+        tensors += (residual, sum_out)
+    elif sum_out is not None:
+        raise ValueError("sum_out holds x + residual: it takes a residual")
+    r, c, ldo = _mx_rows(out, "out")
+    if (r, c) != (rows, cols):
+        raise ValueError(f"out must have shape {(rows, cols)}")
+    _mx_call(lib.pdgemm_rms_norm, (rows, cols, x.data_ptr(), ldx, kind, *add, weight.data_ptr(), wkind, eps,
+                                   out.data_ptr(), ldo, out_kind, None if scale is None else scale.data_ptr()),
+             tensors, stream)
+    return sum_out
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+             out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+             sum_out: torch.Tensor | None = None, stream=None):
+    """y = h * weight / sqrt(mean(h^2) + eps) over the rows of h = x, or with a residual of h = x + residual
+    (rounded to x's type), then (y, h).  x (rows, cols) float32, float16 or bfloat16, at most 32768 columns;
+    y has out's dtype, else out_dtype, else x's.  sum_out takes h: it may be residual or x itself; out may be
+    x itself too."""
+    if out is None:
+        rows, cols, _ = _mx_rows(x, "x")
+        out = _mx_empty(rows, cols, x.dtype if out_dtype is None else out_dtype, x.device, stream)
+    kind = _mx_type(out.dtype, "the output")
+    h = _rms_norm(x, weight, eps, residual, sum_out, out, kind, None, stream)
+    return out if h is None else (out, h)
+
+
+def rms_norm_i8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                out=None, sum_out: torch.Tensor | None = None, stream=None):
+    """(q, scale), with a residual (q, scale, h): rms_norm's rows as int8 codes of their largest magnitude over 127,
+    and that scale, float32 (rows,): the A and scale_a of gemm_i8_dequant.  A row of zeros takes scale 0, a row that
+    holds an infinity or a NaN codes 0 and scale NaN.  out: a (q, scale) pair to write; a new q has rows of a multiple
+    of 16 bytes, as the products take them."""
+    rows, cols, _ = _mx_rows(x, "x")
+    if out is None:
+        q = _mx_empty(rows, _round_up(cols, 16), torch.int8, x.device, stream)[:, :cols]
+        scale = _mx_empty(1, rows, torch.float32, x.device, stream)[0]
+    else:
+        q, scale = out
+        if not isinstance(q, torch.Tensor) or q.dtype is not torch.int8:
+            raise TypeError("out's codes must be an int8 tensor")
+        _scale(scale, rows, "out's scale")
+    h = _rms_norm(x, weight, eps, residual, sum_out, q, _I8, scale, stream)
+    return (q, scale) if h is None else (q, scale, h)
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                      dh: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      dweight: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """(dx, dweight) of y = rms_norm(h) for the gradient dy of y: dx, of h's type, is the gradient of x and of the
+    residual alike, with dh, the gradient that h has from elsewhere, added; dweight is float32.  All matrices have
+    h's type and shape; out may be dy or dh itself."""
+    kind = _mx_type(h.dtype, "h")
+    rows, cols, ldh = _mx_rows(h, "h")
+    wkind = _norm_weight(weight, cols)
+    lddy = _like_x(dy, h, "dy")
+    lddh = 0 if dh is None else _like_x(dh, h, "dh")
+    if out is None:
+        out = _new_like(h, stream)
+    lddx = _like_x(out, h, "out")
+    if dweight is None:
+        dweight = _mx_empty(1, cols, torch.float32, h.device, stream)[0]
+    need = lib.pdgemm_rms_norm_backward_workspace_size(rows, cols)
+    if workspace is None and need:
+        workspace = _mx_empty(1, need, torch.uint8, h.device, stream)
+    ws, ws_bytes = _workspace(workspace, h.device)
+    _mx_call(lib.pdgemm_rms_norm_backward,
+             (rows, cols, dy.data_ptr(), lddy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(), lddh, kind,
+              weight.data_ptr(), wkind, eps, out.data_ptr(), lddx, _scale(dweight, cols, "dweight"), ws, ws_bytes),
+             (h, dy, weight, out, dweight) + (() if dh is None else (dh,)), stream)
+    return out, dweight
 
 
 def prepare(prec: str, A: torch.Tensor, Bt: torch.Tensor, out: torch.Tensor, K: int | None = None,

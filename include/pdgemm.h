@@ -107,7 +107,7 @@ extern "C" {
 #define PDGEMM_ENULL (-3)       /* NULL pointer for an operand with nonzero extent */
 #define PDGEMM_EINVAL_I4 (-4)   /* gemm_i4: K, lda or ldb odd */
 #define PDGEMM_EALIGN (-5)      /* a pointer or leading dimension breaks the alignment rules */
-#define PDGEMM_EINVAL_CFG (-6)  /* unknown precision, element type, scale rule or tile configuration,
+#define PDGEMM_EINVAL_CFG (-6)  /* unknown precision, element type, scale rule, group or tile configuration,
                                    or a dequantizing epilogue for FP16; reported before any other check.  Every
                                    configuration, the K-split ones included, serves both B layouts */
 
@@ -493,6 +493,66 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
                              const void *dh, int64_t lddh, int type, const void *weight, int weight_type, float eps,
                              void *dx, int64_t lddx, float *dweight, void *workspace, int64_t workspace_bytes,
                              void *stream);
+
+/* C = A * B of 16-bit A (a_type PDGEMM_F16 or PDGEMM_BF16, row-major, rows of a
+ * multiple of 16 bytes, 16-byte aligned) and INT4 weights B with group scales,
+ * the 4-bit form of most checkpoints: N rows of K signed 4-bit codes packed as
+ * for gemm_i4 (ldb counts 4-bit elements, a multiple of 32, B 16-byte aligned;
+ * K may be odd), and one scale per `group` consecutive k of a row, group any
+ * multiple of 32 (a group of K or more: one scale a row; else
+ * PDGEMM_EINVAL_CFG).  The scales are stored by group: that of group q of row j
+ * at scale_b[q * ldsb + j], of scale_type PDGEMM_F32, _F16 or _BF16, ldsb >= N,
+ * with their element's alignment, a row of at most 4 MiB.
+ *   C[i][j] = sum over q of scale_b[q][j] * sum over k in q of A[i][k] * code[j][k]
+ * The codes enter exactly, the sums are binary32 in a fixed order, and C is
+ * rounded once to out_type: |C - exact| <= (ceil(K / 32) + 2) * 2^-22 * sum |a b|
+ * plus that rounding where no sum leaves binary32's normal range.  As elsewhere
+ * the 16-byte granule that holds a row's last element may be read whole, and
+ * values outside the operands never reach a stored result.  K = 0 stores zeros.
+ * _cfg takes an explicit tile configuration (0 <= cfg <
+ * pdgemm_a16_i4_num_configs(), any shape), _pick is the one gemm_a16_i4 takes. */
+int gemm_a16_i4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
+                int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc,
+                int out_type, void *stream);
+int pdgemm_a16_i4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type,
+                      const uint8_t *B, int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type,
+                      int64_t group, void *C, int64_t ldc, int out_type, void *stream);
+int pdgemm_a16_i4_num_configs(void);
+int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K);
+
+/* A mixture-of-experts layer for a few tokens: what follows the router's product.
+ *
+ * pdgemm_moe_route: the `top` largest of each row of logits (T x E, of `type`, any
+ * ld >= E), E <= 1024, top <= min(E, 64), in falling order, ties to the lower index:
+ * their indices to ids and their softmax to weights (T x top both, dense), among
+ * themselves (normalize != 0) or among all of the row.  An expert at -infinity is
+ * not taken: slots left over take id -1 and weight 0.  A NaN counts as the largest;
+ * a row with a NaN or +infinity takes weights NaN. */
+int pdgemm_moe_route(int64_t T, int64_t E, int64_t top, const void *logits, int64_t ld, int type, int normalize,
+                     int32_t *ids, float *weights, void *stream);
+
+/* y[t] = sum over the slots s of weights[t][s] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),
+ * e = ids[t][s], in two kernels.  x (T x H, rows of a multiple of 16 bytes, 16-byte
+ * aligned) and y are of `type`, PDGEMM_F16 or PDGEMM_BF16; ids and weights T x top,
+ * dense.  An id outside 0 .. E - 1 adds nothing (a padded token, an expert that is
+ * elsewhere); one that a token names twice adds with the weights' sum; a token of no
+ * expert takes zeros.
+ *   w13  per expert 2 I rows of H codes: Wg's I rows, then Wu's;
+ *   w2   per expert H rows of I codes,
+ * with group scales, as gemm_a16_i4's B (ld counts 4-bit elements; an expert's scales
+ * are stored by group); expert strides are counted as the ld beside them are, those of codes a
+ * multiple of 32.  H and I are any length, E <= 1024, top <= 64, T * top <= 4096,
+ * T * ldx * 2 and T * top * (2 I + 16) below 2^31 (PDGEMM_EINVAL_DIM, for ldx
+ * PDGEMM_EINVAL_LD).  The codes enter exactly and sums are binary32 in a fixed order;
+ * silu(..) * (..), times the pair's weight, is rounded to `type` as the second
+ * product's operand, and y once.  The workspace (16-byte aligned) is undefined on
+ * return; calls that overlap, and graphs that may run at once, need one each. */
+int64_t pdgemm_moe_a16_i4_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top);
+int pdgemm_moe_a16_i4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, const void *x, int64_t ldx, int type,
+                      const int32_t *ids, const float *weights, const uint8_t *w13, int64_t ld13, int64_t expert13,
+                      const void *s13, int64_t lds13, int64_t expert_s13, const uint8_t *w2, int64_t ld2,
+                      int64_t expert2, const void *s2, int64_t lds2, int64_t expert_s2, int scale_type, int64_t group,
+                      void *y, int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Static message for a return code (never NULL): the PDGEMM_E* codes above,
  * or hipGetErrorString() for a positive hipError_t.  Part of the error

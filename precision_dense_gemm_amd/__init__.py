@@ -147,6 +147,21 @@ lib.pdgemm_rms_norm_backward_workspace_size.restype = _i64
 lib.pdgemm_rms_norm_backward.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _i, ctypes.c_float, _p,
                                          _i64, _p, _p, _i64, _p]
 lib.pdgemm_rms_norm_backward.restype = _i
+lib.gemm_a16_i4.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _i, _i64, _p, _i64, _i, _p]
+lib.gemm_a16_i4.restype = _i
+lib.pdgemm_a16_i4_cfg.argtypes = [_i] + lib.gemm_a16_i4.argtypes
+lib.pdgemm_a16_i4_cfg.restype = _i
+lib.pdgemm_a16_i4_num_configs.argtypes = []
+lib.pdgemm_a16_i4_num_configs.restype = _i
+lib.pdgemm_a16_i4_pick.argtypes = [_i64, _i64, _i64]
+lib.pdgemm_a16_i4_pick.restype = _i
+lib.pdgemm_moe_route.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _i, _p, _p, _p]
+lib.pdgemm_moe_route.restype = _i
+lib.pdgemm_moe_a16_i4_workspace_size.argtypes = [_i64] * 5
+lib.pdgemm_moe_a16_i4_workspace_size.restype = _i64
+lib.pdgemm_moe_a16_i4.argtypes = ([_i64] * 5 + [_p, _i64, _i, _p, _p] + [_p, _i64, _i64] * 4
+                                  + [_i, _i64, _p, _i64, _p, _i64, _p])
+lib.pdgemm_moe_a16_i4.restype = _i
 lib.pdgemm_strerror.argtypes = [_i]
 lib.pdgemm_strerror.restype = ctypes.c_char_p
 lib.pdgemm_version.argtypes = []
@@ -930,12 +945,161 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, e
     need = lib.pdgemm_rms_norm_backward_workspace_size(rows, cols)
     if workspace is None and need:
         workspace = _mx_empty(1, need, torch.uint8, h.device, stream)
-    ws, ws_bytes = _workspace(workspace, h.device)
+        ws, ws_bytes = workspace.data_ptr(), need
+    else:
+        ws, ws_bytes = _workspace(workspace, h.device)
     _mx_call(lib.pdgemm_rms_norm_backward,
              (rows, cols, dy.data_ptr(), lddy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(), lddh, kind,
               weight.data_ptr(), wkind, eps, out.data_ptr(), lddx, _scale(dweight, cols, "dweight"), ws, ws_bytes),
              (h, dy, weight, out, dweight) + (() if dh is None else (dh,)), stream)
     return out, dweight
+
+
+# ---- INT4 weights with group scales ----
+
+def _i4_weights(codes: torch.Tensor, scales: torch.Tensor, K: int, group: int, name: str):
+    """(rows, ld in values, scale row stride, scale type) of INT4 weights.  The stride of a single row is its
+    length, up to the next multiple the library accepts."""
+    if not isinstance(codes, torch.Tensor) or codes.dtype is not torch.uint8:
+        raise TypeError(f"{name} must be a uint8 tensor of packed 4-bit values")
+    if group <= 0 or group % MX_BLOCK:
+        raise ValueError("group must be a positive multiple of 32")
+    kind = _mx_type(scales.dtype, f"{name}'s scales") if isinstance(scales, torch.Tensor) else None
+    if kind is None:
+        raise TypeError(f"{name}'s scales must be a tensor")
+    rows, width, ld = _mx_rows(codes, name)
+    if width != (K + 1) // 2:
+        raise ValueError(f"{name} must hold {(K + 1) // 2} bytes per row for K = {K}")
+    groups, cols, lds = _mx_rows(scales, f"{name}'s scales")
+    if groups != (K + group - 1) // group or cols != rows:
+        raise ValueError(f"{name}'s scales must have shape {((K + group - 1) // group, rows)}")
+    return rows, 2 * (_round_up(ld, 16) if rows <= 1 else ld), lds, kind
+
+
+def gemm_a16_i4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, group: int, out: torch.Tensor | None = None,
+                out_dtype: torch.dtype = torch.float32, stream=None, cfg: int | None = None) -> torch.Tensor:
+    """C = A * B of float16 or bfloat16 A (M, K), rows of a multiple of 16 bytes, and INT4 weights: Bt (N, ceil(K/2))
+    packed bytes as gemm_i4 takes them, and scale_b (ceil(K/group), N), float32, float16 or bfloat16, one scale per
+    `group` (a multiple of 32) values of a row.  Binary32 sums, C (M, N) float32, float16 or bfloat16 (out's dtype,
+    else out_dtype).  Scales that a checkpoint keeps by row, (N, K/group), are transposed once: scales.t().contiguous().
+    cfg: an explicit tile configuration."""
+    if A.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("gemm_a16_i4 takes a float16 or bfloat16 A")
+    M, K, lda = _mx_rows(A, "A")
+    if M <= 1:
+        lda = _round_up(lda, 8)
+    N, ldb, ldsb, skind = _i4_weights(Bt, scale_b, K, group, "Bt")
+    out, ldc, kind = _mx_dense_out(out, M, N, out_dtype, A.device, stream)
+    args = (M, N, K, A.data_ptr(), lda, _MX_TYPES[A.dtype], Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb, skind, group,
+            out.data_ptr(), ldc, kind)
+    fn, args = (lib.gemm_a16_i4, args) if cfg is None else (lib.pdgemm_a16_i4_cfg, (cfg,) + args)
+    _mx_call(fn, args, (A, Bt, scale_b, out), stream)
+    return out
+
+
+def a16_i4_num_configs() -> int:
+    return lib.pdgemm_a16_i4_num_configs()
+
+
+def a16_i4_pick(M: int, N: int, K: int) -> int:
+    """The tile configuration gemm_a16_i4 takes for a shape."""
+    return lib.pdgemm_a16_i4_pick(M, N, K)
+
+
+def _moe_pairs(t, rows: int, dtype, name: str) -> int:
+    """Columns of a dense (rows, top) tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.dim() != 2 or t.shape[0] != rows or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape ({rows}, top_k)")
+    return t.shape[1]
+
+
+def moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, out=None, stream=None):
+    """(ids, weights): int32 and float32 (T, top_k), the top_k largest of each row of logits (T, E) in falling order,
+    ties to the lower index, and their softmax among themselves, or without normalize among all of the row.  An expert
+    at -inf is not taken (id -1, weight 0).  out: a pair of contiguous tensors to write."""
+    kind = _mx_type(logits.dtype, "logits")
+    T, E, ld = _mx_rows(logits, "logits")
+    if out is None:
+        out = (_mx_empty(T, top_k, torch.int32, logits.device, stream), _mx_empty(T, top_k, torch.float32, logits.device, stream))
+    ids, weights = out
+    if _moe_pairs(ids, T, torch.int32, "ids") != top_k or _moe_pairs(weights, T, torch.float32, "weights") != top_k:
+        raise ValueError(f"ids and weights must have {top_k} columns")
+    _mx_call(lib.pdgemm_moe_route, (T, E, top_k, logits.data_ptr(), ld, kind, 1 if normalize else 0, ids.data_ptr(),
+                                    weights.data_ptr()), (logits, ids, weights), stream)
+    return ids, weights
+
+
+def _moe_weights(codes, scales, E: int, N: int, K: int, group: int, name: str):
+    """The C call's (codes, ld, expert stride, scales, ld, expert stride) of E experts' weights."""
+    if not isinstance(codes, torch.Tensor) or codes.dtype is not torch.uint8:
+        raise TypeError(f"{name} must be a uint8 tensor of packed 4-bit values")
+    if not isinstance(scales, torch.Tensor):
+        raise TypeError(f"{name}'s scales must be a tensor")
+    if tuple(codes.shape) != (E, N, (K + 1) // 2):
+        raise ValueError(f"{name} must have shape {(E, N, (K + 1) // 2)}")
+    if tuple(scales.shape) != (E, (K + group - 1) // group, N):
+        raise ValueError(f"{name}'s scales must have shape {(E, (K + group - 1) // group, N)}")
+    e, ld, step = codes.stride()
+    es, lds, steps = scales.stride()
+    if (step != 1 and codes.shape[2] > 1) or (steps != 1 and N > 1):
+        raise ValueError(f"{name} and its scales must have contiguous rows")
+    # strides that nothing is read by may be anything
+    if N == 1:
+        ld = _round_up(codes.shape[2], 16)
+    if E == 1:
+        e, es = 0, 0
+    if scales.shape[1] == 1:
+        lds = N
+    return codes.data_ptr(), 2 * ld, 2 * e, scales.data_ptr(), lds, es
+
+
+def moe_a16_i4_workspace_size(T: int, H: int, I: int, E: int, top_k: int) -> int:
+    """Bytes of workspace moe_a16_i4 needs."""
+    return lib.pdgemm_moe_a16_i4_workspace_size(T, H, I, E, top_k)
+
+
+def moe_a16_i4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor,
+               w2: torch.Tensor, s2: torch.Tensor, group: int, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """A mixture-of-experts layer for a few tokens (T * top_k <= 4096): y (T, H), of x's type, with
+        y[t] = sum over the slots s of weights[t, s] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),  e = ids[t, s].
+    x (T, H) float16 or bfloat16, rows of a multiple of 16 bytes; ids int32 and weights float32 (T, top_k), as moe_route
+    makes them; INT4 weights of E experts: w13 (E, 2 I, ceil(H/2)), the gate's rows and then the up projection's, w2
+    (E, H, ceil(I/2)), and their scales s13 (E, ceil(H/group), 2 I), s2 (E, ceil(I/group), H), both of one type.  An id
+    outside 0 .. E - 1 adds nothing.  workspace: moe_a16_i4_workspace_size bytes, not shared by calls that overlap."""
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("moe_a16_i4 takes a float16 or bfloat16 x")
+    T, H, ldx = _mx_rows(x, "x")
+    if T <= 1:
+        ldx = _round_up(ldx, 8)
+    top = _moe_pairs(ids, T, torch.int32, "ids")
+    if _moe_pairs(weights, T, torch.float32, "weights") != top:
+        raise ValueError("ids and weights must have the same shape")
+    if group <= 0 or group % MX_BLOCK:
+        raise ValueError("group must be a positive multiple of 32")
+    if not isinstance(w13, torch.Tensor) or w13.dim() != 3 or w13.shape[1] % 2:
+        raise ValueError("w13 must have shape (E, 2 * I, ceil(H / 2))")
+    E, I = w13.shape[0], w13.shape[1] // 2
+    first = _moe_weights(w13, s13, E, 2 * I, H, group, "w13")
+    second = _moe_weights(w2, s2, E, H, I, group, "w2")
+    if s13.dtype is not s2.dtype:
+        raise TypeError("s13 and s2 must have the same type")
+    skind = _mx_type(s13.dtype, "the scales")
+    out, ldy, kind = _mx_dense_out(out, T, H, x.dtype, x.device, stream)
+    if out.dtype is not x.dtype:
+        raise TypeError("out must be of x's type")
+    if workspace is None:
+        ws_bytes = max(lib.pdgemm_moe_a16_i4_workspace_size(T, H, I, E, top), 16)
+        workspace = _mx_empty(1, ws_bytes, torch.uint8, x.device, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, ws_bytes = _workspace(workspace, x.device)
+    _mx_call(lib.pdgemm_moe_a16_i4, (T, H, I, E, top, x.data_ptr(), ldx, kind, ids.data_ptr(), weights.data_ptr(), *first,
+                                     *second, skind, group, out.data_ptr(), ldy, ws, ws_bytes),
+             (x, ids, weights, w13, s13, w2, s2, out), stream)
+    return out
 
 
 def prepare(prec: str, A: torch.Tensor, Bt: torch.Tensor, out: torch.Tensor, K: int | None = None,

@@ -509,14 +509,22 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
  * plus that rounding where no sum leaves binary32's normal range.  As elsewhere
  * the 16-byte granule that holds a row's last element may be read whole, and
  * values outside the operands never reach a stored result.  K = 0 stores zeros.
+ * Where there are too few tiles for the GPU, K is split over workgroups, whose sums
+ * meet in a workspace of pdgemm_a16_i4_workspace_size() bytes (0: none is needed, and it
+ * may be NULL), 16-byte aligned, undefined on return; calls that overlap, and graphs that
+ * may run at once, need one each.
  * _cfg takes an explicit tile configuration (0 <= cfg <
- * pdgemm_a16_i4_num_configs(), any shape), _pick is the one gemm_a16_i4 takes. */
+ * pdgemm_a16_i4_num_configs(), any shape) and the workspace of
+ * _cfg_workspace_size; _pick is the one gemm_a16_i4 takes. */
+int64_t pdgemm_a16_i4_workspace_size(int64_t M, int64_t N, int64_t K);
 int gemm_a16_i4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                 int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc,
-                int out_type, void *stream);
+                int out_type, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t pdgemm_a16_i4_cfg_workspace_size(int cfg, int64_t M, int64_t N, int64_t K);
 int pdgemm_a16_i4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type,
                       const uint8_t *B, int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type,
-                      int64_t group, void *C, int64_t ldc, int out_type, void *stream);
+                      int64_t group, void *C, int64_t ldc, int out_type, void *workspace, int64_t workspace_bytes,
+                      void *stream);
 int pdgemm_a16_i4_num_configs(void);
 int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K);
 

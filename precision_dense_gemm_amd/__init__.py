@@ -147,10 +147,14 @@ lib.pdgemm_rms_norm_backward_workspace_size.restype = _i64
 lib.pdgemm_rms_norm_backward.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _i, ctypes.c_float, _p,
                                          _i64, _p, _p, _i64, _p]
 lib.pdgemm_rms_norm_backward.restype = _i
-lib.gemm_a16_i4.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _i, _i64, _p, _i64, _i, _p]
+lib.gemm_a16_i4.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _i, _i64, _p, _i64, _i, _p, _i64, _p]
 lib.gemm_a16_i4.restype = _i
 lib.pdgemm_a16_i4_cfg.argtypes = [_i] + lib.gemm_a16_i4.argtypes
 lib.pdgemm_a16_i4_cfg.restype = _i
+lib.pdgemm_a16_i4_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.pdgemm_a16_i4_workspace_size.restype = _i64
+lib.pdgemm_a16_i4_cfg_workspace_size.argtypes = [_i, _i64, _i64, _i64]
+lib.pdgemm_a16_i4_cfg_workspace_size.restype = _i64
 lib.pdgemm_a16_i4_num_configs.argtypes = []
 lib.pdgemm_a16_i4_num_configs.restype = _i
 lib.pdgemm_a16_i4_pick.argtypes = [_i64, _i64, _i64]
@@ -847,45 +851,49 @@ def _like_x(t, x, name: str):
     """The row stride of a tensor of x's shape and type."""
     if not isinstance(t, torch.Tensor) or t.dtype is not x.dtype:
         raise TypeError(f"{name} must be a tensor of x's type")
-    rows, cols, ld = _mx_rows(t, name)
-    if t.shape != x.shape:
+    shape = t.shape
+    if shape != x.shape:
         raise ValueError(f"{name} must have shape {tuple(x.shape)}")
-    return ld
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
+    return ld if shape[0] > 1 else shape[1]
 
 
 def _norm_weight(weight, cols: int) -> int:
     if not isinstance(weight, torch.Tensor):
         raise TypeError("weight must be a tensor")
     kind = _mx_type(weight.dtype, "weight")
-    if weight.dim() != 1 or weight.shape[0] != cols:
+    if weight.shape != (cols,):
         raise ValueError(f"weight must hold {cols} values")
-    if cols > 1 and weight.stride(0) != 1:
+    if cols > 1 and weight.stride() != (1,):
         raise ValueError("weight must be contiguous")
     return kind
 
 
-def _new_like(t, stream):
-    rows, cols = t.shape
-    return _mx_empty(rows, cols, t.dtype, t.device, stream)
+def _new_vector(n, dtype, device, stream):
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
 
 
-def _rms_norm(x, weight, eps, residual, sum_out, out, out_kind, scale, stream):
+def _rms_norm(x, rows, cols, ldx, weight, eps, residual, sum_out, out, ldo, out_kind, scale, stream):
     kind = _mx_type(x.dtype, "x")
-    rows, cols, ldx = _mx_rows(x, "x")
     wkind = _norm_weight(weight, cols)
     tensors = (x, weight, out) if scale is None else (x, weight, out, scale)
-    add = (None, 0, None, 0)
     if residual is not None:
         ldr = _like_x(residual, x, "residual")
         if sum_out is None:
-            sum_out = _new_like(x, stream)
-        add = (residual.data_ptr(), ldr, sum_out.data_ptr(), _like_x(sum_out, x, "sum_out"))
+            sum_out, lds = _mx_empty(rows, cols, x.dtype, x.device, stream), cols
+        else:
+            lds = _like_x(sum_out, x, "sum_out")
+        add = (residual.data_ptr(), ldr, sum_out.data_ptr(), lds)
         tensors += (residual, sum_out)
     elif sum_out is not None:
         raise ValueError("sum_out holds x + residual: it takes a residual")
-    r, c, ldo = _mx_rows(out, "out")
-    if (r, c) != (rows, cols):
-        raise ValueError(f"out must have shape {(rows, cols)}")
+    else:
+        add = (None, 0, None, 0)
     _mx_call(lib.pdgemm_rms_norm, (rows, cols, x.data_ptr(), ldx, kind, *add, weight.data_ptr(), wkind, eps,
                                    out.data_ptr(), ldo, out_kind, None if scale is None else scale.data_ptr()),
              tensors, stream)
@@ -899,11 +907,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     (rounded to x's type), then (y, h).  x (rows, cols) float32, float16 or bfloat16, at most 32768 columns;
     y has out's dtype, else out_dtype, else x's.  sum_out takes h: it may be residual or x itself; out may be
     x itself too."""
-    if out is None:
-        rows, cols, _ = _mx_rows(x, "x")
-        out = _mx_empty(rows, cols, x.dtype if out_dtype is None else out_dtype, x.device, stream)
-    kind = _mx_type(out.dtype, "the output")
-    h = _rms_norm(x, weight, eps, residual, sum_out, out, kind, None, stream)
+    rows, cols, ldx = _mx_rows(x, "x")
+    out, ldo, kind = _mx_dense_out(out, rows, cols, x.dtype if out_dtype is None else out_dtype, x.device, stream)
+    h = _rms_norm(x, rows, cols, ldx, weight, eps, residual, sum_out, out, ldo, kind, None, stream)
     return out if h is None else (out, h)
 
 
@@ -913,16 +919,22 @@ def rms_norm_i8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     and that scale, float32 (rows,): the A and scale_a of gemm_i8_dequant.  A row of zeros takes scale 0, a row that
     holds an infinity or a NaN codes 0 and scale NaN.  out: a (q, scale) pair to write; a new q has rows of a multiple
     of 16 bytes, as the products take them."""
-    rows, cols, _ = _mx_rows(x, "x")
+    rows, cols, ldx = _mx_rows(x, "x")
     if out is None:
-        q = _mx_empty(rows, _round_up(cols, 16), torch.int8, x.device, stream)[:, :cols]
-        scale = _mx_empty(1, rows, torch.float32, x.device, stream)[0]
+        ldo = _round_up(cols, 16)
+        q = _mx_empty(rows, ldo, torch.int8, x.device, stream)
+        if ldo != cols:
+            q = q.as_strided((rows, cols), (ldo, 1))
+        scale = _new_vector(rows, torch.float32, x.device, stream)
     else:
         q, scale = out
         if not isinstance(q, torch.Tensor) or q.dtype is not torch.int8:
             raise TypeError("out's codes must be an int8 tensor")
+        r, c, ldo = _mx_rows(q, "out's codes")
+        if (r, c) != (rows, cols):
+            raise ValueError(f"out's codes must have shape {(rows, cols)}")
         _scale(scale, rows, "out's scale")
-    h = _rms_norm(x, weight, eps, residual, sum_out, q, _I8, scale, stream)
+    h = _rms_norm(x, rows, cols, ldx, weight, eps, residual, sum_out, q, ldo, _I8, scale, stream)
     return (q, scale) if h is None else (q, scale, h)
 
 
@@ -938,10 +950,14 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, e
     lddy = _like_x(dy, h, "dy")
     lddh = 0 if dh is None else _like_x(dh, h, "dh")
     if out is None:
-        out = _new_like(h, stream)
-    lddx = _like_x(out, h, "out")
+        out, lddx = _mx_empty(rows, cols, h.dtype, h.device, stream), cols
+    else:
+        lddx = _like_x(out, h, "out")
     if dweight is None:
-        dweight = _mx_empty(1, cols, torch.float32, h.device, stream)[0]
+        dweight = _new_vector(cols, torch.float32, h.device, stream)
+        dw = dweight.data_ptr()
+    else:
+        dw = _scale(dweight, cols, "dweight")
     need = lib.pdgemm_rms_norm_backward_workspace_size(rows, cols)
     if workspace is None and need:
         workspace = _mx_empty(1, need, torch.uint8, h.device, stream)
@@ -950,7 +966,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, e
         ws, ws_bytes = _workspace(workspace, h.device)
     _mx_call(lib.pdgemm_rms_norm_backward,
              (rows, cols, dy.data_ptr(), lddy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(), lddh, kind,
-              weight.data_ptr(), wkind, eps, out.data_ptr(), lddx, _scale(dweight, cols, "dweight"), ws, ws_bytes),
+              weight.data_ptr(), wkind, eps, out.data_ptr(), lddx, dw, ws, ws_bytes),
              (h, dy, weight, out, dweight) + (() if dh is None else (dh,)), stream)
     return out, dweight
 
@@ -977,11 +993,13 @@ def _i4_weights(codes: torch.Tensor, scales: torch.Tensor, K: int, group: int, n
 
 
 def gemm_a16_i4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, group: int, out: torch.Tensor | None = None,
-                out_dtype: torch.dtype = torch.float32, stream=None, cfg: int | None = None) -> torch.Tensor:
+                out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None, stream=None,
+                cfg: int | None = None) -> torch.Tensor:
     """C = A * B of float16 or bfloat16 A (M, K), rows of a multiple of 16 bytes, and INT4 weights: Bt (N, ceil(K/2))
     packed bytes as gemm_i4 takes them, and scale_b (ceil(K/group), N), float32, float16 or bfloat16, one scale per
     `group` (a multiple of 32) values of a row.  Binary32 sums, C (M, N) float32, float16 or bfloat16 (out's dtype,
     else out_dtype).  Scales that a checkpoint keeps by row, (N, K/group), are transposed once: scales.t().contiguous().
+    workspace: a16_i4_workspace_size bytes, not shared by calls that overlap; allocated where it is needed and omitted.
     cfg: an explicit tile configuration."""
     if A.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("gemm_a16_i4 takes a float16 or bfloat16 A")
@@ -992,9 +1010,25 @@ def gemm_a16_i4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, group:
     out, ldc, kind = _mx_dense_out(out, M, N, out_dtype, A.device, stream)
     args = (M, N, K, A.data_ptr(), lda, _MX_TYPES[A.dtype], Bt.data_ptr(), ldb, scale_b.data_ptr(), ldsb, skind, group,
             out.data_ptr(), ldc, kind)
+    if workspace is not None:
+        args += _workspace(workspace, out.device)
+    else:
+        need = a16_i4_workspace_size(M, N, K, cfg) if M > 16 or cfg is not None else 0
+        if need:
+            workspace = _mx_empty(1, need, torch.uint8, A.device, stream)
+            args += (workspace.data_ptr(), need)
+        else:
+            args += (None, 0)
     fn, args = (lib.gemm_a16_i4, args) if cfg is None else (lib.pdgemm_a16_i4_cfg, (cfg,) + args)
     _mx_call(fn, args, (A, Bt, scale_b, out), stream)
     return out
+
+
+def a16_i4_workspace_size(M: int, N: int, K: int, cfg: int | None = None) -> int:
+    """Bytes of workspace gemm_a16_i4 needs for a shape (0: none)."""
+    if cfg is None:
+        return lib.pdgemm_a16_i4_workspace_size(M, N, K)
+    return lib.pdgemm_a16_i4_cfg_workspace_size(cfg, M, N, K)
 
 
 def a16_i4_num_configs() -> int:
@@ -1010,9 +1044,10 @@ def _moe_pairs(t, rows: int, dtype, name: str) -> int:
     """Columns of a dense (rows, top) tensor."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.dim() != 2 or t.shape[0] != rows or not t.is_contiguous():
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape ({rows}, top_k)")
-    return t.shape[1]
+    return shape[1]
 
 
 def moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, out=None, stream=None):
@@ -1022,10 +1057,12 @@ def moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, out=None
     kind = _mx_type(logits.dtype, "logits")
     T, E, ld = _mx_rows(logits, "logits")
     if out is None:
-        out = (_mx_empty(T, top_k, torch.int32, logits.device, stream), _mx_empty(T, top_k, torch.float32, logits.device, stream))
-    ids, weights = out
-    if _moe_pairs(ids, T, torch.int32, "ids") != top_k or _moe_pairs(weights, T, torch.float32, "weights") != top_k:
-        raise ValueError(f"ids and weights must have {top_k} columns")
+        ids = _mx_empty(T, top_k, torch.int32, logits.device, stream)
+        weights = _mx_empty(T, top_k, torch.float32, logits.device, stream)
+    else:
+        ids, weights = out
+        if _moe_pairs(ids, T, torch.int32, "ids") != top_k or _moe_pairs(weights, T, torch.float32, "weights") != top_k:
+            raise ValueError(f"ids and weights must have {top_k} columns")
     _mx_call(lib.pdgemm_moe_route, (T, E, top_k, logits.data_ptr(), ld, kind, 1 if normalize else 0, ids.data_ptr(),
                                     weights.data_ptr()), (logits, ids, weights), stream)
     return ids, weights
@@ -1037,9 +1074,9 @@ def _moe_weights(codes, scales, E: int, N: int, K: int, group: int, name: str):
         raise TypeError(f"{name} must be a uint8 tensor of packed 4-bit values")
     if not isinstance(scales, torch.Tensor):
         raise TypeError(f"{name}'s scales must be a tensor")
-    if tuple(codes.shape) != (E, N, (K + 1) // 2):
+    if codes.shape != (E, N, (K + 1) // 2):
         raise ValueError(f"{name} must have shape {(E, N, (K + 1) // 2)}")
-    if tuple(scales.shape) != (E, (K + group - 1) // group, N):
+    if scales.shape != (E, (K + group - 1) // group, N):
         raise ValueError(f"{name}'s scales must have shape {(E, (K + group - 1) // group, N)}")
     e, ld, step = codes.stride()
     es, lds, steps = scales.stride()
@@ -1087,12 +1124,12 @@ def moe_a16_i4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: t
     if s13.dtype is not s2.dtype:
         raise TypeError("s13 and s2 must have the same type")
     skind = _mx_type(s13.dtype, "the scales")
-    out, ldy, kind = _mx_dense_out(out, T, H, x.dtype, x.device, stream)
-    if out.dtype is not x.dtype:
+    if out is not None and out.dtype is not x.dtype:
         raise TypeError("out must be of x's type")
+    out, ldy, kind = _mx_dense_out(out, T, H, x.dtype, x.device, stream)
     if workspace is None:
         ws_bytes = max(lib.pdgemm_moe_a16_i4_workspace_size(T, H, I, E, top), 16)
-        workspace = _mx_empty(1, ws_bytes, torch.uint8, x.device, stream)
+        workspace = _new_vector(ws_bytes, torch.uint8, x.device, stream)
         ws = workspace.data_ptr()
     else:
         ws, ws_bytes = _workspace(workspace, x.device)

@@ -8,12 +8,15 @@ struct A16I4Args {
     const uint8_t *A;
     const uint8_t *B;
     void *C;
+    float *part;        // the splits' sums, M x N each
     I4Scales s;
     int64_t lda, ldb;   // bytes
     int64_t ldc;        // elements
     int M, N, K;
-    int tiles_n;
+    int tiles_m, tiles_n;
+    int splits;
     int group, out_type;
+    uint32_t group_magic;
 };
 
 __device__ __forceinline__ void store_as(void *C, int type, int64_t at, float v) {
@@ -24,29 +27,50 @@ __device__ __forceinline__ void store_as(void *C, int type, int64_t at, float v)
     else
         static_cast<__bf16 *>(C)[at] = (__bf16)v;
 }
+// the first n of N neighbours
+template <int N>
+__device__ __forceinline__ void store_as(void *C, int type, int64_t at, const float (&v)[N], int n) {
+    if (type == kF32) {
+        store_some<N>(static_cast<float *>(C) + at, v, n);
+    } else if (type == kF16) {
+        _Float16 e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = (_Float16)v[i];
+        store_some<N>(static_cast<_Float16 *>(C) + at, e, n);
+    } else {
+        __bf16 e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = (__bf16)v[i];
+        store_some<N>(static_cast<__bf16 *>(C) + at, e, n);
+    }
+}
 
-// A tile of 16 MT rows and 16 NT columns of C to a workgroup, K split over its W waves, whose
-// sums meet in LDS and are added in wave order.
-template <int T, int MT, int NT, int W, int Q, bool kS32>
-__global__ __launch_bounds__(W *kWave) void a16_i4_kernel(A16I4Args args) {
+// Few rows: a tile of RA rows and 16 NT columns of C to a workgroup, K split over its W waves,
+// whose sums meet in LDS and are added in wave order.
+template <int T, int RA, int NT, int W, int Q, bool kS32, bool kAhead>
+__global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int kTile = MT * NT * 256;
-    __shared__ float part[W][kTile];
+    using Wave = I4Wave<T, RA, NT, 1, Q, kS32, kAhead>;
+    constexpr int kTile = NT * 256;
+    __shared__ union {
+        uint4 xs[W][Wave::kLds];
+        float part[W][kTile];
+    } lds;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane % 16, g = lane / 16;
-    const int m0 = (blockIdx.x / args.tiles_n) * 16 * MT, n0 = (blockIdx.x % args.tiles_n) * 16 * NT;
+    const int m0 = (blockIdx.x / args.tiles_n) * RA, n0 = (blockIdx.x % args.tiles_n) * 16 * NT;
     const int M = args.M, N = args.N, K = args.K;
 
-    I4Source<MT, NT, 1> src;
+    typename Wave::Source src;
     src.a = args.A + (int64_t)m0 * args.lda;
-    src.a_end = (int)((min(16 * MT, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15);
+    src.a_end = (int)((min(RA, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15);
     src.b[0] = args.B + (int64_t)n0 * args.ldb;
     src.b_end[0] = (int)((min(16 * NT, N - n0) - 1) * args.ldb) + (((K + 1) / 2 + 15) & ~15);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int row = 16 * i + r;
-        src.va[i] = row < M - m0 ? (uint32_t)row * (uint32_t)args.lda + 16 * g : kOutside;
+    for (int j = 0; j < Wave::kX; ++j) {
+        const int row = Wave::copied_row(j);
+        src.xa[j] = row < M - m0 ? (uint32_t)row * (uint32_t)args.lda + 16 * Wave::copied_chunk() : kOutside;
     }
     const int size = kS32 ? 4 : 2;
 #pragma unroll
@@ -56,52 +80,250 @@ __global__ __launch_bounds__(W *kWave) void a16_i4_kernel(A16I4Args args) {
         src.vs[t] = (uint32_t)(n0 + min(row, N - n0 - 1)) * size;
     }
     src.s[0] = args.s;
-    src.K = K, src.group = args.group;
+    src.K = K, src.group_magic = args.group_magic, src.groups = (K + args.group - 1) / args.group;
 
-    I4Wave<T, MT, NT, 1, Q, kS32, MT == 4 ? 2 : 4> w;
-    // pairs of steps, which are whole 128-byte lines of the codes' rows
-    const int steps = (K + kStep - 1) / kStep, pairs = (steps + 1) / 2;
-    const int mine = wave < pairs ? (pairs - wave + W - 1) / W : 0;
-    const int odd = mine > 0 && wave + (mine - 1) * W == pairs - 1 ? steps % 2 : 0;   // the last pair may be half of one
-    w.run(src, 2 * mine - odd, [&](int i, auto &) { return 2 * (wave + (i >> 1) * W) + (i & 1); });
+    // The workgroups of an XCD begin at different places of their rows, or all of them would ask
+    // the same memory channels at a time where a row is a power of two long.
+    const int units = (K + 2 * kStep - 1) / (2 * kStep);
+    const int turned = units > 0 ? (int)(blockIdx.x / 8 * W % units) : 0;
+    int next = wave;
+    Wave w;
+    w.run(
+        src, lds.xs[wave],
+        [&](auto &, auto &) {
+            if (next >= units) return -1;
+            const int unit = next + turned;
+            next += W;
+            return unit < units ? unit : unit - units;
+        },
+        [](auto &) {});
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lds.part[wave][(t * 4 + e) * kWave + lane] = w.acc[t][e];
+    __syncthreads();
+    // fragment t holds, in register e of lane l, row 4 (l / 16) + e and column 16 t + l % 16
+    for (int x = tid; x < RA * 16 * NT; x += W * kWave) {
+        const int row = x / (16 * NT), col = x % (16 * NT);
+        if (m0 + row >= M || n0 + col >= N) continue;
+        const int at = (col / 16 * 4 + row % 4) * kWave + row / 4 * 16 + col % 16;
+        float sum = lds.part[0][at];
+#pragma unroll
+        for (int v = 1; v < W; ++v) sum += lds.part[v][at];
+        store_as(args.C, args.out_type, (int64_t)(m0 + row) * args.ldc + n0 + col, sum);
+    }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// More rows: a tile of 16 MT rows to a workgroup, whose W waves have 16 NT columns each, so that a
+// code is converted once per tile.  Activations go through LDS, a step of 128 values of K at a
+// time and two deep, for all waves; codes come straight into the lanes that convert them, a
+// line of 256 values ahead.  Fragment t holds columns NT n + t (n = l % 16) of the wave's: a lane's
+// results are neighbours in C.  With `splits`, K is split over that many workgroups, which
+// write binary32 sums for split_join_kernel.
+template <int T, int MT, int NT, int W, int Q, bool kS32>
+__global__ __launch_bounds__(W *kWave, 2) void a16_i4_tile_kernel(A16I4Args args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int BM = 16 * MT, BN = 16 * NT * W, kThreads = W * kWave;
+    constexpr int kX = BM * 16 / kThreads, kSc = 4 / Q;
+    static_assert(BM * 16 % kThreads == 0, "a step of activations in whole runs");
+    __shared__ uint4 xs[2][BM][16];
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int r = lane % 16, g = lane / 16;
+    const int M = args.M, N = args.N, K = args.K;
+    const int tile = blockIdx.x / args.splits, split = blockIdx.x % args.splits;
+    const int m0 = tile % args.tiles_m * BM, n0 = tile / args.tiles_m * BN + wave * 16 * NT;
+    const int units = (K + 2 * kStep - 1) / (2 * kStep);
+    const int first = (int)((int64_t)units * split / args.splits), last = (int)((int64_t)units * (split + 1) / args.splits);
+
+    const uint8_t *const a = args.A + (int64_t)m0 * args.lda;
+    const int a_end = (int)((min(BM, M - m0) - 1) * args.lda) + ((2 * K + 15) & ~15);
+    const int cols = min(max(N - n0, 0), 16 * NT);   // (a wave may have no column)
+    const uint8_t *const b = args.B + (int64_t)(cols > 0 ? n0 : 0) * args.ldb;
+    const int b_end = cols > 0 ? (int)((cols - 1) * args.ldb) + (((K + 1) / 2 + 15) & ~15) : 0;
+    uint32_t xa[kX], vb[NT], vs[NT];
+#pragma unroll
+    for (int j = 0; j < kX; ++j) {
+        const int row = (tid + j * kThreads) / 16;
+        xa[j] = row < M - m0 ? (uint32_t)row * (uint32_t)args.lda + 16 * (tid % 16) : kOutside;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int col = NT * r + t;
+        vb[t] = col < cols ? (uint32_t)col * (uint32_t)args.ldb + 16 * g : kOutside;
+        vs[t] = (uint32_t)(cols > 0 ? n0 + min(col, cols - 1) : 0) * (kS32 ? 4 : 2);
+    }
+    const int groups = (K + args.group - 1) / args.group;
+
+    uint4 xr[kX];
+    auto load_x = [&](int step) __attribute__((always_inline)) {
+        const int left = step < 2 * last ? a_end - step * 256 : 0;
+        const auto ra = rsrc(a + (int64_t)step * 256, left > 0 ? left : 0);
+#pragma unroll
+        for (int j = 0; j < kX; ++j) xr[j] = load16(ra, xa[j]);
+    };
+    auto store_x = [&](int step) __attribute__((always_inline)) {
+        if (step * kStep + kStep > K) {
+            // activations at and past K may be anything, a NaN too: they become zeros
+            const int n = K - step * kStep - tid % 16 * 8;
+            uint32_t m[4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) m[d] = n >= 2 * d + 2 ? 0xFFFFFFFFu : n == 2 * d + 1 ? 0xFFFFu : 0u;
+#pragma unroll
+            for (int j = 0; j < kX; ++j) xr[j] = make_uint4(xr[j].x & m[0], xr[j].y & m[1], xr[j].z & m[2], xr[j].w & m[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < kX; ++j) {
+            const int row = (tid + j * kThreads) / 16;
+            xs[step & 1][row][(tid % 16) ^ (row % 8)] = xr[j];
+        }
+    };
+    struct Codes {
+        uint4 b[NT][2];
+        uint32_t s[NT][2 * kSc];
+    };
+    auto load_codes = [&](Codes &c, int unit) __attribute__((always_inline)) {
+        const int left = unit < last ? b_end - unit * 128 : 0;
+        const auto rb = rsrc(b + (int64_t)unit * 128, left > 0 ? left : 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            c.b[t][0] = load16(rb, vb[t]);
+            c.b[t][1] = load16(rb, vb[t] + 64);
+        }
+#pragma unroll
+        for (int u = 0; u < 2 * kSc; ++u) {
+            const int q = I4Groups::of(unit * 8 + u * Q, args.group_magic, groups);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint8_t *const p = args.s.p + q * args.s.ld + vs[t];
+                if constexpr (kS32)
+                    c.s[t][u] = *reinterpret_cast<const uint32_t *>(p);
+                else
+                    c.s[t][u] = *reinterpret_cast<const uint16_t *>(p);
+            }
+        }
+    };
+    floatx4_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) acc[i][t] = floatx4_t{0, 0, 0, 0};
+
+    if (first < last) {
+        Codes now, next;
+        load_codes(now, first);
+        load_x(2 * first);
+        store_x(2 * first);
+        load_x(2 * first + 1);
+        for (int unit = first; unit < last; ++unit) {
+            load_codes(next, unit + 1);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[wave][((i * NT + t) * 4 + e) * kWave + lane] = w.acc[i][t][e];
-    __syncthreads();
-    // fragment (i, t) holds, in register e of lane l, row 16 i + 4 (l / 16) + e and column 16 t + l % 16
-    for (int x = tid; x < kTile; x += W * kWave) {
-        const int row = x / (16 * NT), col = x % (16 * NT);
-        if (m0 + row >= M || n0 + col >= N) continue;
-        const int at = ((row / 16 * NT + col / 16) * 4 + row % 4) * kWave + row % 16 / 4 * 16 + col % 16;
-        float sum = part[0][at];
+            for (int h = 0; h < 2; ++h) {
+                const int step = 2 * unit + h;
+                __syncthreads();
+                store_x(step + 1);
+                load_x(step + 2);
+                uint4 x[MT][4];
 #pragma unroll
-        for (int v = 1; v < W; ++v) sum += part[v][at];
-        store_as(args.C, args.out_type, (int64_t)(m0 + row) * args.ldc + n0 + col, sum);
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) x[i][u] = xs[h][16 * i + r][position<Q>(u, g) ^ (r % 8)];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    uint32_t w[4] = {now.b[t][h].x, now.b[t][h].y, now.b[t][h].z, now.b[t][h].w};
+                    share_out<Q>(w);
+#pragma unroll
+                    for (int v = 0; v < kSc; ++v) {
+                        uint4 c[Q];
+#pragma unroll
+                        for (int u = 0; u < Q; ++u) c[u] = widen<T>(w[v * Q + u]);
+                        float s = scale_value<kS32>(now.s[t][h * kSc + v], args.s.half);
+                        s = step * kStep + v * Q * kBlock < K ? s * 16.0f : 0.0f;   // (no scale past K)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            floatx4_t p = {0, 0, 0, 0};
+#pragma unroll
+                            for (int u = 0; u < Q; ++u) p = mfma16<T>(x[i][v * Q + u], c[u], p);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[i][t][e] = __builtin_fmaf(p[e], s, acc[i][t][e]);
+                        }
+                    }
+                }
+            }
+            now = next;
+        }
     }
+    float *const part = args.splits > 1 ? args.part + (int64_t)split * M * N : nullptr;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = m0 + 16 * i + 4 * g + e;
+            if (row >= M) continue;
+            float v[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) v[t] = acc[i][t][e];
+            const int n = cols - NT * r;
+            if (n <= 0) continue;
+            if (part)
+                store_some<NT>(part + (int64_t)row * N + n0 + NT * r, v, n);
+            else
+                store_as<NT>(args.C, args.out_type, (int64_t)row * args.ldc + n0 + NT * r, v, n);
+        }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+constexpr int kMaxSplits = 16;
+
+// C from the splits' sums, added in their order; four neighbours of a row to a thread.
+__global__ __launch_bounds__(256) void split_join_kernel(A16I4Args args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int per_row = (args.N + 3) / 4;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = x / per_row;
+    const int col = (int)(x % per_row) * 4;
+    if (row >= args.M) return;
+    const float *const p = args.part + row * args.N + col;
+    // (all loads before the first sum)
+    float v[kMaxSplits][4], sum[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+        if (k < args.splits) load_some<4>(v[k], p + (int64_t)k * args.M * args.N, args.N - col);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+        if (k < args.splits)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] += v[k][i];
+    store_as<4>(args.C, args.out_type, row * args.ldc + col, sum, args.N - col);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
 // ---------------------------------------------------------------------------
 // host side
 
+// few: rows of a tile 2, 8 or 16; else 16 MT
 struct Config {
-    int mt, nt, waves;
+    bool few;
+    int rows, nt, waves;
 };
-constexpr Config kConfigs[] = {{1, 1, 8}, {1, 2, 8}, {1, 4, 8}, {2, 1, 8}, {2, 2, 8}, {4, 2, 4}, {4, 4, 4}};
+constexpr Config kConfigs[] = {{true, 2, 1, 8},  {true, 2, 2, 8},   {true, 8, 1, 8},   {true, 8, 2, 8},  {true, 16, 1, 8},
+                               {true, 16, 2, 8}, {false, 32, 2, 4}, {false, 48, 2, 4}, {false, 64, 2, 4}};
 constexpr int kNumConfigs = sizeof(kConfigs) / sizeof(kConfigs[0]);
 
-template <int T, int C, int Q>
-const void *a16_i4_ptr(bool s32) {
+template <int T, int C, int Q, bool kS32>
+const void *a16_i4_ptr() {
     constexpr Config c = kConfigs[C];
-    return s32 ? reinterpret_cast<const void *>(&a16_i4_kernel<T, c.mt, c.nt, c.waves, Q, true>)
-               : reinterpret_cast<const void *>(&a16_i4_kernel<T, c.mt, c.nt, c.waves, Q, false>);
+    if constexpr (c.few)
+        return reinterpret_cast<const void *>(&a16_i4_few_kernel<T, c.rows, c.nt, c.waves, Q, kS32, c.rows != 16>);
+    else
+        return reinterpret_cast<const void *>(&a16_i4_tile_kernel<T, c.rows / 16, c.nt, c.waves, Q, kS32>);
 }
 template <int T, int Q, int C = 0>
 const void *a16_i4_ptr(int cfg, bool s32) {
-    if constexpr (C < kNumConfigs) return cfg == C ? a16_i4_ptr<T, C, Q>(s32) : a16_i4_ptr<T, Q, C + 1>(cfg, s32);
+    if constexpr (C < kNumConfigs)
+        return cfg != C ? a16_i4_ptr<T, Q, C + 1>(cfg, s32) : s32 ? a16_i4_ptr<T, C, Q, true>() : a16_i4_ptr<T, C, Q, false>();
     return nullptr;
 }
 template <int T>
@@ -111,22 +333,42 @@ const void *a16_i4_ptr(int cfg, int group, bool s32) {
                              : a16_i4_ptr<T, 1>(cfg, s32);
 }
 
+int64_t tiles_m(int c, int64_t M) { return cdiv(M, kConfigs[c].rows); }
+int64_t tiles_n(int c, int64_t N) { return cdiv(N, 16 * kConfigs[c].nt * (kConfigs[c].few ? 1 : kConfigs[c].waves)); }
+
 // The widest tile of the rows that still makes a workgroup for each CU.
 int pick_a16_i4(int64_t M, int64_t N, int64_t K) {
     (void)K;
-    auto tiles = [&](int c) { return cdiv(M, 16 * kConfigs[c].mt) * cdiv(N, 16 * kConfigs[c].nt); };
-    if (M <= 16) return tiles(2) >= 256 ? 2 : tiles(1) >= 256 ? 1 : 0;
-    if (M <= 32) return tiles(4) >= 256 ? 4 : 3;
-    return tiles(6) >= 256 ? 6 : tiles(5) >= 256 ? 5 : tiles(4) >= 256 ? 4 : 3;
+    if (M <= 2) return tiles_n(1, N) >= 256 ? 1 : 0;
+    if (M <= 8) return tiles_n(3, N) >= 256 ? 3 : 2;
+    if (M <= 16) return tiles_n(5, N) >= 256 ? 5 : 4;
+    return M <= 32 ? 6 : M <= 48 ? 7 : 8;
+}
+
+// Ranges of K of a tile configuration: as many as make two workgroups for each CU, of a unit or more.
+int splits_of(int cfg, int64_t M, int64_t N, int64_t K) {
+    if (kConfigs[cfg].few) return 1;
+    const int64_t tiles = tiles_m(cfg, M) * tiles_n(cfg, N), units = cdiv(K, 2 * kStep);
+    int64_t s = 512 / tiles;
+    if (s > units / 2) s = units / 2;
+    return s < 2 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
+}
+int64_t split_bytes(int cfg, int64_t M, int64_t N, int64_t K) {
+    const int s = splits_of(cfg, M, N, K);
+    return s > 1 ? 4 * s * M * N : 0;
+}
+
+bool sizes_ok(int64_t M, int64_t N, int64_t K) {
+    return M >= 0 && N >= 0 && K >= 0 && M <= INT32_MAX && N <= INT32_MAX && K <= (int64_t(1) << 30);
 }
 
 int launch_a16_i4(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                   int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc,
-                  int out_type, void *stream) {
+                  int out_type, void *workspace, int64_t workspace_bytes, void *stream) {
     if (cfg >= kNumConfigs || (a_type != kF16 && a_type != kBF16) || !known_type(scale_type) || !known_type(out_type) ||
         group <= 0 || group % kBlock || group > (int64_t(1) << 30))
         return PDGEMM_EINVAL_CFG;
-    if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > (int64_t(1) << 30)) return PDGEMM_EINVAL_DIM;
+    if (!sizes_ok(M, N, K)) return PDGEMM_EINVAL_DIM;
     if (lda < K || ldb < K || ldsb < N || ldc < N) return PDGEMM_EINVAL_LD;
     if (M == 0 || N == 0) return PDGEMM_OK;
     int rc = check_plain(C, ldc, out_type);
@@ -137,42 +379,63 @@ int launch_a16_i4(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64
     if (rc == PDGEMM_OK && K > 0 && (lda % 8 || ldb % 32 || ((uintptr_t)A & 15) || ((uintptr_t)B & 15))) rc = PDGEMM_EALIGN;
     if (rc != PDGEMM_OK) return rc;
     if (cfg < 0) cfg = pick_a16_i4(M, N, K);
+    const int splits = splits_of(cfg, M, N, K);
+    if (splits > 1) {
+        if (!workspace) return PDGEMM_ENULL;
+        if (workspace_bytes < split_bytes(cfg, M, N, K) || ((uintptr_t)workspace & 15)) return PDGEMM_EWORKSPACE;
+    }
     const Config &c = kConfigs[cfg];
     // with K = 0 no operand is read: the kernels form addresses from C instead
     const uint8_t *const p = static_cast<const uint8_t *>(C);
     A16I4Args args = {K ? static_cast<const uint8_t *>(A) : p,
                       K ? B : p,
                       C,
-                      {K ? static_cast<const uint8_t *>(scale_b) : p, K ? ldsb * elem_size(scale_type) : 0, scale_type},
+                      static_cast<float *>(workspace),
+                      {K ? static_cast<const uint8_t *>(scale_b) : p, K ? ldsb * elem_size(scale_type) : 0, scale_type == kF16 ? ~0u : 0u},
                       K ? 2 * lda : 0,
                       K ? ldb / 2 : 0,
                       ldc,
                       (int)M,
                       (int)N,
                       (int)K,
-                      (int)cdiv(N, 16 * c.nt),
+                      (int)tiles_m(cfg, M),
+                      (int)tiles_n(cfg, N),
+                      splits,
                       (int)group,
-                      out_type};
+                      out_type,
+                      I4Groups::magic(group)};
     const bool s32 = scale_type == kF32;
     const void *fn = a_type == kF16 ? a16_i4_ptr<kF16>(cfg, (int)group, s32) : a16_i4_ptr<kBF16>(cfg, (int)group, s32);
-    return run(fn, cdiv(M, 16 * c.mt) * args.tiles_n, c.waves * kWave, &args, stream);
+    rc = run(fn, (int64_t)args.tiles_m * args.tiles_n * splits, c.waves * kWave, &args, stream);
+    if (rc != PDGEMM_OK || splits == 1) return rc;
+    return run(reinterpret_cast<const void *>(&split_join_kernel), cdiv(M * cdiv(N, 4), 256), 256, &args, stream);
 }
 
 }  // namespace
 
 extern "C" {
 
+int64_t pdgemm_a16_i4_workspace_size(int64_t M, int64_t N, int64_t K) {
+    return sizes_ok(M, N, K) && M > 0 && N > 0 ? split_bytes(pick_a16_i4(M, N, K), M, N, K) : 0;
+}
+
 int gemm_a16_i4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B, int64_t ldb,
                 const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc, int out_type,
-                void *stream) {
-    return launch_a16_i4(-1, M, N, K, A, lda, a_type, B, ldb, scale_b, ldsb, scale_type, group, C, ldc, out_type, stream);
+                void *workspace, int64_t workspace_bytes, void *stream) {
+    return launch_a16_i4(-1, M, N, K, A, lda, a_type, B, ldb, scale_b, ldsb, scale_type, group, C, ldc, out_type, workspace,
+                         workspace_bytes, stream);
+}
+
+int64_t pdgemm_a16_i4_cfg_workspace_size(int cfg, int64_t M, int64_t N, int64_t K) {
+    return cfg >= 0 && cfg < kNumConfigs && sizes_ok(M, N, K) && M > 0 && N > 0 ? split_bytes(cfg, M, N, K) : 0;
 }
 
 int pdgemm_a16_i4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                       int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc,
-                      int out_type, void *stream) {
+                      int out_type, void *workspace, int64_t workspace_bytes, void *stream) {
     if (cfg < 0) return PDGEMM_EINVAL_CFG;
-    return launch_a16_i4(cfg, M, N, K, A, lda, a_type, B, ldb, scale_b, ldsb, scale_type, group, C, ldc, out_type, stream);
+    return launch_a16_i4(cfg, M, N, K, A, lda, a_type, B, ldb, scale_b, ldsb, scale_type, group, C, ldc, out_type, workspace,
+                         workspace_bytes, stream);
 }
 
 int pdgemm_a16_i4_num_configs(void) { return kNumConfigs; }

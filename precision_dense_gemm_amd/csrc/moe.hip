@@ -11,7 +11,6 @@ namespace {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 64;
 constexpr int kMaxPairs = 4096;
-constexpr uint32_t kNone = 0xFFFFu;   // no pair
 
 // ---------------------------------------------------------------------------
 // routing
@@ -90,10 +89,12 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs args) {
 // ---------------------------------------------------------------------------
 // experts
 //
-// A pair is a token and one of its slots, p = t * top + s.  The first kernel computes the
-// gated activations of every pair, times the pair's weight, in 16 bits: a row of `act` per
-// pair.  The second adds the experts up: a tile of y's columns to a workgroup, whose waves
-// share out all (expert, range of I), so no sum leaves the workgroup and their order is fixed.
+// A pair is a token and one of its slots, p = t * top + s; an expert that a token names twice is
+// computed for the first of the slots, with the weights' sum.  The first kernel computes the gated
+// activations of every pair, times its weight, in 16 bits: a row of `act` per pair.  The second adds
+// the experts up: 16 columns of y to a workgroup, whose waves share out all (expert, line of
+// its rows), each with sums of its own for every token, so no sum leaves the workgroup and
+// their order is fixed.
 
 struct MoeArgs {
     const uint8_t *x;
@@ -102,8 +103,9 @@ struct MoeArgs {
     const uint8_t *w13, *w2;
     const uint8_t *s13, *s2;
     uint8_t *act;
-    int32_t *active;        // how many experts have a token, then which
-    uint16_t *table;        // of each of them: its pair for every token, or kNone
+    int32_t *active;        // how many experts have a token, and which
+    int32_t *offset;        // where the pairs of each of them begin in `order`, and their end
+    uint16_t *order;        // the pairs by expert
     uint8_t *y;
     int64_t ldx, ldact;     // bytes
     int64_t ld13, e13, ld2, e2;         // bytes: a row, an expert
@@ -111,11 +113,14 @@ struct MoeArgs {
     int64_t ldy;            // elements
     int T, H, I, E, top;
     int most;               // of active experts
-    int tiles;
-    int group, s_type;
+    int tiles;              // workgroups along an expert's rows
+    int wk;                 // waves that share a tile's K
+    int group;
+    uint32_t s_half;        // of I4Scales
+    uint32_t group_magic;
 };
 
-// The experts that some pair names, as bits, and their count; the a-th of them.
+// The experts that some pair names, as bits, and their count; the a-th of them, and which one e is.
 struct Active {
     uint32_t bits[kMaxExperts / 32];
     int count[kMaxExperts / 32];   // in the words before
@@ -152,180 +157,248 @@ __device__ __forceinline__ int nth_active(const Active &act, int a) {
     for (int n = a - act.count[word]; n > 0; --n) left &= left - 1;
     return word * 32 + __builtin_ctz(left);
 }
+__device__ __forceinline__ int rank_of(const Active &act, int e) {
+    return act.count[e / 32] + __builtin_popcount(act.bits[e / 32] & ((1u << (e % 32)) - 1));
+}
 
-// Gate and up rows of one active expert: 8 NT rows of each (tile t of the wave has the gate's
-// rows where t is even, else the up projection's).
-template <int T, int MT, int NT, int W, int Q, bool kS32, int D>
-__global__ __launch_bounds__(W *kWave) void moe_up_kernel(MoeArgs args) {
+// whether an earlier slot of pair p's token names the same expert
+__device__ __forceinline__ bool named_before(const int32_t *ids, int p, int top) {
+    for (int q = p - p % top; q < p; ++q)
+        if (ids[q] == ids[p]) return true;
+    return false;
+}
+
+// active, offset and order, by one workgroup; n: LDS of kMaxExperts
+__device__ __forceinline__ void sort_pairs(const MoeArgs &args, const Active &act, int *n) {
+    const int tid = threadIdx.x, pairs = args.T * args.top;
+    for (int a = tid; a < act.total; a += blockDim.x) {
+        n[a] = 0;
+        args.active[1 + a] = nth_active(act, a);
+    }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += blockDim.x)
+        if ((uint32_t)args.ids[p] < (uint32_t)args.E && !named_before(args.ids, p, args.top))
+            atomicAdd(&n[rank_of(act, args.ids[p])], 1);
+    __syncthreads();
+    if (tid < kWave) {
+        constexpr int kEach = kMaxExperts / kWave;
+        int own = 0;
+        for (int i = 0; i < kEach; ++i) own += tid * kEach + i < act.total ? n[tid * kEach + i] : 0;
+        int sum = own;
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int before = __shfl_up(sum, d);
+            if (tid >= d) sum += before;
+        }
+        int at = sum - own;
+        for (int i = 0; i < kEach; ++i) {
+            const int a = tid * kEach + i;
+            if (a >= act.total) break;
+            const int c = n[a];
+            n[a] = args.offset[a] = at;
+            at += c;
+        }
+        if (tid == kWave - 1) {
+            args.active[0] = act.total;
+            args.offset[act.total] = sum;
+        }
+    }
+    __syncthreads();
+    // (the order within an expert is whichever comes first: nothing is added up along it)
+    for (int p = tid; p < pairs; p += blockDim.x)
+        if ((uint32_t)args.ids[p] < (uint32_t)args.E && !named_before(args.ids, p, args.top))
+            args.order[atomicAdd(&n[rank_of(act, args.ids[p])], 1)] = (uint16_t)p;
+    __syncthreads();
+}
+
+// 16 gate rows of an active expert and the up projection's 16 beside them to args.wk waves, which
+// split K; RA pairs at a time.
+template <int T, int RA, int Q, bool kS32, bool kAhead>
+__global__ __launch_bounds__(512) void moe_up_kernel(MoeArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using Elem = typename ElemOf<T>::type;
-    constexpr int kCols = 8 * NT, kTile = MT * NT * 256;
+    using Wave = I4Wave<T, RA, 2, 2, Q, kS32, kAhead>;
+    constexpr int W = 8;
+    extern __shared__ float own_weight[];   // of the expert's pairs, and the pairs
+    uint16_t *const own = reinterpret_cast<uint16_t *>(own_weight + args.T);
     __shared__ Active active;
-    __shared__ uint16_t list[kMaxPairs];
     __shared__ int listed;
-    __shared__ float part[W][kTile];
+    __shared__ union {
+        int n[kMaxExperts];
+        uint4 xs[W][Wave::kLds];
+        floatx4_t part[W][2][kWave];
+    } lds;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane % 16, g = lane / 16;
-    const int a = blockIdx.x / args.tiles, tile = blockIdx.x % args.tiles;
+    const int a = blockIdx.x / args.tiles;
     const int H = args.H, I = args.I, top = args.top, pairs = args.T * top;
 
     if (tid == 0) listed = 0;
     find_active(active, args.ids, pairs, args.E);
-    if (blockIdx.x == 0 && tid == 0) args.active[0] = active.total;
+    if (blockIdx.x == 0) sort_pairs(args, active, lds.n);
     if (a >= active.total) return;
     const int e = __builtin_amdgcn_readfirstlane(nth_active(active, a));
-    if (tile == 0) {
-        if (tid == 0) args.active[1 + a] = e;
-        for (int t = tid; t < args.T; t += W * kWave) {
-            int p = kNone;
-            for (int s = top - 1; s >= 0; --s)
-                if (args.ids[t * top + s] == e) p = t * top + s;
-            args.table[(int64_t)a * args.T + t] = (uint16_t)p;
-        }
-    }
     for (int p = tid; p < pairs; p += W * kWave)
-        if (args.ids[p] == e) {
-            bool again = false;   // an expert that a token names twice is computed once, with the weights' sum
-            for (int q = p - p % top; q < p; ++q) again |= args.ids[q] == e;
-            if (!again) list[atomicAdd(&listed, 1)] = (uint16_t)p;
+        if (args.ids[p] == e && !named_before(args.ids, p, top)) {
+            float weight = args.weights[p];
+            for (int q = p + 1; q < p - p % top + top; ++q)
+                if (args.ids[q] == e) weight += args.weights[q];
+            const int at = atomicAdd(&listed, 1);
+            own[at] = (uint16_t)p;
+            own_weight[at] = weight;
         }
     __syncthreads();
     const int rows = listed;
 
-    const int i0 = tile * kCols;
-    const int cols = min(kCols, I - i0);
-    using Wave = I4Wave<T, MT, NT, 2, Q, kS32, D>;
+    const int wk = args.wk, k0 = wave % wk;
+    const int i0 = (blockIdx.x % args.tiles * (W / wk) + wave / wk) * 16;
+    const int cols = min(16, I - i0);   // (a wave may have none)
     typename Wave::Source src;
     src.a = args.x;
     src.a_end = (int)((args.T - 1) * args.ldx) + ((2 * H + 15) & ~15);
     const int size = kS32 ? 4 : 2;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        src.b[b] = args.w13 + e * args.e13 + (int64_t)(b * I + i0) * args.ld13;
+        const int64_t row = b * I + i0;
+        src.b[b] = args.w13 + e * args.e13 + row * args.ld13;
         src.b_end[b] = (int)((cols - 1) * args.ld13) + (((H + 1) / 2 + 15) & ~15);
-        src.s[b] = {args.s13 + e * args.es13 + (int64_t)(b * I + i0) * size, args.lds13, args.s_type};
+        src.s[b] = {args.s13 + e * args.es13 + row * size, args.lds13, args.s_half};
+        src.vb[b] = r < cols ? (uint32_t)r * (uint32_t)args.ld13 + 16 * g : kOutside;
+        src.vs[b] = (uint32_t)min(r, cols - 1) * size;
     }
+    src.K = H, src.group_magic = args.group_magic, src.groups = (H + args.group - 1) / args.group;
+    const int units = cols > 0 ? (H + 2 * kStep - 1) / (2 * kStep) : 0;
+    for (int first = 0; first < rows; first += RA) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int row = 16 * (t / 2) + r;
-        src.vb[t] = row < cols ? (uint32_t)row * (uint32_t)args.ld13 + 16 * g : kOutside;
-        src.vs[t] = (uint32_t)min(row, cols - 1) * size;
-    }
-    src.K = H, src.group = args.group;
-    const int steps = (H + kStep - 1) / kStep, lines = (steps + 1) / 2;
-    const int mine = wave < lines ? (lines - wave + W - 1) / W : 0;
-    const int odd = mine > 0 && wave + (mine - 1) * W == lines - 1 ? steps % 2 : 0;
-    for (int first = 0; first < rows; first += 16 * MT) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int at = first + 16 * i + r;
-            src.va[i] = at < rows ? (uint32_t)(list[at] / top) * (uint32_t)args.ldx + 16 * g : kOutside;
+        for (int j = 0; j < Wave::kX; ++j) {
+            const int at = first + Wave::copied_row(j);
+            src.xa[j] = at < rows ? (uint32_t)(own[at] / top) * (uint32_t)args.ldx + 16 * Wave::copied_chunk() : kOutside;
         }
+        int next = k0;
         Wave w;
-        w.run(src, 2 * mine - odd, [&](int i, auto &) { return 2 * (wave + (i >> 1) * W) + (i & 1); });
-        if (first > 0) __syncthreads();
+        w.run(
+            src, lds.xs[wave],
+            [&](auto &, auto &) {
+                if (next >= units) return -1;
+                const int unit = next;
+                next += wk;
+                return unit;
+            },
+            [](auto &) {});
+        if (wk > 1) {
+            __syncthreads();   // (the sums take the activations' place)
+            lds.part[wave][0][lane] = w.acc[0];
+            lds.part[wave][1][lane] = w.acc[1];
+            __syncthreads();
+            if (k0 == 0)
+                for (int k = 1; k < wk; ++k) {
+                    w.acc[0] += lds.part[wave + k][0][lane];
+                    w.acc[1] += lds.part[wave + k][1][lane];
+                }
+            __syncthreads();
+        }
+        if (k0 != 0 || r >= cols) continue;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) part[wave][((i * NT + t) * 4 + k) * kWave + lane] = w.acc[i][t][k];
-        __syncthreads();
-        for (int x = tid; x < 16 * MT * kCols; x += W * kWave) {
-            const int row = x / kCols, col = x % kCols;
-            if (first + row >= rows || col >= cols) continue;
-            const int at = ((row / 16 * NT + col / 16 * 2) * 4 + row % 4) * kWave + row % 16 / 4 * 16 + col % 16;
-            float gate = part[0][at], up = part[0][at + 4 * kWave];
-#pragma unroll
-            for (int v = 1; v < W; ++v) gate += part[v][at], up += part[v][at + 4 * kWave];
-            const int p = list[first + row];
-            float weight = args.weights[p];
-            for (int q = p + 1; q < p - p % top + top; ++q)
-                if (args.ids[q] == e) weight += args.weights[q];
+        for (int k = 0; k < 4; ++k) {
+            const int at = first + 4 * g + k;
+            if (4 * g + k >= RA || at >= rows) break;
+            const float gate = w.acc[0][k], up = w.acc[1][k];
             // (rounded to the type that the second product's matrix instructions take)
-            reinterpret_cast<Elem *>(args.act + (int64_t)p * args.ldact)[i0 + col] =
-                (Elem)(gate / (1.0f + __expf(-gate)) * up * weight);
+            reinterpret_cast<Elem *>(args.act + (int64_t)own[at] * args.ldact)[i0 + r] =
+                (Elem)(gate / (1.0f + __expf(-gate)) * up * own_weight[at]);
         }
     }
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-// Columns of y.  Row t of a fragment of activations is token t's, for every expert: its pair's
-// row of `act`, or nothing, so the experts add up in the accumulators.
-template <int T, int MT, int NT, int W, int Q, bool kS32, int D>
+// 16 columns of y for TT tokens.
+template <int T, int RA, int TT, int W, int Q, bool kS32, bool kAhead>
 __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using Elem = typename ElemOf<T>::type;
-    constexpr int kCols = 16 * NT, kRows = 16 * MT, kTile = MT * NT * 256;
-    extern __shared__ uint8_t lds[];   // the pairs of each expert, then the waves' sums
-    uint16_t *const pair = reinterpret_cast<uint16_t *>(lds);
-    float(*const part)[kTile] = reinterpret_cast<float(*)[kTile]>(lds);
+    using Wave = I4Wave<T, RA, 1, 1, Q, kS32, kAhead>;
+    __shared__ int expert[kMaxExperts], offset[kMaxExperts + 1];
+    __shared__ uint16_t pair[kMaxPairs], token[kMaxPairs];
+    __shared__ uint4 xs[W][Wave::kLds];
+    __shared__ float sums[W][TT][16];
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane % 16, g = lane / 16;
-    const int t0 = blockIdx.x / args.tiles * kRows, n0 = blockIdx.x % args.tiles * kCols;
+    const int t0 = blockIdx.x / args.tiles * TT, n0 = blockIdx.x % args.tiles * 16;
     const int H = args.H, I = args.I;
-    const int experts = __builtin_amdgcn_readfirstlane(min(args.active[0], args.most));
+    const int experts = __builtin_amdgcn_readfirstlane(args.active[0]);
+    const int listed = args.offset[experts];
 
-    for (int x = tid; x < experts * kRows; x += W * kWave) {
-        const int t = t0 + x % kRows;
-        pair[x] = t < args.T ? args.table[(int64_t)(x / kRows) * args.T + t] : (uint16_t)kNone;
+    for (int a = tid; a < experts; a += W * kWave) {
+        expert[a] = args.active[1 + a];
+        offset[a] = args.offset[a];
     }
+    if (tid == 0) offset[experts] = listed;
+    for (int i = tid; i < listed; i += W * kWave) {
+        const int p = args.order[i];
+        pair[i] = (uint16_t)p;
+        token[i] = (uint16_t)(p / args.top);
+    }
+    for (int i = lane; i < TT * 16; i += kWave) (&sums[wave][0][0])[i] = 0.0f;
     __syncthreads();
 
-    using Wave = I4Wave<T, MT, NT, 1, Q, kS32, D, true>;
+    const int cols = min(16, H - n0), size = kS32 ? 4 : 2;
     typename Wave::Source src;
     src.a = args.act;
     src.a_end = (int)((args.T * args.top - 1) * args.ldact) + ((2 * I + 15) & ~15);
-    const int cols = min(kCols, H - n0), size = kS32 ? 4 : 2;
     src.b_end[0] = (int)((cols - 1) * args.ld2) + (((I + 1) / 2 + 15) & ~15);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int row = 16 * t + r;
-        src.vb[t] = row < cols ? (uint32_t)row * (uint32_t)args.ld2 + 16 * g : kOutside;
-        src.vs[t] = (uint32_t)min(row, cols - 1) * size;
-    }
-    src.K = I, src.group = args.group;
-    // unit u: a pair of steps of one expert, wave u % W's
-    const int steps = (I + kStep - 1) / kStep, lines = (steps + 1) / 2;
-    const int units = experts * lines, mine = wave < units ? (units - wave + W - 1) / W : 0;
+    src.vb[0] = r < cols ? (uint32_t)r * (uint32_t)args.ld2 + 16 * g : kOutside;
+    src.vs[0] = (uint32_t)min(r, cols - 1) * size;
+    src.K = I, src.group_magic = args.group_magic, src.groups = (I + args.group - 1) / args.group;
+    // (expert, line) number i is wave i % W's; an expert of more than RA pairs takes a turn for every RA
+    const int lines = (I + 2 * kStep - 1) / (2 * kStep);
     const int by_expert = W / lines, by_line = W % lines;
-    int at = wave / lines, line = wave % lines;   // of the next unit
+    int at = wave / lines, line = wave % lines, first = 0;
     Wave w;
-    w.run(src, 2 * mine, [&](int i, auto &src) -> int {
-        if (i % 2) {   // the second step of the unit, which an odd number of steps leaves out
-            const int step = 2 * line + 1;
-            at += by_expert, line += by_line;
-            if (line >= lines) line -= lines, ++at;
-            return step < steps ? step : -1;
-        }
-        const int e = __builtin_amdgcn_readfirstlane(args.active[1 + at]);
-        src.b[0] = args.w2 + e * args.e2 + (int64_t)n0 * args.ld2;
-        src.s[0] = {args.s2 + e * args.es2 + (int64_t)n0 * size, args.lds2, args.s_type};
+    w.run(
+        src, xs[wave],
+        [&](auto &st, auto &src) {
+            if (at >= experts) return -1;
+            const int e = __builtin_amdgcn_readfirstlane(expert[at]);
+            const int from = __builtin_amdgcn_readfirstlane(offset[at]), to = __builtin_amdgcn_readfirstlane(offset[at + 1]);
+            st.tag = from + first;
+            st.left = min(to - st.tag, RA);
+            src.b[0] = args.w2 + e * args.e2 + (int64_t)n0 * args.ld2;
+            src.s[0] = {args.s2 + e * args.es2 + (int64_t)n0 * size, args.lds2, args.s_half};
 #pragma unroll
-        for (int k = 0; k < MT; ++k) {
-            const uint32_t p = pair[at * kRows + 16 * k + r];
-            src.va[k] = p != kNone ? p * (uint32_t)args.ldact + 16 * g : kOutside;
-        }
-        return 2 * line;
-    });
+            for (int j = 0; j < Wave::kX; ++j) {
+                const int row = Wave::copied_row(j), i = st.tag + min(row, st.left - 1);
+                const bool in = row < st.left && (uint32_t)(token[i] - t0) < (uint32_t)TT;
+                src.xa[j] = in ? (uint32_t)pair[i] * (uint32_t)args.ldact + 16 * Wave::copied_chunk() : kOutside;
+            }
+            const int unit = line;
+            first += RA;
+            if (from + first >= to) {
+                first = 0, at += by_expert, line += by_line;
+                if (line >= lines) line -= lines, ++at;
+            }
+            return unit;
+        },
+        [&](auto &st) {
+            // a token has one pair of an expert: the lanes add to different sums
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int row = 4 * g + k;
+                const int t = token[st.tag + min(row, st.left - 1)] - t0;
+                if (row < st.left && (uint32_t)t < (uint32_t)TT) sums[wave][t][r] += w.acc[0][k];
+            }
+            wave_lds_order();
+            w.clear();
+        });
     __syncthreads();
+    for (int x = tid; x < TT * 16; x += W * kWave) {
+        const int t = x / 16, col = x % 16;
+        if (t0 + t >= args.T || col >= cols) continue;
+        float sum = sums[0][t][col];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) part[wave][((i * NT + t) * 4 + k) * kWave + lane] = w.acc[i][t][k];
-    __syncthreads();
-    for (int x = tid; x < kTile; x += W * kWave) {
-        const int row = x / kCols, col = x % kCols;
-        if (t0 + row >= args.T || col >= cols) continue;
-        const int from = ((row / 16 * NT + col / 16) * 4 + row % 4) * kWave + row % 16 / 4 * 16 + col % 16;
-        float sum = part[0][from];
-#pragma unroll
-        for (int v = 1; v < W; ++v) sum += part[v][from];
-        reinterpret_cast<Elem *>(args.y)[(int64_t)(t0 + row) * args.ldy + n0 + col] = (Elem)sum;
+        for (int v = 1; v < W; ++v) sum += sums[v][t][col];
+        reinterpret_cast<Elem *>(args.y)[(int64_t)(t0 + t) * args.ldy + n0 + col] = (Elem)sum;
     }
 #endif  // __HIP_DEVICE_COMPILE__
 }
@@ -335,17 +408,18 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 
 int64_t round_up(int64_t x, int64_t m) { return cdiv(x, m) * m; }
 
-// The workspace: act, then the active experts, then the table of pairs
+// The workspace: act, the active experts, their offsets, the order of pairs
 struct Workspace {
-    int64_t ldact, active, table, bytes;   // bytes: a row of act; where the others begin; in all
+    int64_t ldact, active, offset, order, bytes;   // bytes: a row of act; where the others begin; in all
 };
 Workspace workspace_of(int64_t T, int64_t top, int64_t I, int64_t E) {
-    const int64_t pairs = T * top, most = E < pairs ? E : pairs;
+    const int64_t pairs = T * top, list = round_up(4 * (1 + (E < pairs ? E : pairs)), 16);
     Workspace w;
     w.ldact = round_up(2 * I, 16);
     w.active = pairs * w.ldact;
-    w.table = w.active + round_up(4 * (1 + most), 16);
-    w.bytes = w.table + round_up(2 * most * T, 16);
+    w.offset = w.active + list;
+    w.order = w.offset + list;
+    w.bytes = w.order + round_up(2 * pairs, 16);
     return w;
 }
 
@@ -355,24 +429,33 @@ bool moe_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top) {
            H <= row / 2 && I <= row / 2 && T * top * (2 * I + 16) <= INT32_MAX;
 }
 
-template <int T, int Q, bool kS32>
+template <int T, int RA, int Q, bool kS32>
 int launch_moe(MoeArgs args, void *stream) {
-    // (a token's experts are few of many: a fragment's 16 rows hold an expert's pairs)
-    args.tiles = (int)cdiv(args.I, 16);
-    int rc = run(reinterpret_cast<const void *>(&moe_up_kernel<T, 1, 2, 8, Q, kS32, 4>), (int64_t)args.most * args.tiles, 512,
-                 &args, stream);
-    if (rc != PDGEMM_OK) return rc;
-    int mt = args.T <= 16 ? 1 : args.T <= 32 ? 2 : 4;
-    while (mt > 1 && 32 * mt * args.most > 64 * 1024) mt /= 2;
-    args.tiles = (int)cdiv(args.H, 16);
-    const int waves = mt == 4 ? 8 : 16;
-    const int join = waves * mt * 1024, table = 32 * mt * args.most, bytes = join > table ? join : table;
-    const void *fn = mt == 1   ? reinterpret_cast<const void *>(&moe_down_kernel<T, 1, 1, 16, Q, kS32, 4>)
-                     : mt == 2 ? reinterpret_cast<const void *>(&moe_down_kernel<T, 2, 1, 16, Q, kS32, 2>)
-                               : reinterpret_cast<const void *>(&moe_down_kernel<T, 4, 1, 8, Q, kS32, 2>);
-    void *kargs[] = {&args};
+    constexpr bool kAhead = true;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    return finish(hipLaunchKernel(fn, dim3((unsigned)(cdiv(args.T, 16 * mt) * args.tiles)), dim3(waves * kWave), kargs, bytes, s), s);
+    const int64_t tiles = cdiv(args.I, 16);
+    // waves that share a tile: as many as make 2048 of them, eight for each CU
+    args.wk = 1;
+    while (args.wk < 8 && args.most * tiles * args.wk < 2048) args.wk *= 2;
+    args.tiles = (int)cdiv(tiles * args.wk, 8);
+    void *kargs[] = {&args};
+    int rc = finish(hipLaunchKernel(reinterpret_cast<const void *>(&moe_up_kernel<T, RA, Q, kS32, kAhead>),
+                                    dim3((unsigned)(args.most * args.tiles)), dim3(512), kargs, 6 * args.T, s), s);
+    if (rc != PDGEMM_OK) return rc;
+    args.tiles = (int)cdiv(args.H, 16);
+    constexpr int W = RA == 2 ? 16 : 8;   // (as registers and LDS allow)
+    if (args.T <= 16)
+        return run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 16, W, Q, kS32, kAhead>), args.tiles, W * kWave, &args, stream);
+    return run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 64, 8, Q, kS32, kAhead>), cdiv(args.T, 64) * args.tiles, 512,
+               &args, stream);
+}
+// Pairs that an expert's rows of codes are read for at once
+template <int T, int Q, bool kS32>
+int launch_moe(const MoeArgs &args, void *stream) {
+    const int pairs = args.T * args.top;
+    return args.T <= 2              ? launch_moe<T, 2, Q, kS32>(args, stream)
+           : pairs <= 6 * args.most ? launch_moe<T, 8, Q, kS32>(args, stream)
+                                    : launch_moe<T, 16, Q, kS32>(args, stream);
 }
 template <int T, bool kS32>
 int launch_moe(const MoeArgs &args, void *stream) {
@@ -450,9 +533,9 @@ int pdgemm_moe_a16_i4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, c
     const int64_t pairs = T * top;
     const MoeArgs args = {static_cast<const uint8_t *>(x), ids, weights, w13, w2, static_cast<const uint8_t *>(s13),
                           static_cast<const uint8_t *>(s2), ws, reinterpret_cast<int32_t *>(ws + w.active),
-                          reinterpret_cast<uint16_t *>(ws + w.table), static_cast<uint8_t *>(y), 2 * ldx, w.ldact, ld13 / 2,
+                          reinterpret_cast<int32_t *>(ws + w.offset), reinterpret_cast<uint16_t *>(ws + w.order), static_cast<uint8_t *>(y), 2 * ldx, w.ldact, ld13 / 2,
                           expert13 / 2, ld2 / 2, expert2 / 2, lds13 * size, expert_s13 * size, lds2 * size, expert_s2 * size, ldy,
-                          (int)T, (int)H, (int)I, (int)E, (int)top, (int)(E < pairs ? E : pairs), 0, (int)group, scale_type};
+                          (int)T, (int)H, (int)I, (int)E, (int)top, (int)(E < pairs ? E : pairs), 0, 1, (int)group, scale_type == kF16 ? ~0u : 0u, I4Groups::magic(group)};
     const bool s32 = scale_type == kF32;
     if (type == kF16) return s32 ? launch_moe<kF16, true>(args, stream) : launch_moe<kF16, false>(args, stream);
     return s32 ? launch_moe<kBF16, true>(args, stream) : launch_moe<kBF16, false>(args, stream);

@@ -58,9 +58,10 @@ P = {n: 0x10000 * (k + 1) for k, n in enumerate(
     ("A", "B", "s", "C", "x", "ids", "w", "w13", "s13", "w2", "s2", "y", "ws", "logits"))}
 
 
-def product(L, M=4, N=80, K=96, lda=96, a_type=2, ldb=96, ldsb=80, stype=0, group=32, ldc=80, type=0, cfg=None, **ptr):
+def product(L, M=4, N=80, K=96, lda=96, a_type=2, ldb=96, ldsb=80, stype=0, group=32, ldc=80, type=0, cfg=None, ws_bytes=1 << 30,
+            **ptr):
     p = {**P, **ptr}
-    args = (M, N, K, p["A"], lda, a_type, p["B"], ldb, p["s"], ldsb, stype, group, p["C"], ldc, type, None)
+    args = (M, N, K, p["A"], lda, a_type, p["B"], ldb, p["s"], ldsb, stype, group, p["C"], ldc, type, p["ws"], ws_bytes, None)
     return L.gemm_a16_i4(*args) if cfg is None else L.pdgemm_a16_i4_cfg(cfg, *args)
 
 
@@ -126,7 +127,7 @@ def test_empty_calls_succeed_without_pointers(lib):
     assert experts(lib, T=0, **none) == 0 and route(lib, T=0, **none) == 0
     assert lib.pdgemm_moe_a16_i4_workspace_size(0, 96, 64, 8, 2) == 0
     assert lib.pdgemm_moe_a16_i4_workspace_size(5, 96, 64, 2000, 2) == 0
-    assert lib.pdgemm_moe_a16_i4_workspace_size(5, 96, 60, 8, 2) == 10 * 128 + 48 + 80
+    assert lib.pdgemm_moe_a16_i4_workspace_size(5, 96, 60, 8, 2) == 10 * 128 + 48 + 48 + 32
 
 
 @built

@@ -11,6 +11,7 @@ namespace {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 64;
 constexpr int kMaxPairs = 4096;
+constexpr int kMaxSplits = 8;
 
 // ---------------------------------------------------------------------------
 // routing
@@ -106,6 +107,7 @@ struct MoeArgs {
     int32_t *active;        // how many experts have a token, and which
     int32_t *offset;        // where the pairs of each of them begin in `order`, and their end
     uint16_t *order;        // the pairs by expert
+    float *part;            // the splits' sums, T x H each
     uint8_t *y;
     int64_t ldx, ldact;     // bytes
     int64_t ld13, e13, ld2, e2;         // bytes: a row, an expert
@@ -115,6 +117,7 @@ struct MoeArgs {
     int most;               // of active experts
     int tiles;              // workgroups along an expert's rows
     int wk;                 // waves that share a tile's K
+    int splits;             // workgroups that share a tile of y
     int group;
     uint32_t s_half;        // of I4Scales
     uint32_t group_magic;
@@ -312,7 +315,10 @@ __global__ __launch_bounds__(512) void moe_up_kernel(MoeArgs args) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-// 16 columns of y for TT tokens.
+// 16 columns of y for TT tokens.  Where there are few such tiles, args.splits workgroups share
+// the (expert, line) pairs of one, and their sums are added up by moe_join_kernel.  (With the last of them to
+// finish adding up what the others wrote, ordered by fences of the device's scope, 16 tokens through 8 of 128
+// experts took 180 us instead of 50: such a fence writes back and drops a whole L2.)
 template <int T, int RA, int TT, int W, int Q, bool kS32, bool kAhead>
 __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -325,7 +331,8 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane % 16, g = lane / 16;
-    const int t0 = blockIdx.x / args.tiles * TT, n0 = blockIdx.x % args.tiles * 16;
+    const int tile = blockIdx.x / args.splits, split = blockIdx.x % args.splits;
+    const int t0 = tile / args.tiles * TT, n0 = tile % args.tiles * 16;
     const int H = args.H, I = args.I;
     const int experts = __builtin_amdgcn_readfirstlane(args.active[0]);
     const int listed = args.offset[experts];
@@ -351,10 +358,11 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
     src.vb[0] = r < cols ? (uint32_t)r * (uint32_t)args.ld2 + 16 * g : kOutside;
     src.vs[0] = (uint32_t)min(r, cols - 1) * size;
     src.K = I, src.group_magic = args.group_magic, src.groups = (I + args.group - 1) / args.group;
-    // (expert, line) number i is wave i % W's; an expert of more than RA pairs takes a turn for every RA
+    // (expert, line) number i is wave i's of the splits' waves, round and round; an expert of more than RA
+    // pairs takes a turn for every RA
     const int lines = (I + 2 * kStep - 1) / (2 * kStep);
-    const int by_expert = W / lines, by_line = W % lines;
-    int at = wave / lines, line = wave % lines, first = 0;
+    const int stride = W * args.splits, by_expert = stride / lines, by_line = stride % lines;
+    int at = (split * W + wave) / lines, line = (split * W + wave) % lines, first = 0;
     Wave w;
     w.run(
         src, xs[wave],
@@ -398,8 +406,28 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
         float sum = sums[0][t][col];
 #pragma unroll
         for (int v = 1; v < W; ++v) sum += sums[v][t][col];
-        reinterpret_cast<Elem *>(args.y)[(int64_t)(t0 + t) * args.ldy + n0 + col] = (Elem)sum;
+        if (args.splits == 1)
+            reinterpret_cast<Elem *>(args.y)[(int64_t)(t0 + t) * args.ldy + n0 + col] = (Elem)sum;
+        else
+            args.part[((int64_t)split * args.T + t0 + t) * H + n0 + col] = sum;
     }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// y from the splits' sums, added in their order.
+template <int T>
+__global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs args) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using Elem = typename ElemOf<T>::type;
+    const int x = blockIdx.x * 256 + threadIdx.x, t = x / args.H, col = x % args.H;
+    if (t >= args.T) return;
+    float v[kMaxSplits], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) v[k] = k < args.splits ? args.part[(int64_t)k * args.T * args.H + x] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+        if (k < args.splits) sum += v[k];
+    reinterpret_cast<Elem *>(args.y)[(int64_t)t * args.ldy + col] = (Elem)sum;
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -408,18 +436,32 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 
 int64_t round_up(int64_t x, int64_t m) { return cdiv(x, m) * m; }
 
-// The workspace: act, the active experts, their offsets, the order of pairs
+// Tiles of y, of 16 columns for up to 64 tokens, and how many workgroups share one: as many as make
+// 512, two for each CU, each of a few experts
+int64_t y_tiles(int64_t T, int64_t H) { return cdiv(T, 64) * cdiv(H, 16); }
+int splits_of(int64_t T, int64_t H, int64_t most) {
+    int64_t s = 512 / y_tiles(T, H);
+    if (s > most / 4) s = most / 4;
+    return s < 2 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
+}
+
+// The workspace: act, the active experts, their offsets, the order of pairs, the splits' sums
 struct Workspace {
-    int64_t ldact, active, offset, order, bytes;   // bytes: a row of act; where the others begin; in all
+    int64_t ldact, active, offset, order, part, bytes;   // bytes: a row of act; where the others begin; in all
+    int most, splits;
 };
-Workspace workspace_of(int64_t T, int64_t top, int64_t I, int64_t E) {
-    const int64_t pairs = T * top, list = round_up(4 * (1 + (E < pairs ? E : pairs)), 16);
+Workspace workspace_of(int64_t T, int64_t top, int64_t H, int64_t I, int64_t E) {
+    const int64_t pairs = T * top;
     Workspace w;
+    w.most = (int)(E < pairs ? E : pairs);
+    w.splits = splits_of(T, H, w.most);
+    const int64_t list = round_up(4 * (1 + w.most), 16);
     w.ldact = round_up(2 * I, 16);
     w.active = pairs * w.ldact;
     w.offset = w.active + list;
     w.order = w.offset + list;
-    w.bytes = w.order + round_up(2 * pairs, 16);
+    w.part = w.order + round_up(2 * pairs, 16);
+    w.bytes = w.part + (w.splits > 1 ? round_up(4 * w.splits * T * H, 16) : 0);
     return w;
 }
 
@@ -444,17 +486,20 @@ int launch_moe(MoeArgs args, void *stream) {
     if (rc != PDGEMM_OK) return rc;
     args.tiles = (int)cdiv(args.H, 16);
     constexpr int W = RA == 2 ? 16 : 8;   // (as registers and LDS allow)
-    if (args.T <= 16)
-        return run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 16, W, Q, kS32, kAhead>), args.tiles, W * kWave, &args, stream);
-    return run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 64, 8, Q, kS32, kAhead>), cdiv(args.T, 64) * args.tiles, 512,
-               &args, stream);
+    const int64_t blocks = y_tiles(args.T, args.H) * args.splits;
+    rc = args.T <= 16 ? run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 16, W, Q, kS32, kAhead>), blocks, W * kWave,
+                            &args, stream)
+                      : run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 64, 8, Q, kS32, kAhead>), blocks, 512, &args,
+                            stream);
+    if (rc != PDGEMM_OK || args.splits == 1) return rc;
+    return run(reinterpret_cast<const void *>(&moe_join_kernel<T>), cdiv((int64_t)args.T * args.H, 256), 256, &args, stream);
 }
 // Pairs that an expert's rows of codes are read for at once
 template <int T, int Q, bool kS32>
 int launch_moe(const MoeArgs &args, void *stream) {
     const int pairs = args.T * args.top;
     return args.T <= 2              ? launch_moe<T, 2, Q, kS32>(args, stream)
-           : pairs <= 6 * args.most ? launch_moe<T, 8, Q, kS32>(args, stream)
+           : pairs <= 8 * args.most ? launch_moe<T, 8, Q, kS32>(args, stream)
                                     : launch_moe<T, 16, Q, kS32>(args, stream);
 }
 template <int T, bool kS32>
@@ -500,7 +545,7 @@ int pdgemm_moe_route(int64_t T, int64_t E, int64_t top, const void *logits, int6
 }
 
 int64_t pdgemm_moe_a16_i4_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top) {
-    return moe_sizes_ok(T, H, I, E, top) && T > 0 ? workspace_of(T, top, I, E).bytes : 0;
+    return moe_sizes_ok(T, H, I, E, top) && T > 0 ? workspace_of(T, top, H, I, E).bytes : 0;
 }
 
 int pdgemm_moe_a16_i4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, const void *x, int64_t ldx, int type,
@@ -525,17 +570,17 @@ int pdgemm_moe_a16_i4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, c
     if (rc == PDGEMM_OK && T * ldx * 2 > INT32_MAX) rc = PDGEMM_EINVAL_LD;
     if (rc == PDGEMM_OK && (ldx % 8 || ((uintptr_t)x & 15))) rc = PDGEMM_EALIGN;
     if (rc == PDGEMM_OK && !workspace) rc = PDGEMM_ENULL;
-    const Workspace w = workspace_of(T, top, I, E);
+    const Workspace w = workspace_of(T, top, H, I, E);
     if (rc == PDGEMM_OK && (workspace_bytes < w.bytes || ((uintptr_t)workspace & 15))) rc = PDGEMM_EWORKSPACE;
     if (rc != PDGEMM_OK) return rc;
     uint8_t *const ws = static_cast<uint8_t *>(workspace);
     const int size = elem_size(scale_type);
-    const int64_t pairs = T * top;
     const MoeArgs args = {static_cast<const uint8_t *>(x), ids, weights, w13, w2, static_cast<const uint8_t *>(s13),
                           static_cast<const uint8_t *>(s2), ws, reinterpret_cast<int32_t *>(ws + w.active),
-                          reinterpret_cast<int32_t *>(ws + w.offset), reinterpret_cast<uint16_t *>(ws + w.order), static_cast<uint8_t *>(y), 2 * ldx, w.ldact, ld13 / 2,
+                          reinterpret_cast<int32_t *>(ws + w.offset), reinterpret_cast<uint16_t *>(ws + w.order), reinterpret_cast<float *>(ws + w.part), static_cast<uint8_t *>(y), 2 * ldx, w.ldact, ld13 / 2,
                           expert13 / 2, ld2 / 2, expert2 / 2, lds13 * size, expert_s13 * size, lds2 * size, expert_s2 * size, ldy,
-                          (int)T, (int)H, (int)I, (int)E, (int)top, (int)(E < pairs ? E : pairs), 0, 1, (int)group, scale_type == kF16 ? ~0u : 0u, I4Groups::magic(group)};
+                          (int)T, (int)H, (int)I, (int)E, (int)top, w.most, 0, 1, w.splits, (int)group,
+                          scale_type == kF16 ? ~0u : 0u, I4Groups::magic(group)};
     const bool s32 = scale_type == kF32;
     if (type == kF16) return s32 ? launch_moe<kF16, true>(args, stream) : launch_moe<kF16, false>(args, stream);
     return s32 ? launch_moe<kBF16, true>(args, stream) : launch_moe<kBF16, false>(args, stream);

@@ -127,7 +127,7 @@ def test_empty_calls_succeed_without_pointers(lib):
     assert experts(lib, T=0, **none) == 0 and route(lib, T=0, **none) == 0
     assert lib.pdgemm_moe_a16_i4_workspace_size(0, 96, 64, 8, 2) == 0
     assert lib.pdgemm_moe_a16_i4_workspace_size(5, 96, 64, 2000, 2) == 0
-    assert lib.pdgemm_moe_a16_i4_workspace_size(5, 96, 60, 8, 2) == 10 * 128 + 48 + 48 + 32
+    assert lib.pdgemm_moe_a16_i4_workspace_size(5, 96, 60, 8, 2) == 10 * 128 + 48 + 48 + 32 + 2 * 4 * 5 * 96
 
 
 @built

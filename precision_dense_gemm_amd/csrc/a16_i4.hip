@@ -53,12 +53,11 @@ __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
     using Wave = I4Wave<T, RA, NT, 1, Q, kS32, kAhead>;
     constexpr int kTile = NT * 256;
     __shared__ union {
-        uint4 xs[W][Wave::kLds];
+        typename Wave::Lds wave[W];
         float part[W][kTile];
     } lds;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int r = lane % 16, g = lane / 16;
     const int m0 = (blockIdx.x / args.tiles_n) * RA, n0 = (blockIdx.x % args.tiles_n) * 16 * NT;
     const int M = args.M, N = args.N, K = args.K;
 
@@ -75,9 +74,12 @@ __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
     const int size = kS32 ? 4 : 2;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int row = 16 * t + r;
-        src.vb[t] = row < N - n0 ? (uint32_t)row * (uint32_t)args.ldb + 16 * g : kOutside;
-        src.vs[t] = (uint32_t)(n0 + min(row, N - n0 - 1)) * size;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = 16 * t + Wave::code_row(j);
+            src.vb[t][j] = row < N - n0 ? (uint32_t)row * (uint32_t)args.ldb + 16 * Wave::code_chunk() : kOutside;
+        }
+        src.vs[t] = (uint32_t)(n0 + min(16 * t + lane % 16, N - n0 - 1)) * size;
     }
     src.s[0] = args.s;
     src.K = K, src.group_magic = args.group_magic, src.groups = (K + args.group - 1) / args.group;
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
     int next = wave;
     Wave w;
     w.run(
-        src, lds.xs[wave],
+        src, lds.wave[wave],
         [&](auto &, auto &) {
             if (next >= units) return -1;
             const int unit = next + turned;

@@ -140,8 +140,8 @@ struct I4Scales {
 };
 
 // Where a wave reads: up to 16 rows of activations, and NT fragments of 16 rows of weights,
-// whose tile t has its codes in matrix t % NB (the gate's and the up projection's, say).
-// xa: byte offsets of the rows that this lane copies (see I4Wave), kOutside: no row.
+// whose tile t has its codes in matrix t % NB (the gate's and the up projection's, say).  xa, vb: byte offsets of
+// the rows that this lane copies and its 16 bytes of them (see I4Wave), kOutside: no row.
 template <int kX, int NT, int NB>
 struct I4Source {
     const uint8_t *a;          // activations; K values a row
@@ -149,9 +149,9 @@ struct I4Source {
     uint32_t xa[kX];
     const uint8_t *b[NB];      // codes
     int b_end[NB];
-    uint32_t vb[NT];           // this lane's row l % 16 of each fragment, plus 16 (l / 16)
+    uint32_t vb[NT][2];
     I4Scales s[NB];
-    uint32_t vs[NT];           // byte offset of this lane's row's scale
+    uint32_t vs[NT];           // byte offset of the scale of this lane's row l % 16
     int K;
     uint32_t group_magic;      // of I4Groups
     int groups;
@@ -168,20 +168,27 @@ struct I4Groups {
 };
 
 // A wave's sums over units of 256 values of K: a whole 128-byte line of each row of codes, two
-// steps.  The codes come straight into the lanes that convert them; the activations (RA rows: 2, 8
-// or 16; a fragment's further rows repeat them) as runs of 512 bytes, through LDS of
-// the wave's own.  Q: blocks that share a scale (4: groups of whole steps, 2: of multiples
-// of 64 values, 1: any).  kS32: binary32 scales.  kAhead: see run.
+// steps.  Everything is loaded in whole lines, 8 lanes to a line of codes and 32 to a run of 512 bytes of
+// activations, and goes through LDS of the wave's own to the lanes that want it.  (Codes loaded by the lanes
+// that convert them, 16 rows to an instruction, ask the L1 for four times as many lines.)  RA rows of activations: 2,
+// 8 or 16; a fragment's further rows repeat them.  Q: blocks that share a scale (4: groups of
+// whole steps, 2: of multiples of 64 values, 1: any).  kS32: binary32 scales.  kAhead: see run.
 template <int T, int RA, int NT, int NB, int Q, bool kS32, bool kAhead>
 struct I4Wave {
-    static constexpr int kSc = 4 / Q;      // scales per step
-    static constexpr int kX = RA / 2;      // loads of two rows of activations
-    static constexpr int kLds = RA * 32;   // uint4 of LDS a wave needs
+    static constexpr int kSc = 4 / Q;            // scales per step
+    static constexpr int kX = RA / 2;            // loads of two rows of activations
+    static constexpr int kLoads = Q == 1 ? 2 : 1;   // loads of scales of four groups
     using Source = I4Source<kX, NT, NB>;
+    // chunk c (16 bytes) of row r at c ^ (r % 8): rows that are read together lie in different banks
+    struct Lds {
+        uint4 x[RA][32];
+        uint4 b[NT][16][8];
+        float s[NT][16][2 * kSc];
+    };
     struct Stage {
         uint4 b[NT][2];
         uint4 x[kX];
-        uint32_t s[NT][2 * kSc];
+        uint32_t s[NT][kLoads];
         int unit;
         int tag, left;   // the item's own
     };
@@ -190,6 +197,9 @@ struct I4Wave {
     // row of activations that this lane copies in load j, and its 16 bytes of the run
     static __device__ __forceinline__ int copied_row(int j) { return 2 * j + (threadIdx.x % kWave) / 32; }
     static __device__ __forceinline__ int copied_chunk() { return threadIdx.x % 32; }
+    // and of a fragment of codes
+    static __device__ __forceinline__ int code_row(int j) { return 8 * j + (threadIdx.x % kWave) / 8; }
+    static __device__ __forceinline__ int code_chunk() { return threadIdx.x % 8; }
 
     __device__ __forceinline__ void load(Stage &st, const Source &src, int unit) {
         st.unit = unit;
@@ -198,27 +208,29 @@ struct I4Wave {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const auto rb = rsrc(src.b[t % NB], src.b_end[t % NB]);
-            st.b[t][0] = load16(rb, src.vb[t], unit * 128);
-            st.b[t][1] = load16(rb, src.vb[t] + 64, unit * 128);
+            st.b[t][0] = load16(rb, src.vb[t][0], unit * 128);
+            st.b[t][1] = load16(rb, src.vb[t][1], unit * 128);
         }
         const auto ra = rsrc(src.a, src.a_end);
 #pragma unroll
         for (int j = 0; j < kX; ++j) st.x[j] = load16(ra, src.xa[j], unit * 512);
 #pragma unroll
-        for (int u = 0; u < 2 * kSc; ++u) {
-            const int q = I4Groups::of(unit * 8 + u * Q, src.group_magic, src.groups);
+        for (int k = 0; k < kLoads; ++k) {
+            const int i = 4 * k + threadIdx.x % kWave / 16, block = unit * 8 + i * Q;
+            // (scales past K are zeros: they may not be there)
+            const bool in = i < 2 * kSc && block * kBlock < src.K;
+            const int64_t q = I4Groups::of(block, src.group_magic, src.groups);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                st.s[t][k] = 0;
                 const uint8_t *const p = src.s[t % NB].p + q * src.s[t % NB].ld + src.vs[t];
-                if constexpr (kS32)
-                    st.s[t][u] = *reinterpret_cast<const uint32_t *>(p);
-                else
-                    st.s[t][u] = *reinterpret_cast<const uint16_t *>(p);
+                if (in) st.s[t][k] = kS32 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p);
             }
         }
     }
 
-    __device__ __forceinline__ void add(Stage &st, const Source &src, uint4 (*xs)[32]) {
+    __device__ __forceinline__ void add(Stage &st, const Source &src, Lds &lds) {
+        const int lane = threadIdx.x % kWave;
         if (__builtin_expect(st.unit * 2 * kStep + 2 * kStep > src.K, 0)) {
             // activations at and past K may be anything, a NaN too: they become zeros
             const int n = src.K - st.unit * 2 * kStep - copied_chunk() * 8;
@@ -228,42 +240,68 @@ struct I4Wave {
 #pragma unroll
             for (int j = 0; j < kX; ++j)
                 st.x[j] = make_uint4(st.x[j].x & m[0], st.x[j].y & m[1], st.x[j].z & m[2], st.x[j].w & m[3]);
-            // and so do the scales of groups past it, which may not be there
+        }
 #pragma unroll
-            for (int u = 0; u < 2 * kSc; ++u)
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) lds.b[t][code_row(j)][code_chunk() ^ (code_row(j) % 8)] = st.b[t][j];
+#pragma unroll
+        for (int j = 0; j < kX; ++j) lds.x[copied_row(j)][copied_chunk() ^ (copied_row(j) % 8)] = st.x[j];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            if (4 * k + lane / 16 < 2 * kSc)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    if (st.unit * 2 * kStep + u * Q * kBlock >= src.K) st.s[t][u] = 0;
-        }
-        // chunk c of row r at c ^ (r % 8): rows that are read together lie in different banks
-#pragma unroll
-        for (int j = 0; j < kX; ++j) xs[copied_row(j)][copied_chunk() ^ (copied_row(j) % 8)] = st.x[j];
+                    lds.s[t][lane % 16][4 * k + lane / 16] = scale_value<kS32>(st.s[t][k], src.s[0].half);
         wave_lds_order();
         floatx4_t d[NT];
-        sum_unit<true>(d, st, src, xs);
+        sum_unit<true>(d, lds);
         float odd = 0;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) odd = __builtin_fmaf(d[t][e], 0.0f, odd);
-        if (__builtin_expect(__any(!(odd == 0.0f)), 0)) sum_unit<false>(d, st, src, xs);   // (NaN: infinity or NaN in d)
+        if (__builtin_expect(__any(!(odd == 0.0f)), 0)) sum_unit<false>(d, lds);   // (NaN: infinity or NaN in d)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[t] += d[t];
         wave_lds_order();
     }
 
+    // the dwords of matrix instructions 0 .. 3 of step h of fragment t
+    static __device__ __forceinline__ void codes(uint32_t (&w)[4], const Lds &lds, int t, int h) {
+        const int lane = threadIdx.x % kWave, g = lane / 16, r = lane % 16;
+        if constexpr (Q == 4) {
+            const uint4 v = lds.b[t][r][(4 * h + g) ^ (r % 8)];
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else if constexpr (Q == 2) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint2 x = reinterpret_cast<const uint2 *>(&lds.b[t][r][(4 * h + 2 * v + (g & 1)) ^ (r % 8)])[g >> 1];
+                w[2 * v] = x.x, w[2 * v + 1] = x.y;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) w[u] = reinterpret_cast<const uint32_t *>(&lds.b[t][r][(4 * h + u) ^ (r % 8)])[g];
+        }
+    }
+
     // a unit's sums
     template <bool kBiased>
-    __device__ __forceinline__ void sum_unit(floatx4_t (&d)[NT], const Stage &st, const Source &src, uint4 (*xs)[32]) {
+    static __device__ __forceinline__ void sum_unit(floatx4_t (&d)[NT], const Lds &lds) {
         const int lane = threadIdx.x % kWave, g = lane / 16, row = lane % RA % 16;
         constexpr uint32_t kB = Biased<T>::kBiasPair;
+        float s[NT][2 * kSc];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) d[t] = floatx4_t{0, 0, 0, 0};
+        for (int t = 0; t < NT; ++t) {
+            d[t] = floatx4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int v = 0; v < 2 * kSc; ++v) s[t][v] = lds.s[t][lane % 16][v] * (kBiased ? Biased<T>::f : 16.0f);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint4 a[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) a[u] = xs[row][(16 * h + position<Q>(u, g)) ^ (row % 8)];
+            for (int u = 0; u < 4; ++u) a[u] = lds.x[row][(16 * h + position<Q>(u, g)) ^ (row % 8)];
             floatx4_t bias[kSc];
 #pragma unroll
             for (int v = 0; v < kSc; ++v) {
@@ -274,17 +312,16 @@ struct I4Wave {
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                uint32_t w[4] = {st.b[t][h].x, st.b[t][h].y, st.b[t][h].z, st.b[t][h].w};
-                share_out<Q>(w);
+                uint32_t w[4];
+                codes(w, lds, t, h);
 #pragma unroll
                 for (int v = 0; v < kSc; ++v) {
                     floatx4_t p = bias[v];
 #pragma unroll
                     for (int u = 0; u < Q; ++u)
                         p = mfma16<T>(a[v * Q + u], kBiased ? widen_biased<T>(w[v * Q + u]) : widen<T>(w[v * Q + u]), p);
-                    const float s = scale_value<kS32>(st.s[t][h * kSc + v], src.s[0].half) * (kBiased ? Biased<T>::f : 16.0f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d[t][e] = __builtin_fmaf(p[e], s, d[t][e]);
+                    for (int e = 0; e < 4; ++e) d[t][e] = __builtin_fmaf(p[e], s[t][h * kSc + v], d[t][e]);
                 }
             }
         }
@@ -296,19 +333,19 @@ struct I4Wave {
     }
 
     // The wave's units in turn: item(st, src) gives the next one, and its source in src, or -1 after
-    // the last; done(st) is called after each unit's sums.  xs: LDS of the wave's own.
+    // the last; done(st) is called after each unit's sums.
     // The next unit's loads are on their way while one is summed (kAhead), or not.  One copy of the code,
     // and registers moved: with the loop unrolled so that none are, two to four units ahead, one row
     // against 8192 x 8192 took 9.1 to 10.2 us instead of 8.1, for a launch fetches its code anew.
     template <typename F, typename G>
-    __device__ __forceinline__ void run(Source &src, uint4 *xs, F &&item, G &&done) {
+    __device__ __forceinline__ void run(Source &src, Lds &lds, F &&item, G &&done) {
         clear();
         Stage next;
         load(next, src, item(next, src));
         while (next.unit >= 0) {
             Stage st = next;
             if constexpr (kAhead) load(next, src, item(next, src));
-            add(st, src, reinterpret_cast<uint4(*)[32]>(xs));
+            add(st, src, lds);
             done(st);
             if constexpr (!kAhead) load(next, src, item(next, src));
         }

@@ -12,6 +12,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 64;
 constexpr int kMaxPairs = 4096;
 constexpr int kMaxSplits = 8;
+constexpr int kUpWaves = 4;   // of a workgroup of the first product
 
 // ---------------------------------------------------------------------------
 // routing
@@ -129,10 +130,8 @@ struct Active {
     int count[kMaxExperts / 32];   // in the words before
     int total;
 };
-__device__ __forceinline__ void find_active(Active &act, const int32_t *ids, int pairs, int E) {
+__device__ __forceinline__ void find_active(Active &act, const int *ids, int pairs, int E) {   // (ids in LDS)
     const int tid = threadIdx.x;
-    if (tid < kMaxExperts / 32) act.bits[tid] = 0;
-    __syncthreads();
     for (int p = tid; p < pairs; p += blockDim.x) {
         const int e = ids[p];
         if ((uint32_t)e < (uint32_t)E) atomicOr(&act.bits[e / 32], 1u << (e % 32));
@@ -164,15 +163,15 @@ __device__ __forceinline__ int rank_of(const Active &act, int e) {
     return act.count[e / 32] + __builtin_popcount(act.bits[e / 32] & ((1u << (e % 32)) - 1));
 }
 
-// whether an earlier slot of pair p's token names the same expert
-__device__ __forceinline__ bool named_before(const int32_t *ids, int p, int top) {
-    for (int q = p - p % top; q < p; ++q)
-        if (ids[q] == ids[p]) return true;
-    return false;
+// whether an earlier slot of pair p's token names the same expert (ids in LDS)
+__device__ __forceinline__ bool named_before(const int *ids, int p, int top) {
+    bool found = false;
+    for (int q = p - p % top; q < p; ++q) found |= ids[q] == ids[p];
+    return found;
 }
 
-// active, offset and order, by one workgroup; n: LDS of kMaxExperts
-__device__ __forceinline__ void sort_pairs(const MoeArgs &args, const Active &act, int *n) {
+// active, offset and order, by one workgroup; ids, n: LDS, n of kMaxExperts
+__device__ __forceinline__ void sort_pairs(const MoeArgs &args, const Active &act, const int *ids, int *n) {
     const int tid = threadIdx.x, pairs = args.T * args.top;
     for (int a = tid; a < act.total; a += blockDim.x) {
         n[a] = 0;
@@ -180,8 +179,7 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs &args, const Active &ac
     }
     __syncthreads();
     for (int p = tid; p < pairs; p += blockDim.x)
-        if ((uint32_t)args.ids[p] < (uint32_t)args.E && !named_before(args.ids, p, args.top))
-            atomicAdd(&n[rank_of(act, args.ids[p])], 1);
+        if ((uint32_t)ids[p] < (uint32_t)args.E && !named_before(ids, p, args.top)) atomicAdd(&n[rank_of(act, ids[p])], 1);
     __syncthreads();
     if (tid < kWave) {
         constexpr int kEach = kMaxExperts / kWave;
@@ -209,26 +207,28 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs &args, const Active &ac
     __syncthreads();
     // (the order within an expert is whichever comes first: nothing is added up along it)
     for (int p = tid; p < pairs; p += blockDim.x)
-        if ((uint32_t)args.ids[p] < (uint32_t)args.E && !named_before(args.ids, p, args.top))
-            args.order[atomicAdd(&n[rank_of(act, args.ids[p])], 1)] = (uint16_t)p;
+        if ((uint32_t)ids[p] < (uint32_t)args.E && !named_before(ids, p, args.top))
+            args.order[atomicAdd(&n[rank_of(act, ids[p])], 1)] = (uint16_t)p;
     __syncthreads();
 }
 
 // 16 gate rows of an active expert and the up projection's 16 beside them to args.wk waves, which
 // split K; RA pairs at a time.
 template <int T, int RA, int Q, bool kS32, bool kAhead>
-__global__ __launch_bounds__(512) void moe_up_kernel(MoeArgs args) {
+__global__ __launch_bounds__(kUpWaves *kWave) void moe_up_kernel(MoeArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using Elem = typename ElemOf<T>::type;
     using Wave = I4Wave<T, RA, 2, 2, Q, kS32, kAhead>;
-    constexpr int W = 8;
-    extern __shared__ float own_weight[];   // of the expert's pairs, and the pairs
+    constexpr int W = kUpWaves;
+    // all pairs' experts and weights, then the expert's own pairs and their weights
+    extern __shared__ int ids[];
+    float *const weights = reinterpret_cast<float *>(ids + args.T * args.top), *const own_weight = weights + args.T * args.top;
     uint16_t *const own = reinterpret_cast<uint16_t *>(own_weight + args.T);
     __shared__ Active active;
     __shared__ int listed;
     __shared__ union {
         int n[kMaxExperts];
-        uint4 xs[W][Wave::kLds];
+        typename Wave::Lds wave[W];
         floatx4_t part[W][2][kWave];
     } lds;
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -238,15 +238,20 @@ __global__ __launch_bounds__(512) void moe_up_kernel(MoeArgs args) {
     const int H = args.H, I = args.I, top = args.top, pairs = args.T * top;
 
     if (tid == 0) listed = 0;
-    find_active(active, args.ids, pairs, args.E);
-    if (blockIdx.x == 0) sort_pairs(args, active, lds.n);
+    if (tid < kMaxExperts / 32) active.bits[tid] = 0;
+    for (int p = tid; p < pairs; p += W * kWave) {
+        ids[p] = args.ids[p];
+        weights[p] = args.weights[p];
+    }
+    __syncthreads();
+    find_active(active, ids, pairs, args.E);
+    if (blockIdx.x == 0) sort_pairs(args, active, ids, lds.n);
     if (a >= active.total) return;
     const int e = __builtin_amdgcn_readfirstlane(nth_active(active, a));
     for (int p = tid; p < pairs; p += W * kWave)
-        if (args.ids[p] == e && !named_before(args.ids, p, top)) {
-            float weight = args.weights[p];
-            for (int q = p + 1; q < p - p % top + top; ++q)
-                if (args.ids[q] == e) weight += args.weights[q];
+        if (ids[p] == e && !named_before(ids, p, top)) {
+            float weight = weights[p];
+            for (int q = p + 1; q < p - p % top + top; ++q) weight += ids[q] == e ? weights[q] : 0.0f;
             const int at = atomicAdd(&listed, 1);
             own[at] = (uint16_t)p;
             own_weight[at] = weight;
@@ -267,7 +272,11 @@ __global__ __launch_bounds__(512) void moe_up_kernel(MoeArgs args) {
         src.b[b] = args.w13 + e * args.e13 + row * args.ld13;
         src.b_end[b] = (int)((cols - 1) * args.ld13) + (((H + 1) / 2 + 15) & ~15);
         src.s[b] = {args.s13 + e * args.es13 + row * size, args.lds13, args.s_half};
-        src.vb[b] = r < cols ? (uint32_t)r * (uint32_t)args.ld13 + 16 * g : kOutside;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int at = Wave::code_row(j);
+            src.vb[b][j] = at < cols ? (uint32_t)at * (uint32_t)args.ld13 + 16 * Wave::code_chunk() : kOutside;
+        }
         src.vs[b] = (uint32_t)min(r, cols - 1) * size;
     }
     src.K = H, src.group_magic = args.group_magic, src.groups = (H + args.group - 1) / args.group;
@@ -281,7 +290,7 @@ __global__ __launch_bounds__(512) void moe_up_kernel(MoeArgs args) {
         int next = k0;
         Wave w;
         w.run(
-            src, lds.xs[wave],
+            src, lds.wave[wave],
             [&](auto &, auto &) {
                 if (next >= units) return -1;
                 const int unit = next;
@@ -326,7 +335,7 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
     using Wave = I4Wave<T, RA, 1, 1, Q, kS32, kAhead>;
     __shared__ int expert[kMaxExperts], offset[kMaxExperts + 1];
     __shared__ uint16_t pair[kMaxPairs], token[kMaxPairs];
-    __shared__ uint4 xs[W][Wave::kLds];
+    __shared__ typename Wave::Lds own[W];
     __shared__ float sums[W][TT][16];
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -334,15 +343,14 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
     const int tile = blockIdx.x / args.splits, split = blockIdx.x % args.splits;
     const int t0 = tile / args.tiles * TT, n0 = tile % args.tiles * 16;
     const int H = args.H, I = args.I;
-    const int experts = __builtin_amdgcn_readfirstlane(args.active[0]);
-    const int listed = args.offset[experts];
 
-    for (int a = tid; a < experts; a += W * kWave) {
-        expert[a] = args.active[1 + a];
+    // (whole lists, so that no load waits for another's count: what lies past the counts is not looked at)
+    const int experts = __builtin_amdgcn_readfirstlane(args.active[0]);
+    for (int a = tid; a <= args.most; a += W * kWave) {
+        if (a < args.most) expert[a] = args.active[1 + a];
         offset[a] = args.offset[a];
     }
-    if (tid == 0) offset[experts] = listed;
-    for (int i = tid; i < listed; i += W * kWave) {
+    for (int i = tid; i < args.T * args.top; i += W * kWave) {
         const int p = args.order[i];
         pair[i] = (uint16_t)p;
         token[i] = (uint16_t)(p / args.top);
@@ -355,7 +363,11 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
     src.a = args.act;
     src.a_end = (int)((args.T * args.top - 1) * args.ldact) + ((2 * I + 15) & ~15);
     src.b_end[0] = (int)((cols - 1) * args.ld2) + (((I + 1) / 2 + 15) & ~15);
-    src.vb[0] = r < cols ? (uint32_t)r * (uint32_t)args.ld2 + 16 * g : kOutside;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int row = Wave::code_row(j);
+        src.vb[0][j] = row < cols ? (uint32_t)row * (uint32_t)args.ld2 + 16 * Wave::code_chunk() : kOutside;
+    }
     src.vs[0] = (uint32_t)min(r, cols - 1) * size;
     src.K = I, src.group_magic = args.group_magic, src.groups = (I + args.group - 1) / args.group;
     // (expert, line) number i is wave i's of the splits' waves, round and round; an expert of more than RA
@@ -365,7 +377,7 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
     int at = (split * W + wave) / lines, line = (split * W + wave) % lines, first = 0;
     Wave w;
     w.run(
-        src, xs[wave],
+        src, own[wave],
         [&](auto &st, auto &src) {
             if (at >= experts) return -1;
             const int e = __builtin_amdgcn_readfirstlane(expert[at]);
@@ -437,10 +449,10 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs args) {
 int64_t round_up(int64_t x, int64_t m) { return cdiv(x, m) * m; }
 
 // Tiles of y, of 16 columns for up to 64 tokens, and how many workgroups share one: as many as make
-// 512, two for each CU, each of a few experts
+// 256, one for each CU, each of a few experts
 int64_t y_tiles(int64_t T, int64_t H) { return cdiv(T, 64) * cdiv(H, 16); }
 int splits_of(int64_t T, int64_t H, int64_t most) {
-    int64_t s = 512 / y_tiles(T, H);
+    int64_t s = 256 / y_tiles(T, H);
     if (s > most / 4) s = most / 4;
     return s < 2 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
 }
@@ -478,11 +490,12 @@ int launch_moe(MoeArgs args, void *stream) {
     const int64_t tiles = cdiv(args.I, 16);
     // waves that share a tile: as many as make 2048 of them, eight for each CU
     args.wk = 1;
-    while (args.wk < 8 && args.most * tiles * args.wk < 2048) args.wk *= 2;
-    args.tiles = (int)cdiv(tiles * args.wk, 8);
+    while (args.wk < kUpWaves && args.most * tiles * args.wk < 2048) args.wk *= 2;
+    args.tiles = (int)cdiv(tiles * args.wk, kUpWaves);
     void *kargs[] = {&args};
     int rc = finish(hipLaunchKernel(reinterpret_cast<const void *>(&moe_up_kernel<T, RA, Q, kS32, kAhead>),
-                                    dim3((unsigned)(args.most * args.tiles)), dim3(512), kargs, 6 * args.T, s), s);
+                                    dim3((unsigned)(args.most * args.tiles)), dim3(kUpWaves * kWave), kargs,
+                                    8 * args.T * args.top + 6 * args.T, s), s);
     if (rc != PDGEMM_OK) return rc;
     args.tiles = (int)cdiv(args.H, 16);
     constexpr int W = RA == 2 ? 16 : 8;   // (as registers and LDS allow)
@@ -499,7 +512,7 @@ template <int T, int Q, bool kS32>
 int launch_moe(const MoeArgs &args, void *stream) {
     const int pairs = args.T * args.top;
     return args.T <= 2              ? launch_moe<T, 2, Q, kS32>(args, stream)
-           : pairs <= 8 * args.most ? launch_moe<T, 8, Q, kS32>(args, stream)
+           : pairs <= 6 * args.most ? launch_moe<T, 8, Q, kS32>(args, stream)
                                     : launch_moe<T, 16, Q, kS32>(args, stream);
 }
 template <int T, bool kS32>

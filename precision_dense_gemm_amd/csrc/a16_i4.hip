@@ -69,16 +69,13 @@ __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
 #pragma unroll
     for (int j = 0; j < Wave::kX; ++j) {
         const int row = Wave::copied_row(j);
-        src.xa[j] = row < M - m0 ? (uint32_t)row * (uint32_t)args.lda + 16 * Wave::copied_chunk() : kOutside;
+        src.xa[j] = row < RA && row < M - m0 ? (uint32_t)row * (uint32_t)args.lda + 16 * Wave::copied_chunk() : kOutside;
     }
     const int size = kS32 ? 4 : 2;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int row = 16 * t + Wave::code_row(j);
-            src.vb[t][j] = row < N - n0 ? (uint32_t)row * (uint32_t)args.ldb + 16 * Wave::code_chunk() : kOutside;
-        }
+        const int row = 16 * t + Wave::code_row();
+        src.vb[t] = row < N - n0 ? (uint32_t)row * (uint32_t)args.ldb + 16 * Wave::code_chunk() : kOutside;
         src.vs[t] = (uint32_t)(n0 + min(16 * t + lane % 16, N - n0 - 1)) * size;
     }
     src.s[0] = args.s;

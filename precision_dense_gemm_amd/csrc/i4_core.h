@@ -71,19 +71,36 @@ __device__ __forceinline__ uint4 widen(uint32_t w) {
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// The same codes with a bias, by half the instructions.  bf16: code + 24, a code's four bits (their
+// The same in the order 0 4 1 5 2 6 3 7, in which a dword's halves hold them
+template <int T>
+__device__ __forceinline__ uint4 widen_spread(uint32_t w) {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = pair_of<T>(__builtin_amdgcn_cvt_off_f32_i4(w >> (4 * i)), __builtin_amdgcn_cvt_off_f32_i4(w >> (4 * i + 16)));
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+// eight 16-bit values in that order
+__device__ __forceinline__ uint4 spread(const uint4 &x) {
+    return make_uint4(__builtin_amdgcn_perm(x.z, x.x, 0x05040100u), __builtin_amdgcn_perm(x.z, x.x, 0x07060302u),
+                      __builtin_amdgcn_perm(x.w, x.y, 0x05040100u), __builtin_amdgcn_perm(x.w, x.y, 0x07060302u));
+}
+
+// The same codes with a bias, in a shift and a bit operation for two.  bf16: code + 24, a code's four bits (their
 // sign flipped) on top of the mantissa of 16.  f16: 2^-18 (code + 8), as a subnormal, which the
 // matrix instructions keep.  Operand kBiasPair, the bias with the other sign in all places, takes it
 // off again: the sums of activations it makes are the same for every column.  Activations that
 // are infinite, or whose sums with the bias overflow, leave infinities or NaN, and the unit is summed
-// again with widen() (I4Wave).  f of Biased: what a sum is short of.
+// again with widen_spread() (I4Wave).  f of Biased: what a sum is short of.
 template <int T> struct Biased;
 template <> struct Biased<kBF16> {
-    static constexpr uint32_t kMul = 0x8008u, kMask = 0x00780078u, kFlip = 0x41C041C0u, kBiasPair = 0xC1C0C1C0u;
+    static constexpr uint32_t kMask = 0x00780078u, kFlip = 0x41C041C0u, kBiasPair = 0xC1C0C1C0u;
+    static constexpr int kShift = 3;   // the first pair's, to the left; 4 less for each pair after it
     static constexpr float f = 1.0f;
 };
 template <> struct Biased<kF16> {
-    static constexpr uint32_t kMul = 0x40040u, kMask = 0x03C003C0u, kFlip = 0x02000200u, kBiasPair = 0x82008200u;
+    static constexpr uint32_t kMask = 0x03C003C0u, kFlip = 0x02000200u, kBiasPair = 0x82008200u;
+    static constexpr int kShift = 6;
     static constexpr float f = 0x1p18f;
 };
 template <int T>
@@ -91,7 +108,10 @@ __device__ __forceinline__ uint4 widen_biased(uint32_t w) {
     using B = Biased<T>;
     uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = (__umul24((w >> (8 * i)) & 0xFF, B::kMul) & B::kMask) ^ B::kFlip;   // byte i's two codes
+    for (int i = 0; i < 4; ++i) {
+        const int s = B::kShift - 4 * i;
+        x[i] = ((s >= 0 ? w << (s >= 0 ? s : 0) : w >> (s < 0 ? -s : 0)) & B::kMask) ^ B::kFlip;
+    }
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
@@ -149,7 +169,7 @@ struct I4Source {
     uint32_t xa[kX];
     const uint8_t *b[NB];      // codes
     int b_end[NB];
-    uint32_t vb[NT][2];
+    uint32_t vb[NT];
     I4Scales s[NB];
     uint32_t vs[NT];           // byte offset of the scale of this lane's row l % 16
     int K;
@@ -168,26 +188,32 @@ struct I4Groups {
 };
 
 // A wave's sums over units of 256 values of K: a whole 128-byte line of each row of codes, two
-// steps.  Everything is loaded in whole lines, 8 lanes to a line of codes and 32 to a run of 512 bytes of
-// activations, and goes through LDS of the wave's own to the lanes that want it.  (Codes loaded by the lanes
-// that convert them, 16 rows to an instruction, ask the L1 for four times as many lines.)  RA rows of activations: 2,
-// 8 or 16; a fragment's further rows repeat them.  Q: blocks that share a scale (4: groups of
-// whole steps, 2: of multiples of 64 values, 1: any).  kS32: binary32 scales.  kAhead: see run.
+// steps.  Everything is loaded in runs of a row, 4 lanes to 64 bytes of codes and 16 to 256 of activations, and goes
+// through LDS of the wave's own, a step at a time, to the lanes that want it.  (Codes loaded by the lanes
+// that convert them, 16 rows to an instruction, ask the L1 for four times as many lines: 16 rows against 8192 x
+// 8192 took 12.1 us and not 10.9.)  RA rows of activations: 2, 8 or 16; a fragment's further rows repeat
+// them.  With RA = 2 there is little but the codes, and they do go straight to their lanes (kDirect): one row
+// against 8192 x 8192 takes 8.3 us so, and 9.5 through LDS.  Q: blocks that share a scale (4: groups of whole steps, 2: of multiples of 64 values, 1: any).
+// kS32: binary32 scales.  kAhead: see run.
 template <int T, int RA, int NT, int NB, int Q, bool kS32, bool kAhead>
 struct I4Wave {
-    static constexpr int kSc = 4 / Q;            // scales per step
-    static constexpr int kX = RA / 2;            // loads of two rows of activations
-    static constexpr int kLoads = Q == 1 ? 2 : 1;   // loads of scales of four groups
+    static constexpr int kSc = 4 / Q;                 // scales per step
+    static constexpr bool kDirect = RA == 2;
+    static constexpr int kX = kDirect ? 1 : RA / 4;   // loads of four rows of a step of activations (two of a unit)
+    static constexpr int kXs = kDirect ? 1 : 2;       // ... each for every step
+    static constexpr int kRun = kDirect ? 32 : 16;    // chunks of a row of x
+    static constexpr int kLoads = Q == 1 ? 2 : 1;     // loads of scales of four groups
     using Source = I4Source<kX, NT, NB>;
-    // chunk c (16 bytes) of row r at c ^ (r % 8): rows that are read together lie in different banks
+    // chunk c (16 bytes) of row r of x at c ^ (r % 8), of b at c ^ (r / 2 % 4): rows that are read together lie in
+    // different banks; x's values in the order of widen_biased
     struct Lds {
-        uint4 x[RA][32];
-        uint4 b[NT][16][8];
+        uint4 x[RA][kRun];
+        uint4 b[kDirect ? 1 : NT][kDirect ? 1 : 16][4];
         float s[NT][16][2 * kSc];
     };
     struct Stage {
         uint4 b[NT][2];
-        uint4 x[kX];
+        uint4 x[kX][kXs];
         uint32_t s[NT][kLoads];
         int unit;
         int tag, left;   // the item's own
@@ -195,11 +221,11 @@ struct I4Wave {
     floatx4_t acc[NT];
 
     // row of activations that this lane copies in load j, and its 16 bytes of the run
-    static __device__ __forceinline__ int copied_row(int j) { return 2 * j + (threadIdx.x % kWave) / 32; }
-    static __device__ __forceinline__ int copied_chunk() { return threadIdx.x % 32; }
+    static __device__ __forceinline__ int copied_row(int j) { return kWave / kRun * j + (threadIdx.x % kWave) / kRun; }
+    static __device__ __forceinline__ int copied_chunk() { return threadIdx.x % kRun; }
     // and of a fragment of codes
-    static __device__ __forceinline__ int code_row(int j) { return 8 * j + (threadIdx.x % kWave) / 8; }
-    static __device__ __forceinline__ int code_chunk() { return threadIdx.x % 8; }
+    static __device__ __forceinline__ int code_row() { return kDirect ? threadIdx.x % 16 : threadIdx.x % kWave / 4; }
+    static __device__ __forceinline__ int code_chunk() { return kDirect ? threadIdx.x % kWave / 16 : threadIdx.x % 4; }
 
     __device__ __forceinline__ void load(Stage &st, const Source &src, int unit) {
         st.unit = unit;
@@ -208,12 +234,15 @@ struct I4Wave {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const auto rb = rsrc(src.b[t % NB], src.b_end[t % NB]);
-            st.b[t][0] = load16(rb, src.vb[t][0], unit * 128);
-            st.b[t][1] = load16(rb, src.vb[t][1], unit * 128);
+            st.b[t][0] = load16(rb, src.vb[t], unit * 128);
+            st.b[t][1] = load16(rb, src.vb[t] + 64, unit * 128);
         }
         const auto ra = rsrc(src.a, src.a_end);
 #pragma unroll
-        for (int j = 0; j < kX; ++j) st.x[j] = load16(ra, src.xa[j], unit * 512);
+        for (int j = 0; j < kX; ++j) {
+            st.x[j][0] = load16(ra, src.xa[j], unit * 512);
+            if constexpr (!kDirect) st.x[j][1] = load16(ra, src.xa[j] + 256, unit * 512);
+        }
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
             const int i = 4 * k + threadIdx.x % kWave / 16, block = unit * 8 + i * Q;
@@ -233,96 +262,100 @@ struct I4Wave {
         const int lane = threadIdx.x % kWave;
         if (__builtin_expect(st.unit * 2 * kStep + 2 * kStep > src.K, 0)) {
             // activations at and past K may be anything, a NaN too: they become zeros
-            const int n = src.K - st.unit * 2 * kStep - copied_chunk() * 8;
-            uint32_t m[4];
 #pragma unroll
-            for (int d = 0; d < 4; ++d) m[d] = n >= 2 * d + 2 ? 0xFFFFFFFFu : n == 2 * d + 1 ? 0xFFFFu : 0u;
+            for (int h = 0; h < kXs; ++h) {
+                const int n = src.K - (st.unit * 2 + h) * kStep - copied_chunk() * 8;
+                uint32_t m[4];
 #pragma unroll
-            for (int j = 0; j < kX; ++j)
-                st.x[j] = make_uint4(st.x[j].x & m[0], st.x[j].y & m[1], st.x[j].z & m[2], st.x[j].w & m[3]);
+                for (int d = 0; d < 4; ++d) m[d] = n >= 2 * d + 2 ? 0xFFFFFFFFu : n == 2 * d + 1 ? 0xFFFFu : 0u;
+#pragma unroll
+                for (int j = 0; j < kX; ++j) {
+                    uint4 &x = st.x[j][h];
+                    x = make_uint4(x.x & m[0], x.y & m[1], x.z & m[2], x.w & m[3]);
+                }
+            }
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) lds.b[t][code_row(j)][code_chunk() ^ (code_row(j) % 8)] = st.b[t][j];
-#pragma unroll
-        for (int j = 0; j < kX; ++j) lds.x[copied_row(j)][copied_chunk() ^ (copied_row(j) % 8)] = st.x[j];
 #pragma unroll
         for (int k = 0; k < kLoads; ++k)
             if (4 * k + lane / 16 < 2 * kSc)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     lds.s[t][lane % 16][4 * k + lane / 16] = scale_value<kS32>(st.s[t][k], src.s[0].half);
-        wave_lds_order();
-        floatx4_t d[NT];
-        sum_unit<true>(d, lds);
-        float odd = 0;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (!kDirect)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd = __builtin_fmaf(d[t][e], 0.0f, odd);
-        if (__builtin_expect(__any(!(odd == 0.0f)), 0)) sum_unit<false>(d, lds);   // (NaN: infinity or NaN in d)
+                for (int t = 0; t < NT; ++t) lds.b[t][code_row()][code_chunk() ^ (code_row() / 2 % 4)] = st.b[t][h];
+            if (h < kXs)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] += d[t];
-        wave_lds_order();
+                for (int j = 0; j < kX; ++j)
+                    lds.x[copied_row(j)][copied_chunk() ^ (copied_row(j) % 8)] = spread(st.x[j][h < kXs ? h : 0]);
+            if (h < kXs) wave_lds_order();
+            floatx4_t d[NT];
+            sum_step<true>(d, st, lds, h);
+            float odd = 0;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) odd = __builtin_fmaf(d[t][e], 0.0f, odd);
+            if (__builtin_expect(__any(!(odd == 0.0f)), 0)) sum_step<false>(d, st, lds, h);   // (NaN: infinity or NaN in d)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] += d[t];
+            if (!kDirect || h == 1) wave_lds_order();
+        }
     }
 
     // the dwords of matrix instructions 0 .. 3 of step h of fragment t
-    static __device__ __forceinline__ void codes(uint32_t (&w)[4], const Lds &lds, int t, int h) {
-        const int lane = threadIdx.x % kWave, g = lane / 16, r = lane % 16;
-        if constexpr (Q == 4) {
-            const uint4 v = lds.b[t][r][(4 * h + g) ^ (r % 8)];
+    static __device__ __forceinline__ void codes(uint32_t (&w)[4], const Stage &st, const Lds &lds, int t, int h) {
+        const int lane = threadIdx.x % kWave, g = lane / 16, r = lane % 16, swap = r / 2 % 4;
+        if constexpr (kDirect) {
+            w[0] = st.b[t][h].x, w[1] = st.b[t][h].y, w[2] = st.b[t][h].z, w[3] = st.b[t][h].w;
+            share_out<Q>(w);
+        } else if constexpr (Q == 4) {
+            const uint4 v = lds.b[t][r][g ^ swap];
             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
         } else if constexpr (Q == 2) {
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-                const uint2 x = reinterpret_cast<const uint2 *>(&lds.b[t][r][(4 * h + 2 * v + (g & 1)) ^ (r % 8)])[g >> 1];
+                const uint2 x = reinterpret_cast<const uint2 *>(&lds.b[t][r][(2 * v + (g & 1)) ^ swap])[g >> 1];
                 w[2 * v] = x.x, w[2 * v + 1] = x.y;
             }
         } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) w[u] = reinterpret_cast<const uint32_t *>(&lds.b[t][r][(4 * h + u) ^ (r % 8)])[g];
+            for (int u = 0; u < 4; ++u) w[u] = reinterpret_cast<const uint32_t *>(&lds.b[t][r][u ^ swap])[g];
         }
     }
 
-    // a unit's sums
+    // step h's sums
     template <bool kBiased>
-    static __device__ __forceinline__ void sum_unit(floatx4_t (&d)[NT], const Lds &lds) {
+    static __device__ __forceinline__ void sum_step(floatx4_t (&d)[NT], const Stage &st, const Lds &lds, int h) {
         const int lane = threadIdx.x % kWave, g = lane / 16, row = lane % RA % 16;
         constexpr uint32_t kB = Biased<T>::kBiasPair;
-        float s[NT][2 * kSc];
+        uint4 a[4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            d[t] = floatx4_t{0, 0, 0, 0};
+        for (int u = 0; u < 4; ++u) a[u] = lds.x[row][((kDirect ? 16 * h : 0) + position<Q>(u, g)) ^ (row % 8)];
+        floatx4_t bias[kSc];
 #pragma unroll
-            for (int v = 0; v < 2 * kSc; ++v) s[t][v] = lds.s[t][lane % 16][v] * (kBiased ? Biased<T>::f : 16.0f);
+        for (int v = 0; v < kSc; ++v) {
+            bias[v] = floatx4_t{0, 0, 0, 0};
+            if constexpr (kBiased)
+#pragma unroll
+                for (int u = 0; u < Q; ++u) bias[v] = mfma16<T>(a[v * Q + u], make_uint4(kB, kB, kB, kB), bias[v]);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4 a[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) a[u] = lds.x[row][(16 * h + position<Q>(u, g)) ^ (row % 8)];
-            floatx4_t bias[kSc];
+        for (int t = 0; t < NT; ++t) {
+            uint32_t w[4];
+            codes(w, st, lds, t, h);
+            d[t] = floatx4_t{0, 0, 0, 0};
 #pragma unroll
             for (int v = 0; v < kSc; ++v) {
-                bias[v] = floatx4_t{0, 0, 0, 0};
-                if constexpr (kBiased)
+                floatx4_t p = bias[v];
 #pragma unroll
-                    for (int u = 0; u < Q; ++u) bias[v] = mfma16<T>(a[v * Q + u], make_uint4(kB, kB, kB, kB), bias[v]);
-            }
+                for (int u = 0; u < Q; ++u)
+                    p = mfma16<T>(a[v * Q + u], kBiased ? widen_biased<T>(w[v * Q + u]) : widen_spread<T>(w[v * Q + u]), p);
+                const float s = lds.s[t][lane % 16][h * kSc + v] * (kBiased ? Biased<T>::f : 16.0f);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                uint32_t w[4];
-                codes(w, lds, t, h);
-#pragma unroll
-                for (int v = 0; v < kSc; ++v) {
-                    floatx4_t p = bias[v];
-#pragma unroll
-                    for (int u = 0; u < Q; ++u)
-                        p = mfma16<T>(a[v * Q + u], kBiased ? widen_biased<T>(w[v * Q + u]) : widen<T>(w[v * Q + u]), p);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[t][e] = __builtin_fmaf(p[e], s[t][h * kSc + v], d[t][e]);
-                }
+                for (int e = 0; e < 4; ++e) d[t][e] = __builtin_fmaf(p[e], s, d[t][e]);
             }
         }
     }

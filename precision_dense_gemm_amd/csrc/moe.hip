@@ -272,11 +272,8 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up_kernel(MoeArgs args) {
         src.b[b] = args.w13 + e * args.e13 + row * args.ld13;
         src.b_end[b] = (int)((cols - 1) * args.ld13) + (((H + 1) / 2 + 15) & ~15);
         src.s[b] = {args.s13 + e * args.es13 + row * size, args.lds13, args.s_half};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int at = Wave::code_row(j);
-            src.vb[b][j] = at < cols ? (uint32_t)at * (uint32_t)args.ld13 + 16 * Wave::code_chunk() : kOutside;
-        }
+        const int at = Wave::code_row();
+        src.vb[b] = at < cols ? (uint32_t)at * (uint32_t)args.ld13 + 16 * Wave::code_chunk() : kOutside;
         src.vs[b] = (uint32_t)min(r, cols - 1) * size;
     }
     src.K = H, src.group_magic = args.group_magic, src.groups = (H + args.group - 1) / args.group;
@@ -285,7 +282,7 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up_kernel(MoeArgs args) {
 #pragma unroll
         for (int j = 0; j < Wave::kX; ++j) {
             const int at = first + Wave::copied_row(j);
-            src.xa[j] = at < rows ? (uint32_t)(own[at] / top) * (uint32_t)args.ldx + 16 * Wave::copied_chunk() : kOutside;
+            src.xa[j] = Wave::copied_row(j) < RA && at < rows ? (uint32_t)(own[at] / top) * (uint32_t)args.ldx + 16 * Wave::copied_chunk() : kOutside;
         }
         int next = k0;
         Wave w;
@@ -363,11 +360,7 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
     src.a = args.act;
     src.a_end = (int)((args.T * args.top - 1) * args.ldact) + ((2 * I + 15) & ~15);
     src.b_end[0] = (int)((cols - 1) * args.ld2) + (((I + 1) / 2 + 15) & ~15);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int row = Wave::code_row(j);
-        src.vb[0][j] = row < cols ? (uint32_t)row * (uint32_t)args.ld2 + 16 * Wave::code_chunk() : kOutside;
-    }
+    src.vb[0] = Wave::code_row() < cols ? (uint32_t)Wave::code_row() * (uint32_t)args.ld2 + 16 * Wave::code_chunk() : kOutside;
     src.vs[0] = (uint32_t)min(r, cols - 1) * size;
     src.K = I, src.group_magic = args.group_magic, src.groups = (I + args.group - 1) / args.group;
     // (expert, line) number i is wave i's of the splits' waves, round and round; an expert of more than RA

@@ -505,8 +505,10 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
  * with their element's alignment, a row of at most 4 MiB.
  *   C[i][j] = sum over q of scale_b[q][j] * sum over k in q of A[i][k] * code[j][k]
  * The codes enter exactly, the sums are binary32 in a fixed order, and C is
- * rounded once to out_type: |C - exact| <= (ceil(K / 32) + 2) * 2^-22 * sum |a b|
- * plus that rounding where no sum leaves binary32's normal range.  As elsewhere
+ * rounded once to out_type: |C - exact| <= (512 + K / 12) * 2^-22 * sum over k of
+ * |A[i][k]| |scale| plus that rounding where no sum leaves binary32's normal range (up
+ * to 16 rows a code enters as code + 24, or + 8 for f16 A, and the bias comes off in the same
+ * sum; infinities and NaN of A reach C as the products make them).  As elsewhere
  * the 16-byte granule that holds a row's last element may be read whole, and
  * values outside the operands never reach a stored result.  K = 0 stores zeros.
  * Where there are too few tiles for the GPU, K is split over workgroups, whose sums
@@ -514,9 +516,10 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
  * may be NULL), 16-byte aligned, undefined on return; calls that overlap, and graphs that
  * may run at once, need one each.
  * _cfg takes an explicit tile configuration (0 <= cfg <
- * pdgemm_a16_i4_num_configs(), any shape) and the workspace of
+ * pdgemm_a16_i4_num_configs(), any shape; the last one groups of a multiple of 128 only)
+ * and the workspace of
  * _cfg_workspace_size; _pick is the one gemm_a16_i4 takes. */
-int64_t pdgemm_a16_i4_workspace_size(int64_t M, int64_t N, int64_t K);
+int64_t pdgemm_a16_i4_workspace_size(int64_t M, int64_t N, int64_t K, int64_t group);
 int gemm_a16_i4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                 int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc,
                 int out_type, void *workspace, int64_t workspace_bytes, void *stream);
@@ -526,7 +529,7 @@ int pdgemm_a16_i4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A, i
                       int64_t group, void *C, int64_t ldc, int out_type, void *workspace, int64_t workspace_bytes,
                       void *stream);
 int pdgemm_a16_i4_num_configs(void);
-int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K);
+int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K, int64_t group);
 
 /* A mixture-of-experts layer for a few tokens: what follows the router's product.
  *

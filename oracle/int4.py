@@ -42,26 +42,30 @@ def route(logits: np.ndarray, top: int):
     return ids, weights
 
 
-def experts(x, ids, weights, w13, w2):
+def experts(x, ids, weights, w13, w2, m13=None, m2=None):
     """y (T, H) for lists of dense expert weights w13[e] (2I, H), w2[e] (H, I), and what its errors are relative to: the
-    sum of its terms' magnitudes, of what changes of the first product's terms do to it, and of |w2| (one unit of the
-    gated activation).  An id outside the list adds nothing."""
-    y, size, act_size, mass = (np.zeros_like(x) for _ in range(4))
+    sum of its terms' magnitudes; what changes of the first product's sums of |m13| |x| do to it; the sums of |m2| times
+    the gated activations; and of |w2| (one unit of such an activation).  m13, m2: magnitudes in the place of the
+    weights' (their scales', say).  An id outside the list adds nothing."""
+    m13 = w13 if m13 is None else m13
+    m2 = w2 if m2 is None else m2
+    y, size, act_size, second, mass = (np.zeros_like(x) for _ in range(5))
     for t in range(x.shape[0]):
         for slot, e in enumerate(ids[t]):
             if not 0 <= e < len(w13):
                 continue
             I = w2[e].shape[1]
             both = w13[e] @ x[t]
-            mag = np.abs(w13[e]) @ np.abs(x[t])
+            mag = np.abs(m13[e]) @ np.abs(x[t])
             g, u = both[:I], both[I:]
             s = 1.0 / (1.0 + np.exp(-g))
             act = g * s * u
             # a change of g or u changes act by so much: |d silu| <= 1.1
             change = 1.1 * mag[:I] * np.abs(u) + np.abs(g * s) * mag[I:]
-            wt = weights[t, slot]
-            y[t] += wt * (w2[e] @ act)
-            size[t] += np.abs(wt) * (np.abs(w2[e]) @ np.abs(act))
-            act_size[t] += np.abs(wt) * (np.abs(w2[e]) @ change)
+            wt = np.abs(weights[t, slot])
+            y[t] += weights[t, slot] * (w2[e] @ act)
+            size[t] += wt * (np.abs(w2[e]) @ np.abs(act))
+            act_size[t] += wt * (np.abs(w2[e]) @ change)
+            second[t] += wt * (np.abs(m2[e]) @ np.abs(act))
             mass[t] += np.abs(w2[e]).sum(axis=1)
-    return y, size, act_size, mass
+    return y, size, act_size, second, mass

@@ -151,13 +151,13 @@ lib.gemm_a16_i4.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _p, _i64, _p, _i64, 
 lib.gemm_a16_i4.restype = _i
 lib.pdgemm_a16_i4_cfg.argtypes = [_i] + lib.gemm_a16_i4.argtypes
 lib.pdgemm_a16_i4_cfg.restype = _i
-lib.pdgemm_a16_i4_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.pdgemm_a16_i4_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
 lib.pdgemm_a16_i4_workspace_size.restype = _i64
 lib.pdgemm_a16_i4_cfg_workspace_size.argtypes = [_i, _i64, _i64, _i64]
 lib.pdgemm_a16_i4_cfg_workspace_size.restype = _i64
 lib.pdgemm_a16_i4_num_configs.argtypes = []
 lib.pdgemm_a16_i4_num_configs.restype = _i
-lib.pdgemm_a16_i4_pick.argtypes = [_i64, _i64, _i64]
+lib.pdgemm_a16_i4_pick.argtypes = [_i64, _i64, _i64, _i64]
 lib.pdgemm_a16_i4_pick.restype = _i
 lib.pdgemm_moe_route.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _i, _p, _p, _p]
 lib.pdgemm_moe_route.restype = _i
@@ -1013,7 +1013,7 @@ def gemm_a16_i4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, group:
     if workspace is not None:
         args += _workspace(workspace, out.device)
     else:
-        need = a16_i4_workspace_size(M, N, K, cfg) if M > 16 or cfg is not None else 0
+        need = a16_i4_workspace_size(M, N, K, group, cfg) if M > 16 or cfg is not None else 0
         if need:
             workspace = _mx_empty(1, need, torch.uint8, A.device, stream)
             args += (workspace.data_ptr(), need)
@@ -1024,10 +1024,10 @@ def gemm_a16_i4(A: torch.Tensor, Bt: torch.Tensor, scale_b: torch.Tensor, group:
     return out
 
 
-def a16_i4_workspace_size(M: int, N: int, K: int, cfg: int | None = None) -> int:
+def a16_i4_workspace_size(M: int, N: int, K: int, group: int, cfg: int | None = None) -> int:
     """Bytes of workspace gemm_a16_i4 needs for a shape (0: none)."""
     if cfg is None:
-        return lib.pdgemm_a16_i4_workspace_size(M, N, K)
+        return lib.pdgemm_a16_i4_workspace_size(M, N, K, group)
     return lib.pdgemm_a16_i4_cfg_workspace_size(cfg, M, N, K)
 
 
@@ -1035,9 +1035,9 @@ def a16_i4_num_configs() -> int:
     return lib.pdgemm_a16_i4_num_configs()
 
 
-def a16_i4_pick(M: int, N: int, K: int) -> int:
+def a16_i4_pick(M: int, N: int, K: int, group: int) -> int:
     """The tile configuration gemm_a16_i4 takes for a shape."""
-    return lib.pdgemm_a16_i4_pick(M, N, K)
+    return lib.pdgemm_a16_i4_pick(M, N, K, group)
 
 
 def _moe_pairs(t, rows: int, dtype, name: str) -> int:

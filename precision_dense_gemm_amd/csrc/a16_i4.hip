@@ -116,19 +116,29 @@ __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
 }
 
 // More rows: a tile of 16 MT rows to a workgroup, whose W waves have 16 NT columns each, so that a
-// code is converted once per tile.  Activations go through LDS, a step of 128 values of K at a
-// time and two deep, for all waves; codes come straight into the lanes that convert them, a
-// line of 256 values ahead.  Fragment t holds columns NT n + t (n = l % 16) of the wave's: a lane's
-// results are neighbours in C.  With `splits`, K is split over that many workgroups, which
-// write binary32 sums for split_join_kernel.
-template <int T, int MT, int NT, int W, int Q, bool kS32>
-__global__ __launch_bounds__(W *kWave, 2) void a16_i4_tile_kernel(A16I4Args args) {
+// code is converted once per tile.  Activations go through LDS, a step of 128 values of K at a time
+// and two deep, for all waves; codes are loaded whole lines to four lanes, a unit of 256 values ahead,
+// and pass through LDS to the lanes that convert them.  Fragment t holds columns NT n + t (n = l % 16) of
+// the wave's: a lane's results are neighbours in C.  G such groups of W waves share out the units of K,
+// and their sums meet in LDS.  With `splits`, K is split over that many workgroups too, which write
+// binary32 sums for split_join_kernel; what they write and the second launch cost 37 x 4096 x 8192
+// 7 of 19 us with 16 splits and G = 1, so G is 4 and 2 for the tiles of few rows (14.4 us).
+// Up to some hundred rows the stream of codes bounds it, past that the vector unit: a code takes an
+// instruction and a half, and each sum of a scale's values a multiply-add beside the matrix
+// instructions.  2048 x 8192 x 8192 in groups of 128: 270 us, 1018 TFLOP/s; of 64: 381 us.
+template <int T, int MT, int NT, int W, int G, int Q, bool kS32>
+__global__ __launch_bounds__(G *W *kWave) void a16_i4_tile_kernel(A16I4Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int BM = 16 * MT, BN = 16 * NT * W, kThreads = W * kWave;
+    constexpr int BM = 16 * MT, BN = 16 * NT * W, kThreads = W * kWave;   // (threads of a group)
     constexpr int kX = BM * 16 / kThreads, kSc = 4 / Q;
     static_assert(BM * 16 % kThreads == 0, "a step of activations in whole runs");
-    __shared__ uint4 xs[2][BM][16];
-    const int tid = threadIdx.x, lane = tid % kWave;
+    __shared__ union {
+        uint4 xs[G][2][BM][16];
+        float part[G][G == 1 ? 1 : BM * BN];
+    } lds;
+    __shared__ uint4 codes[G * W][2][NT][16][4];   // a unit's, each wave its own
+    const int tid = threadIdx.x % kThreads, lane = tid % kWave;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane % 16, g = lane / 16;
     const int M = args.M, N = args.N, K = args.K;
@@ -151,7 +161,8 @@ __global__ __launch_bounds__(W *kWave, 2) void a16_i4_tile_kernel(A16I4Args args
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int col = NT * r + t;
-        vb[t] = col < cols ? (uint32_t)col * (uint32_t)args.ldb + 16 * g : kOutside;
+        const int copied = NT * (lane / 4) + t;
+        vb[t] = copied < cols ? (uint32_t)copied * (uint32_t)args.ldb + 16 * (lane % 4) : kOutside;
         vs[t] = (uint32_t)(cols > 0 ? n0 + min(col, cols - 1) : 0) * (kS32 ? 4 : 2);
     }
     const int groups = (K + args.group - 1) / args.group;
@@ -176,7 +187,7 @@ __global__ __launch_bounds__(W *kWave, 2) void a16_i4_tile_kernel(A16I4Args args
 #pragma unroll
         for (int j = 0; j < kX; ++j) {
             const int row = (tid + j * kThreads) / 16;
-            xs[step & 1][row][(tid % 16) ^ (row % 8)] = xr[j];
+            lds.xs[group][step & 1][row][(tid % 16) ^ (row % 8)] = xr[j];
         }
     };
     struct Codes {
@@ -211,50 +222,104 @@ __global__ __launch_bounds__(W *kWave, 2) void a16_i4_tile_kernel(A16I4Args args
         for (int t = 0; t < NT; ++t) acc[i][t] = floatx4_t{0, 0, 0, 0};
 
     if (first < last) {
-        Codes now, next;
-        load_codes(now, first);
-        load_x(2 * first);
-        store_x(2 * first);
-        load_x(2 * first + 1);
-        for (int unit = first; unit < last; ++unit) {
-            load_codes(next, unit + 1);
+        Codes next;
+        // (a group past its last unit sums zeros until all are there)
+        const int mine = first + group, turns = (last - first + G - 1) / G;
+        load_codes(next, mine);
+        load_x(2 * mine);
+        store_x(2 * mine);
+        load_x(2 * mine + 1);
+        for (int i = 0; i < turns; ++i) {
+            const int unit = mine + i * G;
+            float scale[NT][2 * kSc];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) write_codes(codes[group * W + wave][h][t], next.b[t][h]);
+#pragma unroll
+                for (int v = 0; v < 2 * kSc; ++v) {
+                    const float f = scale_value<kS32>(next.s[t][v], args.s.half);
+                    scale[t][v] = unit * 2 * kStep + v * Q * kBlock < K && unit < last ? f * 16.0f : 0.0f;   // (no scale past K)
+                }
+            }
+            load_codes(next, unit + G);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int step = 2 * unit + h;
                 __syncthreads();
-                store_x(step + 1);
-                load_x(step + 2);
-                uint4 x[MT][4];
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) x[i][u] = xs[h][16 * i + r][position<Q>(u, g) ^ (r % 8)];
+                store_x(h ? 2 * (unit + G) : step + 1);
+                load_x(2 * (unit + G) + h);
+                // the step's codes converted once, then four fragments of rows at a time, as the registers hold
+                uint4 c[NT][4];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    uint32_t w[4] = {now.b[t][h].x, now.b[t][h].y, now.b[t][h].z, now.b[t][h].w};
-                    share_out<Q>(w);
+                    uint32_t w[4];
+                    read_codes<Q>(w, codes[group * W + wave][h][t]);
 #pragma unroll
-                    for (int v = 0; v < kSc; ++v) {
-                        uint4 c[Q];
+                    for (int u = 0; u < 4; ++u) c[t][u] = widen<T>(w[u]);
+                }
+                constexpr int kRows = MT < 4 ? MT : 4;
 #pragma unroll
-                        for (int u = 0; u < Q; ++u) c[u] = widen<T>(w[v * Q + u]);
-                        float s = scale_value<kS32>(now.s[t][h * kSc + v], args.s.half);
-                        s = step * kStep + v * Q * kBlock < K ? s * 16.0f : 0.0f;   // (no scale past K)
+                for (int i0 = 0; i0 < MT; i0 += kRows) {
+                    uint4 x[kRows][4];
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            floatx4_t p = {0, 0, 0, 0};
+                    for (int i = 0; i < kRows; ++i)
 #pragma unroll
-                            for (int u = 0; u < Q; ++u) p = mfma16<T>(x[i][v * Q + u], c[u], p);
+                        for (int u = 0; u < 4; ++u)
+                            x[i][u] = lds.xs[group][h][16 * (i0 + i) + r][position<Q>(u, g) ^ (r % 8)];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[i][t][e] = __builtin_fmaf(p[e], s, acc[i][t][e]);
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int v = 0; v < kSc; ++v) {
+                            floatx4_t p[kRows];
+#pragma unroll
+                            for (int u = v * Q; u < v * Q + Q; ++u)
+#pragma unroll
+                                for (int i = 0; i < kRows; ++i)
+                                    p[i] = mfma16<T>(x[i][u], c[t][u], u == v * Q ? floatx4_t{0, 0, 0, 0} : p[i]);
+#pragma unroll
+                            for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    acc[i0 + i][t][e] = __builtin_fmaf(p[i][e], scale[t][h * kSc + v], acc[i0 + i][t][e]);
                         }
-                    }
                 }
             }
-            now = next;
         }
     }
     float *const part = args.splits > 1 ? args.part + (int64_t)split * M * N : nullptr;
+    if constexpr (G > 1) {
+        constexpr int kTile = MT * NT * 256;   // of a wave
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) lds.part[group][wave * kTile + ((i * NT + t) * 4 + e) * kWave + lane] = acc[i][t][e];
+        __syncthreads();
+        // group k adds up every G-th fragment's row
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = m0 + 16 * i + 4 * g + e, n = cols - NT * r;
+                if ((i * 4 + e) % G != group || row >= M || n <= 0) continue;
+                float v[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int at = wave * kTile + ((i * NT + t) * 4 + e) * kWave + lane;
+                    v[t] = lds.part[0][at];
+#pragma unroll
+                    for (int k = 1; k < G; ++k) v[t] += lds.part[k][at];
+                }
+                if (part)
+                    store_some<NT>(part + (int64_t)row * N + n0 + NT * r, v, n);
+                else
+                    store_as<NT>(args.C, args.out_type, (int64_t)row * args.ldc + n0 + NT * r, v, n);
+            }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -274,28 +339,22 @@ __global__ __launch_bounds__(W *kWave, 2) void a16_i4_tile_kernel(A16I4Args args
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+
 constexpr int kMaxSplits = 16;
 
-// C from the splits' sums, added in their order; four neighbours of a row to a thread.
+// C from the splits' sums, added in their order.
 __global__ __launch_bounds__(256) void split_join_kernel(A16I4Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    const int per_row = (args.N + 3) / 4;
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = x / per_row;
-    const int col = (int)(x % per_row) * 4;
-    if (row >= args.M) return;
-    const float *const p = args.part + row * args.N + col;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)args.M * args.N;
+    if (x >= all) return;
     // (all loads before the first sum)
-    float v[kMaxSplits][4], sum[4] = {0, 0, 0, 0};
+    float v[kMaxSplits], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) v[k] = k < args.splits ? args.part[k * all + x] : 0.0f;
 #pragma unroll
     for (int k = 0; k < kMaxSplits; ++k)
-        if (k < args.splits) load_some<4>(v[k], p + (int64_t)k * args.M * args.N, args.N - col);
-#pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k)
-        if (k < args.splits)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] += v[k][i];
-    store_as<4>(args.C, args.out_type, row * args.ldc + col, sum, args.N - col);
+        if (k < args.splits) sum += v[k];
+    store_as(args.C, args.out_type, x / args.N * args.ldc + x % args.N, sum);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -305,19 +364,25 @@ __global__ __launch_bounds__(256) void split_join_kernel(A16I4Args args) {
 // few: rows of a tile 2, 8 or 16; else 16 MT
 struct Config {
     bool few;
-    int rows, nt, waves;
+    int rows, nt, waves, groups;
 };
-constexpr Config kConfigs[] = {{true, 2, 1, 8},  {true, 2, 2, 8},   {true, 8, 1, 8},   {true, 8, 2, 8},  {true, 16, 1, 8},
-                               {true, 16, 2, 8}, {false, 32, 2, 4}, {false, 48, 2, 4}, {false, 64, 2, 4}};
+constexpr Config kConfigs[] = {{true, 2, 1, 8, 1},   {true, 2, 2, 8, 1},   {true, 8, 1, 8, 1},   {true, 8, 2, 8, 1},
+                               {true, 16, 1, 8, 1},  {true, 16, 2, 8, 1},  {false, 32, 1, 4, 4}, {false, 48, 1, 4, 4},
+                               {false, 64, 2, 4, 2}, {false, 64, 2, 8, 1}, {false, 128, 2, 8, 1}};
 constexpr int kNumConfigs = sizeof(kConfigs) / sizeof(kConfigs[0]);
+// The last one is for groups of whole steps: with more scales its values leave the registers (2048 x 8192 x 8192 of
+// f16 in groups of 64 takes 806 us on it, 381 on the one before).
+bool serves(int c, int64_t group) { return c < kNumConfigs - 1 || group % kStep == 0; }
 
 template <int T, int C, int Q, bool kS32>
 const void *a16_i4_ptr() {
     constexpr Config c = kConfigs[C];
     if constexpr (c.few)
         return reinterpret_cast<const void *>(&a16_i4_few_kernel<T, c.rows, c.nt, c.waves, Q, kS32, c.rows != 16>);
+    else if constexpr (C == kNumConfigs - 1 && Q != 4)
+        return nullptr;
     else
-        return reinterpret_cast<const void *>(&a16_i4_tile_kernel<T, c.rows / 16, c.nt, c.waves, Q, kS32>);
+        return reinterpret_cast<const void *>(&a16_i4_tile_kernel<T, c.rows / 16, c.nt, c.waves, c.groups, Q, kS32>);
 }
 template <int T, int Q, int C = 0>
 const void *a16_i4_ptr(int cfg, bool s32) {
@@ -335,23 +400,37 @@ const void *a16_i4_ptr(int cfg, int group, bool s32) {
 int64_t tiles_m(int c, int64_t M) { return cdiv(M, kConfigs[c].rows); }
 int64_t tiles_n(int c, int64_t N) { return cdiv(N, 16 * kConfigs[c].nt * (kConfigs[c].few ? 1 : kConfigs[c].waves)); }
 
-// The widest tile of the rows that still makes a workgroup for each CU.
-int pick_a16_i4(int64_t M, int64_t N, int64_t K) {
-    (void)K;
+// Ranges of K of a tile configuration: as many as make a workgroup for each CU, of a unit or more for each
+// of its groups.
+int splits_of(int cfg, int64_t M, int64_t N, int64_t K) {
+    if (kConfigs[cfg].few) return 1;
+    int64_t s = 256 / (tiles_m(cfg, M) * tiles_n(cfg, N)), most = cdiv(K, 2 * kStep) / kConfigs[cfg].groups;
+    if (s > most) s = most;
+    return s < 2 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
+}
+// To 16 rows, the tile of the least rows that holds them, and the wider one where that makes a workgroup
+// for each CU (one row, us, of width 32 and 16: 8192 x 8192 8.4 and 9.1, 4096 x 4096 5.4 and 4.3).  Past
+// that, the least of a model of time: rounds of the CUs, each K / S values at a configuration's rate (us for
+// 1000 values of K), and where K is split the second launch and what the splits write and read.  Its
+// constants are fitted to all configurations' times at 88 shapes, 20 to 2048 rows against 1024 x 4096 to 14336 x
+// 8192 in groups of 64 and 128: it takes the fastest in 84 of them, and one within 3% of it in the others.
+int pick_a16_i4(int64_t M, int64_t N, int64_t K, int64_t group) {
     if (M <= 2) return tiles_n(1, N) >= 256 ? 1 : 0;
     if (M <= 8) return tiles_n(3, N) >= 256 ? 3 : 2;
     if (M <= 16) return tiles_n(5, N) >= 256 ? 5 : 4;
-    return M <= 32 ? 6 : M <= 48 ? 7 : 8;
+    constexpr double kRate[] = {1.1, 2.48, 3.35, 5.93, 9.08, 14.3};
+    int best = 5;
+    double least = 0;
+    for (int c = 5; c < kNumConfigs; ++c) {
+        if (!serves(c, group)) continue;
+        const int64_t s = splits_of(c, M, N, K);
+        double us = (double)cdiv(tiles_m(c, M) * tiles_n(c, N) * s, 256) * (double)K / (double)s * kRate[c - 5] * 1e-3;
+        if (s > 1) us += 2.76 + (double)(s * M * N) * 2.7e-6;
+        if (c == 5 || us < least) best = c, least = us;
+    }
+    return best;
 }
 
-// Ranges of K of a tile configuration: as many as make two workgroups for each CU, of a unit or more.
-int splits_of(int cfg, int64_t M, int64_t N, int64_t K) {
-    if (kConfigs[cfg].few) return 1;
-    const int64_t tiles = tiles_m(cfg, M) * tiles_n(cfg, N), units = cdiv(K, 2 * kStep);
-    int64_t s = 512 / tiles;
-    if (s > units / 2) s = units / 2;
-    return s < 2 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
-}
 int64_t split_bytes(int cfg, int64_t M, int64_t N, int64_t K) {
     const int s = splits_of(cfg, M, N, K);
     return s > 1 ? 4 * s * M * N : 0;
@@ -365,7 +444,7 @@ int launch_a16_i4(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64
                   int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc,
                   int out_type, void *workspace, int64_t workspace_bytes, void *stream) {
     if (cfg >= kNumConfigs || (a_type != kF16 && a_type != kBF16) || !known_type(scale_type) || !known_type(out_type) ||
-        group <= 0 || group % kBlock || group > (int64_t(1) << 30))
+        group <= 0 || group % kBlock || group > (int64_t(1) << 30) || (cfg >= 0 && !serves(cfg, group)))
         return PDGEMM_EINVAL_CFG;
     if (!sizes_ok(M, N, K)) return PDGEMM_EINVAL_DIM;
     if (lda < K || ldb < K || ldsb < N || ldc < N) return PDGEMM_EINVAL_LD;
@@ -377,7 +456,7 @@ int launch_a16_i4(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64
     if (rc == PDGEMM_OK && K > 0 && ldb > 2 * kMaxRowBytes) rc = PDGEMM_EINVAL_LD;
     if (rc == PDGEMM_OK && K > 0 && (lda % 8 || ldb % 32 || ((uintptr_t)A & 15) || ((uintptr_t)B & 15))) rc = PDGEMM_EALIGN;
     if (rc != PDGEMM_OK) return rc;
-    if (cfg < 0) cfg = pick_a16_i4(M, N, K);
+    if (cfg < 0) cfg = pick_a16_i4(M, N, K, group);
     const int splits = splits_of(cfg, M, N, K);
     if (splits > 1) {
         if (!workspace) return PDGEMM_ENULL;
@@ -405,17 +484,17 @@ int launch_a16_i4(int cfg, int64_t M, int64_t N, int64_t K, const void *A, int64
                       I4Groups::magic(group)};
     const bool s32 = scale_type == kF32;
     const void *fn = a_type == kF16 ? a16_i4_ptr<kF16>(cfg, (int)group, s32) : a16_i4_ptr<kBF16>(cfg, (int)group, s32);
-    rc = run(fn, (int64_t)args.tiles_m * args.tiles_n * splits, c.waves * kWave, &args, stream);
+    rc = run(fn, (int64_t)args.tiles_m * args.tiles_n * splits, c.waves * c.groups * kWave, &args, stream);
     if (rc != PDGEMM_OK || splits == 1) return rc;
-    return run(reinterpret_cast<const void *>(&split_join_kernel), cdiv(M * cdiv(N, 4), 256), 256, &args, stream);
+    return run(reinterpret_cast<const void *>(&split_join_kernel), cdiv(M * N, 256), 256, &args, stream);
 }
 
 }  // namespace
 
 extern "C" {
 
-int64_t pdgemm_a16_i4_workspace_size(int64_t M, int64_t N, int64_t K) {
-    return sizes_ok(M, N, K) && M > 0 && N > 0 ? split_bytes(pick_a16_i4(M, N, K), M, N, K) : 0;
+int64_t pdgemm_a16_i4_workspace_size(int64_t M, int64_t N, int64_t K, int64_t group) {
+    return sizes_ok(M, N, K) && M > 0 && N > 0 ? split_bytes(pick_a16_i4(M, N, K, group), M, N, K) : 0;
 }
 
 int gemm_a16_i4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B, int64_t ldb,
@@ -439,6 +518,6 @@ int pdgemm_a16_i4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A, i
 
 int pdgemm_a16_i4_num_configs(void) { return kNumConfigs; }
 
-int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K) { return pick_a16_i4(M, N, K); }
+int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K, int64_t group) { return pick_a16_i4(M, N, K, group); }
 
 }  // extern "C"

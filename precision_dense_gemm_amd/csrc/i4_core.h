@@ -135,6 +135,30 @@ __device__ __forceinline__ int position(int u, int g) {
     return 4 * u + g;
 }
 
+// The same of a step's codes of a fragment in LDS: chunk c (16 bytes) of row r at c ^ (r / 2 % 4), so that rows that
+// are read together lie in different banks.  A lane that copies has 16 bytes, chunk l % 4 of row l / 4.
+__device__ __forceinline__ void write_codes(uint4 (*b)[4], const uint4 &v) {
+    const int lane = threadIdx.x % kWave, r = lane / 4;
+    b[r][(lane % 4) ^ (r / 2 % 4)] = v;
+}
+template <int Q>
+__device__ __forceinline__ void read_codes(uint32_t (&w)[4], const uint4 (*b)[4]) {
+    const int lane = threadIdx.x % kWave, g = lane / 16, r = lane % 16, swap = r / 2 % 4;
+    if constexpr (Q == 4) {
+        const uint4 v = b[r][g ^ swap];
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (Q == 2) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const uint2 x = reinterpret_cast<const uint2 *>(&b[r][(2 * v + (g & 1)) ^ swap])[g >> 1];
+            w[2 * v] = x.x, w[2 * v + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = reinterpret_cast<const uint32_t *>(&b[r][u ^ swap])[g];
+    }
+}
+
 // Orders a wave's LDS accesses before and after it, across its lanes.  The LDS serves one wave's
 // accesses in the order they are issued, so this costs no instruction: it keeps the compiler,
 // which sees one lane alone, from moving a read above the other lanes' store.
@@ -204,8 +228,8 @@ struct I4Wave {
     static constexpr int kRun = kDirect ? 32 : 16;    // chunks of a row of x
     static constexpr int kLoads = Q == 1 ? 2 : 1;     // loads of scales of four groups
     using Source = I4Source<kX, NT, NB>;
-    // chunk c (16 bytes) of row r of x at c ^ (r % 8), of b at c ^ (r / 2 % 4): rows that are read together lie in
-    // different banks; x's values in the order of widen_biased
+    // chunk c (16 bytes) of row r of x at c ^ (r % 8): rows that are read together lie in different banks; the values
+    // in the order of widen_biased
     struct Lds {
         uint4 x[RA][kRun];
         uint4 b[kDirect ? 1 : NT][kDirect ? 1 : 16][4];
@@ -285,7 +309,7 @@ struct I4Wave {
         for (int h = 0; h < 2; ++h) {
             if constexpr (!kDirect)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) lds.b[t][code_row()][code_chunk() ^ (code_row() / 2 % 4)] = st.b[t][h];
+                for (int t = 0; t < NT; ++t) write_codes(lds.b[t], st.b[t][h]);
             if (h < kXs)
 #pragma unroll
                 for (int j = 0; j < kX; ++j)
@@ -307,22 +331,11 @@ struct I4Wave {
 
     // the dwords of matrix instructions 0 .. 3 of step h of fragment t
     static __device__ __forceinline__ void codes(uint32_t (&w)[4], const Stage &st, const Lds &lds, int t, int h) {
-        const int lane = threadIdx.x % kWave, g = lane / 16, r = lane % 16, swap = r / 2 % 4;
         if constexpr (kDirect) {
             w[0] = st.b[t][h].x, w[1] = st.b[t][h].y, w[2] = st.b[t][h].z, w[3] = st.b[t][h].w;
             share_out<Q>(w);
-        } else if constexpr (Q == 4) {
-            const uint4 v = lds.b[t][r][g ^ swap];
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else if constexpr (Q == 2) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const uint2 x = reinterpret_cast<const uint2 *>(&lds.b[t][r][(2 * v + (g & 1)) ^ swap])[g >> 1];
-                w[2 * v] = x.x, w[2 * v + 1] = x.y;
-            }
         } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) w[u] = reinterpret_cast<const uint32_t *>(&lds.b[t][r][u ^ swap])[g];
+            read_codes<Q>(w, lds.b[t]);
         }
     }
 

@@ -3,11 +3,14 @@
 Every buffer is wider than the operand and holds poison outside it, every output sits among
 sentinels, and each case prints its name before it touches the GPU.
 
-Tolerance: a matrix instruction adds at least 32 products to a binary32 sum, and its result is
-taken to be within four half units (2^-22) of the magnitudes it adds; a block's sum of 32
-values is then scaled and added (two roundings, 2^-23), and up to 8 waves' sums are added (7
-more): (ceil(K / 32) + 2) * 2^-22 of the sum of magnitudes bounds them all.  Rounding to a
-16-bit type adds half a unit of the result, or half its smallest subnormal.
+Tolerance, with A the sum of |a| |scale| over K.  A matrix instruction adds at least 32 products to
+a binary32 sum, and its result is taken to be within four half units (2^-22) of the magnitudes it adds.
+The codes may enter with a bias (16 to 31 in the place of -8 to 7, after 24 times the activations
+were taken off), so those are at most 55 |a| of a step of 128 values, for which at most 8 instructions
+follow one another: 440 * 2^-22 A in all.  Each sum of a group is then scaled and added to a sum below 8
+A, at most 1.25 K / 32 times, and up to 16 waves' and 16 splits' sums are added: another (1.25 K / 32 + 32) * 8
+* 2^-24 A.  (512 + K / 12) * 2^-22 A bounds both.  Rounding to a 16-bit type adds half a unit of the
+result, or half its smallest subnormal.
 """
 from __future__ import annotations
 
@@ -57,11 +60,11 @@ def placed_activations(t):
 
 
 def weights(N, K, group, seed, kind, lo=-8, hi=7):
-    """(codes, scales as a CPU tensor, values in 64 bits)."""
+    """(codes, scales as a CPU tensor, values in 64 bits, the magnitudes of their scales)."""
     rng = np.random.default_rng(seed)
     codes = rng.integers(lo, hi + 1, (N, K))
     scales, sv = held(np.exp2(rng.uniform(-6, 2, (-(-K // group), N))) * rng.choice([-1.0, 1.0], (1, N)), kind)
-    return codes, scales, i4.values(codes, sv, group)
+    return codes, scales, i4.values(codes, sv, group), np.abs(i4.values(np.ones_like(codes), sv, group))
 
 
 def placed_codes(codes):
@@ -81,14 +84,14 @@ def guarded(M, N, kind, pad=3):
     return buf, buf[1:-1, :N]
 
 
-def check(buf, M, N, R, S, K, kind, what):
+def check(buf, M, N, R, A, K, kind, what):
     got = buf.cpu().double().numpy()
     edge = np.ones(got.shape, bool)
     edge[1:-1, :N] = False
     sentinel = float(torch.tensor(-777.0, dtype=TYPES[kind]))
     assert (got[edge] == sentinel).all(), f"{what}: stores beside the result"
     got = got[1:-1, :N]
-    tol = (-(-K // 32) + 2) * 2.0 ** -22 * S
+    tol = (512 + K / 12) * 2.0 ** -22 * A
     tol = tol + (np.abs(R) + tol) * HALF_UNIT[kind] + HALF_TINY[kind]
     bad = ~(np.abs(got - R) <= tol) & (np.abs(R) + tol < float(torch.finfo(TYPES[kind]).max))
     assert not bad.any(), f"{what}: {int(bad.sum())} off, first {np.argwhere(bad)[0]}: {got[bad][0]} for {R[bad][0]}"
@@ -98,20 +101,29 @@ def run_case(pd, M, N, K, group, kind, s_kind, out, seed=0, cfg=None):
     what = f"{M}x{N}x{K} group {group} {kind} scales {s_kind} -> {out} cfg {cfg}"
     gu.note(what)
     a, av = activations(M, K, seed, kind)
-    codes, scales, w = weights(N, K, group, seed + 1, s_kind)
-    R, S = i4.product(av, w)
+    codes, scales, w, m = weights(N, K, group, seed + 1, s_kind)
+    R, A = i4.product(av, w)[0], np.abs(av) @ m.T
     buf, view = guarded(M, N, out)
     pd.gemm_a16_i4(placed_activations(a), placed_codes(codes), placed(scales, 3, float("nan")), group, out=view, cfg=cfg)
-    check(buf, M, N, R, S, K, out, what)
+    check(buf, M, N, R, A, K, out, what)
 
 
-@pytest.mark.parametrize("cfg", range(12))
+def configs(pd, group):
+    """The tile configurations that serve a group: the last one multiples of 128."""
+    return range(pd.a16_i4_num_configs() - (1 if group % 128 else 0))
+
+
+@pytest.mark.parametrize("cfg", range(11))
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 def test_every_tile(pd, cfg, kind):
-    if cfg >= pd.a16_i4_num_configs():
-        pytest.skip("no such configuration")
+    assert pd.a16_i4_num_configs() == 11
     for n, (M, N, K, group) in enumerate([(1, 1, 1, 32), (3, 17, 129, 32), (16, 64, 256, 64), (17, 65, 333, 64), (33, 130, 640, 128),
-                                          (67, 70, 1337, 96), (65, 100, 2048, 256), (130, 33, 5000, 160), (2, 40, 96, 4096)]):
+                                          (67, 70, 1337, 96), (65, 100, 2048, 256), (130, 33, 5000, 160), (2, 40, 96, 4096),
+                                          (260, 270, 1500, 128), (129, 513, 257, 256)]):
+        if cfg not in configs(pd, group):
+            with pytest.raises(pd.PdgemmError):
+                run_case(pd, M, N, K, group, kind, "f32", "f32", 0, cfg)
+            continue
         run_case(pd, M, N, K, group, kind, ("f32", kind)[n % 2], ("f32", "f16", "bf16")[n % 3], 7 * n, cfg)
 
 
@@ -131,20 +143,20 @@ def test_every_code_exactly(pd):
         for group in (32, 64, 128):
             scales, sv = held(np.exp2(np.arange(16) - 8.0)[None, :] * (1 + np.arange(-(-K // group)))[:, None], kind)
             eye = torch.eye(K, dtype=TYPES[kind])
-            for cfg in range(pd.a16_i4_num_configs()):
+            for cfg in configs(pd, group):
                 got = pd.gemm_a16_i4(eye.cuda(), placed_codes(codes), scales.cuda(), group, cfg=cfg)
                 assert np.array_equal(got.cpu().double().numpy(), i4.values(codes, sv, group).T), (kind, group, cfg)
 
 
 def test_infinities_and_nan(pd):
     K, N = 200, 24
-    codes, scales, w = weights(N, K, 64, 5, "f32", lo=1)
+    codes, scales, w, m = weights(N, K, 64, 5, "f32", lo=1)
     for kind in ("f16", "bf16"):
         a, av = activations(4, K, 6, kind)
         a[1, 7], a[2, 190], a[3, 0] = float("inf"), float("nan"), -float("inf")
         with np.errstate(invalid="ignore"):
             R = a.double().numpy() @ w.T                         # no code is zero: infinite, of either sign
-        for cfg in range(pd.a16_i4_num_configs()):
+        for cfg in configs(pd, 64):
             got = pd.gemm_a16_i4(placed_activations(a), placed_codes(codes), scales.cuda(), 64, cfg=cfg).cpu().double().numpy()
             assert np.array_equal(np.isnan(got), np.isnan(R)), (kind, cfg)
             assert np.array_equal(got[1], R[1]) and np.array_equal(got[3], R[3]), (kind, cfg)
@@ -158,13 +170,13 @@ def test_infinities_and_nan(pd):
 def test_large_activations_and_scales_stay_finite(pd):
     """Products of 2^120 activations with small scales, and the other way round."""
     K = 256
-    codes, scales, w = weights(32, K, 128, 8, "f32")
+    codes, scales, w, m = weights(32, K, 128, 8, "f32")
     for up, down in ((2.0 ** 120, 2.0 ** -100), (2.0 ** -100, 2.0 ** 118)):
         a, av = held(np.random.default_rng(1).uniform(-1, 1, (3, K)) * up, "bf16")
-        R, S = i4.product(av, w * down)
+        R, A = i4.product(av, w * down)[0], np.abs(av) @ m.T * down
         buf, view = guarded(3, 32, "f32")
         pd.gemm_a16_i4(a.cuda(), placed_codes(codes), (scales.double() * down).float().cuda(), 128, out=view)
-        check(buf, 3, 32, R, S, K, "f32", f"{up}")
+        check(buf, 3, 32, R, A, K, "f32", f"{up}")
 
 
 def test_empty(pd):
@@ -179,18 +191,18 @@ def test_empty(pd):
 def test_a_sequences_last_token(pd):
     """h[:, -1, :] of one sequence: a row whose stride says nothing."""
     h, hv = activations(9, 512, 3, "bf16")
-    codes, scales, w = weights(100, 512, 128, 4, "bf16")
+    codes, scales, w, m = weights(100, 512, 128, 4, "bf16")
     last = h.cuda().view(1, 9, 512)[:, -1, :]
-    R, S = i4.product(hv[-1:], w)
+    R, A = i4.product(hv[-1:], w)[0], np.abs(hv[-1:]) @ m.T
     buf, view = guarded(1, 100, "f32")
     pd.gemm_a16_i4(last, placed_codes(codes), scales.cuda(), 128, out=view)
-    check(buf, 1, 100, R, S, 512, "f32", "last token")
+    check(buf, 1, 100, R, A, 512, "f32", "last token")
 
 
 def test_long_rows_of_scales_and_codes(pd):
     """Rows at the longest strides: offsets of a tile's last row, and of the last group, past 32 bits."""
     N, K, group = 40, 4096, 32
-    codes, scales, w = weights(N, K, group, 9, "f32")
+    codes, scales, w, m = weights(N, K, group, 9, "f32")
     wide = torch.zeros(N, 1 << 22, dtype=torch.uint8, device="cuda")
     wide[:, :K // 2] = torch.from_numpy(i4.pack(codes))
     s = torch.zeros(K // group, 1 << 20, device="cuda")
@@ -198,15 +210,15 @@ def test_long_rows_of_scales_and_codes(pd):
     many = torch.zeros(70, 1 << 21, dtype=torch.bfloat16, device="cuda")
     a, av = activations(70, K, 10, "bf16")
     many[:, :K] = a
-    R, S = i4.product(av, w)
-    for cfg in range(pd.a16_i4_num_configs()):
+    R, A = i4.product(av, w)[0], np.abs(av) @ m.T
+    for cfg in configs(pd, group):
         buf, view = guarded(70, N, "f32")
         pd.gemm_a16_i4(many[:, :K], wide[:, :K // 2], s[:, :N], group, out=view, cfg=cfg)
-        check(buf, 70, N, R, S, K, "f32", f"cfg {cfg}")
+        check(buf, 70, N, R, A, K, "f32", f"cfg {cfg}")
 
 
 def test_same_bits_again_on_streams_and_in_a_replayed_graph(pd):
-    codes, scales, w = weights(300, 1000, 64, 12, "f16")
+    codes, scales, w, m = weights(300, 1000, 64, 12, "f16")
     b, s = placed_codes(codes), scales.cuda()
     a = activations(20, 1000, 13, "f16")[0].cuda()
     want = pd.gemm_a16_i4(a, b, s, 64)

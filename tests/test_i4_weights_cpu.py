@@ -40,7 +40,7 @@ def test_route_by_hand():
 def test_experts_by_hand():
     w13 = [np.array([[1.0, 0.0], [0.0, 2.0]])]           # gate reads x0, up reads 2 x1
     w2 = [np.array([[3.0], [-1.0]])]
-    y, _, _, _ = i4.experts(np.array([[1.0, 5.0], [1.0, 5.0]]), np.array([[0, -1], [0, 0]]), np.array([[0.5, 9.0], [0.25, 0.5]]), w13, w2)
+    y = i4.experts(np.array([[1.0, 5.0], [1.0, 5.0]]), np.array([[0, -1], [0, 0]]), np.array([[0.5, 9.0], [0.25, 0.5]]), w13, w2)[0]
     act = 10.0 / (1 + np.exp(-1.0))
     assert np.allclose(y, [[1.5 * act, -0.5 * act], [2.25 * act, -0.75 * act]])
 
@@ -136,7 +136,8 @@ def test_every_pick_is_a_configuration(lib):
     for M in (1, 3, 8, 9, 16, 17, 32, 33, 64, 65, 100, 128, 129, 500, 2048, 100000):
         for N in (1, 64, 1000, 4096, 8192, 65536):
             for K in (0, 1, 128, 4096, 65536):
-                assert 0 <= lib.pdgemm_a16_i4_pick(M, N, K) < n
+                for group in (32, 128):
+                    assert 0 <= lib.pdgemm_a16_i4_pick(M, N, K, group) < n
 
 
 @built

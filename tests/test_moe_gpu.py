@@ -1,12 +1,11 @@
 """GPU parity of the expert layer and its routing with the 64-bit oracle.
 
-Tolerance of the layer.  The first product's sums are within (ceil(H / 32) + 2) * 2^-22 of their
-terms' magnitudes (as in the products' own tests), which silu(g) * u carries on with slopes of
-1.1 |u| and |silu(g)|.  silu's exponential takes its argument in binary32: a relative 2^-16
-covers |g| < 128 and the few roundings after it.  The gated activation is rounded to 16 bits:
-half a unit of it (2^-11, 2^-8), or half the type's smallest subnormal.  The second product
-sums over all experts that have a token: (experts * ceil(I / 32) + 18) * 2^-22 of the terms.  y is
-rounded once more.
+Tolerance of the layer.  The first product's sums are within (512 + H / 12) * 2^-22 of the sum of
+|x| |scale| (as in the products' own tests), which silu(g) * u carries on with slopes of 1.1 |u| and
+|silu(g)|.  silu's exponential takes its argument in binary32: a relative 2^-16 covers |g| < 128 and the
+few roundings after it.  The gated activation is rounded to 16 bits: half a unit of it (2^-11,
+2^-8), or half the type's smallest subnormal.  The second product sums over all experts that have a token:
+(512 + experts * I / 12) * 2^-22 of the sum of |activation| |scale|.  y is rounded once more.
 """
 from __future__ import annotations
 
@@ -31,7 +30,8 @@ def pd():
 
 
 def expert_weights(E, N, K, group, seed, kind):
-    """(codes on the GPU (E, N, ceil(K/2)) among 0x77, scales (E, groups, N) among NaN, the list of dense values)."""
+    """(codes on the GPU (E, N, ceil(K/2)) among 0x77, scales (E, groups, N) among NaN, the lists of dense values
+    and of their scales' magnitudes)."""
     rng = np.random.default_rng(seed)
     codes = rng.integers(-8, 8, (E, N, K))
     width = (K + 1) // 2
@@ -45,7 +45,8 @@ def expert_weights(E, N, K, group, seed, kind):
     sb = torch.full((E + 1, groups + 1, N + 3), float("nan"), dtype=scales.dtype)
     sb[:E, :groups, :N] = scales
     dense = [i4.values(codes[e], sv[e], group) for e in range(E)]
-    return buf.cuda()[:E, :N, :width], sb.cuda()[:E, :groups, :N], dense
+    size = [np.abs(i4.values(np.ones_like(codes[e]), sv[e], group)) for e in range(E)]
+    return buf.cuda()[:E, :N, :width], sb.cuda()[:E, :groups, :N], (dense, size)
 
 
 def layer(T, H, I, E, group, seed, kind, s_kind):
@@ -56,11 +57,12 @@ def layer(T, H, I, E, group, seed, kind, s_kind):
     return placed_activations(x), xv, (w13, s13, w2, s2), d13, d2
 
 
-def check_layer(got, edge, xv, ids, weights, d13, d2, kind, what):
+def check_layer(got, edge, xv, ids, weights, first, second, kind, what):
     """got: the output's buffer with `edge` sentinel rows and columns around y."""
     T, H = xv.shape
+    (d13, m13), (d2, m2) = first, second
     I = d2[0].shape[1]
-    R, size, act_size, mass = i4.experts(xv, ids, weights, d13, d2)
+    R, size, act_size, second, mass = i4.experts(xv, ids, weights, d13, d2, m13, m2)
     full = got.cpu().double().numpy()
     y = full[1:-1, :H] if edge else full
     if edge:
@@ -68,8 +70,8 @@ def check_layer(got, edge, xv, ids, weights, d13, d2, kind, what):
         rim[1:-1, :H] = False
         assert (full[rim] == float(torch.tensor(-777.0, dtype=TYPES[kind]))).all(), f"{what}: stores beside the result"
     live = len({e for row in ids for e in row if 0 <= e < len(d2)})
-    tol = act_size * (-(-H // 32) + 2) * 2.0 ** -22 + mass * HALF_TINY[kind]
-    tol += (size + tol) * (HALF_UNIT[kind] + 2.0 ** -16 + (live * -(-I // 32) + 18) * 2.0 ** -22)
+    tol = act_size * (512 + H / 12) * 2.0 ** -22 + mass * HALF_TINY[kind]
+    tol += (size + tol) * (HALF_UNIT[kind] + 2.0 ** -16) + (second + tol) * (512 + live * I / 12) * 2.0 ** -22
     tol += (np.abs(R) + tol) * HALF_UNIT[kind] + HALF_TINY[kind]
     bad = ~(np.abs(y - R) <= tol)
     assert not bad.any(), f"{what}: {int(bad.sum())} off, first {np.argwhere(bad)[0]}: {y[bad][0]} for {R[bad][0]}"
@@ -202,8 +204,8 @@ def test_norm_route_and_experts_together(pd):
     wi, ww = i4.route(logits.cpu().double().numpy(), top)
     assert np.array_equal(ids.cpu().numpy(), wi) and np.allclose(weights.cpu().numpy(), ww, rtol=2.0 ** -17)
     check_layer(out, False, yv, wi, weights.cpu().double().numpy(), d13, d2, "f16", "together")
-    R, S = i4.product(yv, d13[0])
-    assert (np.abs(shared.cpu().double().numpy() - R) <= (H // 32 + 2) * 2.0 ** -22 * S).all()
+    R, A = i4.product(yv, d13[0][0])[0], np.abs(yv) @ d13[1][0].T
+    assert (np.abs(shared.cpu().double().numpy() - R) <= (512 + H / 12) * 2.0 ** -22 * A).all()
 
 
 def test_same_bits_again_on_streams_and_in_replayed_graphs(pd):

@@ -322,7 +322,15 @@ struct I4Wave {
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) odd = __builtin_fmaf(d[t][e], 0.0f, odd);
-            if (__builtin_expect(__any(!(odd == 0.0f)), 0)) sum_step<false>(d, st, lds, h);   // (NaN: infinity or NaN in d)
+            if (__builtin_expect(__any(!(odd == 0.0f)), 0)) {   // (NaN: infinity or NaN in d)
+                // (only those sums change: the others' bits are the same beside them as without them)
+                floatx4_t whole[NT];
+                sum_step<false>(whole, st, lds, h);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[t][e] = d[t][e] * 0.0f == 0.0f ? d[t][e] : whole[t][e];
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] += d[t];
             if (!kDirect || h == 1) wave_lds_order();

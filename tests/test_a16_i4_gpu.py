@@ -217,6 +217,26 @@ def test_long_rows_of_scales_and_codes(pd):
         check(buf, 70, N, R, A, K, "f32", f"cfg {cfg}")
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_what_is_not_finite_leaves_the_other_sums_bits(pd, kind):
+    """A row of A and a column's scale that are not finite change their own row and column alone, to the bit."""
+    M, N, K, group = 40, 100, 700, 64
+    a, _ = activations(M, K, 2, kind)
+    codes, scales, _, _ = weights(N, K, group, 3, "f32")
+    rows, cols = [i for i in range(M) if i % 5 != 1], [j for j in range(N) if j != 17]
+    bad, bad_scales = a.clone(), scales.clone()
+    bad[1::5, 333] = float("inf")
+    bad_scales[2, 17] = float("nan")
+    for m in (2, 7, 16, 40):
+        what = f"{m} rows of {kind}"
+        gu.note(what)
+        want, got = (pd.gemm_a16_i4(placed_activations(x[:m]), placed_codes(codes), s.cuda(), group, out_dtype=torch.float32).cpu()
+                     for x, s in ((a, scales), (bad, bad_scales)))
+        keep = [i for i in rows if i < m]
+        assert torch.equal(got[keep][:, cols], want[keep][:, cols]), what
+        assert torch.isnan(got[:, 17]).all() and not torch.isfinite(got[1]).any(), what
+
+
 def test_same_bits_again_on_streams_and_in_a_replayed_graph(pd):
     codes, scales, w, m = weights(300, 1000, 64, 12, "f16")
     b, s = placed_codes(codes), scales.cuda()

@@ -143,6 +143,23 @@ def test_bad_token_stays_alone(pd):
     assert torch.isfinite(y[keep]).all()
 
 
+def test_bad_tokens_leave_the_others_bits(pd):
+    """Thirty tokens of one expert, in whatever order they reach its tiles: with some of them not finite, the
+    others' results keep their bits."""
+    x, xv, w, d13, d2 = layer(30, 300, 96, 2, 32, 9, "bf16", "f32")
+    ids, ones = torch.zeros(30, 1, dtype=torch.int32, device="cuda"), torch.ones(30, 1, device="cuda")
+    want = pd.moe_a16_i4(x, ids, ones, *w, 32).cpu()
+    x[4, 7], x[13, 280], x[21, 0] = float("nan"), float("-inf"), 3e38
+    keep = [t for t in range(30) if t not in (4, 13, 21)]
+    for _ in range(5):
+        assert torch.equal(pd.moe_a16_i4(x, ids, ones, *w, 32).cpu()[keep], want[keep])
+
+
+@pytest.mark.parametrize("T,E,top", [(4096, 3, 1), (512, 20, 8), (64, 1024, 64)])
+def test_most_pairs(pd, T, E, top):
+    run_layer(pd, T, 32, 16, E, top, 32, "f16", "f16")
+
+
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T,E,top", [(1, 1, 1), (3, 7, 7), (5, 64, 8), (9, 65, 4), (4, 128, 64), (6, 200, 16), (2, 257, 3), (7, 1024, 64)])
 def test_route(pd, T, E, top, kind):

@@ -37,19 +37,17 @@ __device__ __forceinline__ Inverse inverse_of(double e) {
 // whether binary32 sums of squares serve: neither overflown nor lost below its range
 __device__ __forceinline__ bool in_range(float ss, float mean_eps) { return ss <= 0x1p126f && mean_eps >= 0x1p-100f; }
 
-// Sum and maximum over the threads of a row: kLanes neighbouring lanes, or (0) the whole
-// workgroup, whose waves meet in `part`.  The waves' sums are added in wave order.
+// Sum and maximum over the threads of a row: kLanes neighbouring lanes, or (0) waves
+// first .. first + waves - 1 of the workgroup, which meet in `part`.  The waves' sums are added in wave order.
 template <int kLanes>
-__device__ __forceinline__ void over_row(float &a, float &b, float (*part)[2]) {
+__device__ __forceinline__ void over_row(float &a, float &b, float (*part)[2], int first, int waves) {
     a = sum_over_lanes<kLanes ? kLanes : kWave>(a);
     b = sum_over_lanes<kLanes ? kLanes : kWave>(b);
     if constexpr (kLanes == 0) {
-        const int waves = blockDim.x / kWave;
-        if (waves == 1) return;
         if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave][0] = a, part[threadIdx.x / kWave][1] = b;
         __syncthreads();
-        a = part[0][0], b = part[0][1];
-        for (int i = 1; i < waves; ++i) a += part[i][0], b += part[i][1];
+        a = part[first][0], b = part[first][1];
+        for (int i = 1; i < waves; ++i) a += part[first + i][0], b += part[first + i][1];
     }
 }
 template <int kLanes>
@@ -66,15 +64,14 @@ __device__ __forceinline__ void sum_and_max_over_row(float &a, uint32_t &m, floa
     }
 }
 template <int kLanes>
-__device__ __forceinline__ double sum_over_row64(double a, double *part) {
+__device__ __forceinline__ double sum_over_row64(double a, double *part, int first, int waves) {
     a = sum_over_lanes64<kLanes ? kLanes : kWave>(a);
     if constexpr (kLanes == 0) {
-        const int waves = blockDim.x / kWave;
         __syncthreads();   // (the part may be read still)
         if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = a;
         __syncthreads();
-        a = part[0];
-        for (int i = 1; i < waves; ++i) a += part[i];
+        a = part[first];
+        for (int i = 1; i < waves; ++i) a += part[first + i];
     }
     return a;
 }
@@ -140,7 +137,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int i = 0; i < N; ++i) s64 += (double)h[v][i] * (double)h[v][i];
-        return inverse_of(sum_over_row64<kLanes>(s64, part64) / args.cols + (double)args.eps);
+        return inverse_of(sum_over_row64<kLanes>(s64, part64, 0, blockDim.x / kWave) / args.cols + (double)args.eps);
     };
 
     Out *const out = static_cast<Out *>(args.out) + row * args.ldo;
@@ -179,7 +176,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
         }
     } else {
         float none = 0;
-        over_row<kLanes>(ss, none, part);
+        over_row<kLanes>(ss, none, part, 0, blockDim.x / kWave);
         const Inverse f = inverse(ss);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -200,105 +197,186 @@ struct GradArgs {
     float *dw;                 // a row of cols per workgroup
     int64_t lddy, ldh, lddh, lddx;
     int rows, cols;
+    int step;                  // threads of a row
     int w_type;
     float eps;
 };
 
+// 16 bytes of a row, held as they are: converted, 16-bit values take twice the registers
+struct Run {
+    uint32_t d[4];
+};
+template <int T>
+__device__ __forceinline__ Run load_packed(const typename ElemOf<T>::type *p, int n) {
+    using Elem = typename ElemOf<T>::type;
+    constexpr int N = 16 / elem_size(T);
+    Run r = {{0, 0, 0, 0}};
+    if (n >= N) {
+        Elem e[N];
+        load_run<N>(e, p);
+        __builtin_memcpy(&r, e, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) {
+                if constexpr (T == kF32)
+                    r.d[i] = bits_of(p[i]);
+                else
+                    r.d[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (i % 2 * 16);
+            }
+    }
+    return r;
+}
+template <int T>
+__device__ __forceinline__ float value_of(const Run &r, int i) {
+    if constexpr (T == kF32) return as_float(r.d[i]);
+    if constexpr (T == kBF16) return as_float(i % 2 ? r.d[i / 2] & 0xFFFF0000u : r.d[i / 2] << 16);
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)(r.d[i / 2] >> (i % 2 * 16)));
+}
+__device__ __forceinline__ void as_it_is(Run &r) { asm volatile("" : "+v"(r.d[0]), "+v"(r.d[1]), "+v"(r.d[2]), "+v"(r.d[3])); }
+
 // With n = h r and g = dy w: dx = r (g - n mean(g n)) + dh, and dw is the sum over the rows of
-// dy n.  A workgroup takes every gridDim.x-th row (kLanes: a group of lanes every such row
-// of groups), keeps its share of dw in registers, and writes it for join_kernel.
+// dy n.  kLanes lanes, or (0) args.step threads of whole waves, have a row, a workgroup as many rows at a time as
+// it has such groups.  It takes every gridDim.x-th row of groups, keeps its share of dw in registers, and
+// writes it for join_kernel.  Memory bounds it: 4096 x 8192 of bf16 with dh takes 65 us, 268 MB at 4.1 TB/s
+// (shares of dw 17 MB more, join_kernel 4 us), 8192 x 4096 58 us.  A thread's values stay in registers up to two runs:
+// with four and eight they spill, and reading the row again from the caches is faster (1024 x 32768 of bf16 121 us
+// against 149, of f32 169 against 341).
 template <int T, int V, int kLanes>
-__global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_backward_kernel(GradArgs args) {
+__global__ __launch_bounds__(1024, 4) void rms_norm_backward_kernel(GradArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using Elem = typename ElemOf<T>::type;
     constexpr int N = 16 / elem_size(T);
-    constexpr int kGroups = kLanes ? 256 / (kLanes ? kLanes : 1) : 1;
     __shared__ float part[2][16][2];
     __shared__ double part64[16];
-    __shared__ float join[kLanes ? kGroups : 1][kLanes ? kLanes * N * V : 1];
+    __shared__ int odd[3];
+    __shared__ float join[V == 1 ? 256 * N : 1];   // a row of step * N for each group
 
     const int tid = threadIdx.x;
-    const int step = kLanes ? kLanes : (int)blockDim.x, t = kLanes ? tid % (kLanes ? kLanes : 1) : tid;
-    const int group = kLanes ? tid / (kLanes ? kLanes : 1) : 0;
+    const int step = kLanes ? kLanes : args.step, group = tid / step, t = tid - group * step, groups = blockDim.x / step;
+    const int first_wave = kLanes ? 0 : group * (step / kWave), waves = kLanes ? 0 : step / kWave;
 
-    float w[V][N], dw[V][N];
+    constexpr bool kKeep = V * N <= 8;      // the weights stay in registers
+    constexpr int kTurns = V <= 2 ? V : 1;   // runs at a time
+    float w[kKeep ? V : 1][N], dw[V][N];
+    auto load_w = [&](int v) __attribute__((always_inline)) {
+        const int at = (v * step + t) * N;
+        load_some_as_float<N>(w[kKeep ? v : 0], args.w, args.w_type, at, args.cols - at);
+    };
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int at = (v * step + t) * N;
-        load_some_as_float<N>(w[v], args.w, args.w_type, at, args.cols - at);
+        if (kKeep) load_w(v);
 #pragma unroll
         for (int i = 0; i < N; ++i) dw[v][i] = 0;
     }
-    int turn = 0;
-    for (int64_t first = (int64_t)blockIdx.x * kGroups; first < args.rows; first += (int64_t)gridDim.x * kGroups, ++turn) {
+    if (kLanes == 0 && V == 1) {
+        if (tid < 3) odd[tid] = 0;
+        __syncthreads();
+    }
+    int turn = 0, mark = 0;
+    for (int64_t first = (int64_t)blockIdx.x * groups; first < args.rows; first += (int64_t)gridDim.x * groups, ++turn) {
         const int64_t row = first + group;
         const int cols = row < args.rows ? args.cols : 0;
-        Elem h[V][N], dy[V][N], dh[V][N];
+        Run h[V <= 2 ? V : 1], dy[V <= 2 ? V : 1], dh[V <= 2 ? V : 1];
         const Elem *const ph = static_cast<const Elem *>(args.h) + row * args.ldh;
         const Elem *const pdy = static_cast<const Elem *>(args.dy) + row * args.lddy;
+        const Elem *const pdh = static_cast<const Elem *>(args.dh) + row * args.lddh;
+        // (of more runs than two the later passes read the row again, from the caches)
+        auto load = [&](int v, bool all) __attribute__((always_inline)) {
+            const int at = (v * step + t) * N, own = V <= 2 ? v : 0;
+            h[own] = load_packed<T>(ph + at, cols - at);
+            dy[own] = load_packed<T>(pdy + at, cols - at);
+            if (all && args.dh) dh[own] = load_packed<T>(pdh + at, cols - at);
+        };
+        if (V <= 2)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int at = (v * step + t) * N;
-            load_some<N>(h[v], ph + at, cols - at);
-            load_some<N>(dy[v], pdy + at, cols - at);
-        }
-        if (args.dh) {
-            const Elem *const pdh = static_cast<const Elem *>(args.dh) + row * args.lddh;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int at = (v * step + t) * N;
-                load_some<N>(dh[v], pdh + at, cols - at);
-            }
-        }
+            for (int v = 0; v < V; ++v) load(v, true);
         float ss = 0, dot = 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
+#pragma unroll kTurns
+        for (int x = 0; x < V; ++x) {
+            const int v = V <= 2 ? x : 0;
+            if (V > 2) load(x, false);
+            if (!kKeep) load_w(x);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                ss = __builtin_fmaf((float)h[v][i], (float)h[v][i], ss);
-                dot = __builtin_fmaf((float)dy[v][i] * w[v][i], (float)h[v][i], dot);
+                const float value = value_of<T>(h[v], i);
+                ss = __builtin_fmaf(value, value, ss);
+                dot = __builtin_fmaf(value_of<T>(dy[v], i) * w[kKeep ? v : 0][i], value, dot);
             }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (V == 2 && !kKeep) as_it_is(h[v]), as_it_is(dy[v]);
+        // A row whose sums leave binary32's range is summed in 64 bits.  All waves take part, each for its own
+        // row, and rows in range keep their sums; so that one barrier will do, each wave says before it whether
+        // its share may be of such a row (three marks in turn: one is cleared while others are read and set).
+        const bool several = kLanes == 0 && V == 1 && groups > 1;
+        if (several) {
+            const float a = sum_over_lanes<kWave>(ss), b = sum_over_lanes<kWave>(dot);
+            if (tid % kWave == 0 && row < args.rows &&
+                !(a <= 0x1p120f && a / (float)args.cols + args.eps >= 0x1p-100f && fabsf(b) <= 0x1p120f))
+                odd[mark] = 1;
+        }
         // (two parts in turn: a wave writes the next row's while another reads this one's)
-        over_row<kLanes>(ss, dot, part[turn & 1]);
+        over_row<kLanes>(ss, dot, part[turn & 1], first_wave, waves);
         float mean;        // of g n
         Inverse f = {1.0f, 1.0f};
         const float e = ss / (float)args.cols + args.eps;
         float r;
-        if (in_range(ss, e) && fabsf(dot) <= 0x1p126f) {
+        const bool fine = in_range(ss, e) && fabsf(dot) <= 0x1p126f;
+        if (fine) {
             r = f.r = 1.0f / sqrtf(e);
             mean = dot * r / (float)args.cols;
-        } else {
+        }
+        bool sum64 = !fine;
+        if (several) {
+            sum64 = odd[mark];
+            mark = mark < 2 ? mark + 1 : 0;
+            if (tid == 0) odd[mark < 2 ? mark + 1 : 0] = 0;
+        }
+        if (sum64) {
             double s64 = 0, d64 = 0;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
+#pragma unroll kTurns
+            for (int x = 0; x < V; ++x) {
+                const int v = V <= 2 ? x : 0;
+                if (V > 2) load(x, false);
+                if (!kKeep) load_w(x);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    s64 += (double)h[v][i] * (double)h[v][i];
-                    d64 += (double)dy[v][i] * (double)w[v][i] * (double)h[v][i];
+                    const double value = value_of<T>(h[v], i);
+                    s64 += value * value;
+                    d64 += (double)value_of<T>(dy[v], i) * (double)w[kKeep ? v : 0][i] * value;
                 }
-            const double e64 = sum_over_row64<kLanes>(s64, part64) / args.cols + (double)args.eps;
-            f = inverse_of(e64);
-            r = (float)(1.0 / sqrt(e64));
-            mean = (float)(sum_over_row64<kLanes>(d64, part64) / sqrt(e64) / args.cols);
+            }
+            s64 = sum_over_row64<kLanes>(s64, part64, first_wave, waves);
+            d64 = sum_over_row64<kLanes>(d64, part64, first_wave, waves);
+            if (!fine) {
+                const double e64 = s64 / args.cols + (double)args.eps;
+                f = inverse_of(e64);
+                r = (float)(1.0 / sqrt(e64));
+                mean = (float)(d64 / sqrt(e64) / args.cols);
+            }
         }
         Elem *const pdx = static_cast<Elem *>(args.dx) + row * args.lddx;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int at = (v * step + t) * N;
+        for (int x = 0; x < V; ++x) {
+            const int v = V <= 2 ? x : 0, at = (x * step + t) * N;
+            if (V > 2) load(x, true);
+            if (!kKeep) load_w(x);
             Elem dx[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float n = (float)h[v][i] * f.c * f.r;
-                float d = r * __builtin_fmaf(-n, mean, (float)dy[v][i] * w[v][i]);
-                if (args.dh) d += (float)dh[v][i];
+                const float n = value_of<T>(h[v], i) * f.c * f.r, g = value_of<T>(dy[v], i);
+                float d = r * __builtin_fmaf(-n, mean, g * w[kKeep ? v : 0][i]);
+                if (args.dh) d += value_of<T>(dh[v], i);
                 dx[i] = (Elem)d;
-                if (cols) dw[v][i] = __builtin_fmaf((float)dy[v][i], n, dw[v][i]);   // (lanes of no row: n may be NaN)
+                if (cols) dw[x][i] = __builtin_fmaf(g, n, dw[x][i]);   // (lanes of no row: n may be NaN)
             }
             store_some<N>(pdx + at, dx, cols - at);
         }
     }
     float *const out = args.dw + (int64_t)blockIdx.x * args.cols;
-    if constexpr (kLanes == 0) {
+    if (V > 1 || groups == 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int at = (v * step + t) * N;
@@ -306,13 +384,11 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_backward_kernel(
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < N; ++i) join[group][(v * step + t) * N + i] = dw[v][i];
+        for (int i = 0; i < N; ++i) join[tid * N + i] = dw[0][i];
         __syncthreads();
-        for (int j = tid; j < args.cols; j += 256) {
-            float s = join[0][j];
-            for (int k = 1; k < kGroups; ++k) s += join[k][j];
+        for (int j = tid; j < args.cols; j += blockDim.x) {
+            float s = join[j];
+            for (int k = 1; k < groups; ++k) s += join[k * step * N + j];
             out[j] = s;
         }
     }
@@ -397,11 +473,22 @@ int check_norm_sizes(int64_t rows, int64_t cols) {
     return rows < 0 || cols < 0 || rows > (int64_t(1) << 30) || cols > kMaxCols ? PDGEMM_EINVAL_DIM : PDGEMM_OK;
 }
 
-// workgroups of the gradient: two of 1024 threads fit a CU
-int64_t grad_blocks(int64_t rows, int64_t cols) {
-    const Share s = share_of(cols, kF32);
-    const int64_t groups = s.lanes ? cdiv(rows, 256 / s.lanes) : rows;
-    return groups < 512 ? groups : 512;
+// The gradient's share: as many groups of threads with a row each as 256 threads have, and 1024 threads on
+// each CU, what the registers allow.  (Workgroups of 512 and 1024 threads with more rows each, which wait for one
+// another at every sum: 16384 x 2048 of bf16 7 and 12% slower.)
+struct GradShare {
+    Share s;
+    int groups;
+    int64_t blocks;
+};
+GradShare grad_share_of(int64_t rows, int64_t cols, int type) {
+    GradShare g = {share_of(cols, type), 1, 0};
+    const int step = g.s.lanes ? g.s.lanes : g.s.threads;
+    if (g.s.v == 1) g.groups = step < 256 ? 256 / step : 1;
+    g.s.threads = step * g.groups;
+    const int64_t turns = cdiv(rows, g.groups), most = 256 * (g.s.threads < 1024 ? 1024 / g.s.threads : 1);
+    g.blocks = turns < most ? turns : most;
+    return g;
 }
 
 }  // namespace
@@ -436,8 +523,8 @@ int pdgemm_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int 
 
 int64_t pdgemm_rms_norm_backward_workspace_size(int64_t rows, int64_t cols) {
     if (check_norm_sizes(rows, cols) != PDGEMM_OK) return 0;
-    const int64_t blocks = grad_blocks(rows, cols);
-    return blocks > 1 ? blocks * cols * 4 : 0;
+    const int64_t a = grad_share_of(rows, cols, kF32).blocks, b = grad_share_of(rows, cols, kF16).blocks;
+    return a > 1 || b > 1 ? (a > b ? a : b) * cols * 4 : 0;
 }
 
 int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t lddy, const void *h, int64_t ldh,
@@ -463,17 +550,15 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
         if (!workspace) return PDGEMM_ENULL;
         if (workspace_bytes < need || ((uintptr_t)workspace & 15)) return PDGEMM_EWORKSPACE;
     }
-    const int64_t blocks = grad_blocks(rows, cols);
+    const GradShare g = grad_share_of(rows, cols, type);
     if (rows > 0) {
         GradArgs args = {dy, h, dh, weight, dx, need ? static_cast<float *>(workspace) : dweight, lddy, ldh, lddh, lddx,
-                         (int)rows, (int)cols, weight_type, eps};
-        const Share s = share_of(cols, type);
-        const void *fn = type == kF32 ? grad_ptr<kF32>(s) : type == kF16 ? grad_ptr<kF16>(s) : grad_ptr<kBF16>(s);
-        // (a 16-bit row may have fewer groups of lanes than the workspace's size allows for)
-        rc = run(fn, blocks, s.threads, &args, stream);
+                         (int)rows, (int)cols, g.s.threads / g.groups, weight_type, eps};
+        const void *fn = type == kF32 ? grad_ptr<kF32>(g.s) : type == kF16 ? grad_ptr<kF16>(g.s) : grad_ptr<kBF16>(g.s);
+        rc = run(fn, g.blocks, g.s.threads, &args, stream);
         if (rc != PDGEMM_OK || !need) return rc;
     }
-    JoinArgs args = {static_cast<const float *>(workspace), dweight, (int)(rows > 0 ? blocks : 0), (int)cols};
+    JoinArgs args = {static_cast<const float *>(workspace), dweight, (int)(rows > 0 ? g.blocks : 0), (int)cols};
     return run(reinterpret_cast<const void *>(&join_kernel), cdiv(cols, kWave), 1024, &args, stream);
 }
 

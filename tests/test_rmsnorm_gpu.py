@@ -182,7 +182,7 @@ def test_gradient_against_differences(pd):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
-@pytest.mark.parametrize("cols", [40, 300, 5000])
+@pytest.mark.parametrize("cols", [40, 300, 700, 5000, 20000])
 def test_rows_outside_the_range_of_squares(pd, kind, cols):
     """Squares that overflow or vanish in binary32, among ordinary rows."""
     for eps in (EPS, 0.0):
@@ -214,6 +214,25 @@ def test_rows_outside_the_range_of_squares(pd, kind, cols):
         assert (np.abs(got - wdx) <= tol)[top].all(), what
 
 
+@pytest.mark.parametrize("rows,cols", [(5000, 300), (9000, 40), (3000, 200)])
+def test_odd_rows_leave_the_others_bits(pd, rows, cols):
+    """More rows than the groups of threads: rows outside the range of squares, each time beside others."""
+    x, g, dh = (values(rows, cols, 60 + k, "f32")[0].cuda() for k in range(3))
+    w = weights(cols, 63, "f32")[0].cuda()
+    want, _ = pd.rms_norm_backward(g, x, w, EPS, dh=dh)
+    odd = torch.zeros(rows, dtype=torch.bool)
+    odd[::7], odd[rows // 2] = True, True
+    x[odd] *= 2.0 ** 70
+    h = x.cpu().double().numpy()
+    got, _ = pd.rms_norm_backward(g, x, w, EPS, dh=dh)
+    assert torch.equal(got[~odd], want[~odd])
+    wdx, _, size, _ = rn.backward(g.cpu().double().numpy(), h, w.cpu().double().numpy(), EPS, dh.cpu().double().numpy())
+    assert (np.abs(got.cpu().double().numpy() - wdx) <= 129 * U * size).all()
+    x[odd] = float("nan")
+    got, _ = pd.rms_norm_backward(g, x, w, EPS, dh=dh)
+    assert torch.equal(got[~odd], want[~odd]) and got[odd].isnan().all()
+
+
 @pytest.mark.parametrize("cols", [48, 500, 3000])
 def test_rows_of_zeros_infinities_and_nan(pd, cols):
     x = torch.ones(6, cols)
@@ -239,7 +258,7 @@ def test_rows_of_zeros_infinities_and_nan(pd, cols):
 
 
 def test_in_place(pd):
-    for cols in (100, 700, 9000):
+    for cols in (100, 700, 9000, 20000, 32768):
         x, _ = values(5, cols, 51, "bf16")
         r, _ = values(5, cols, 52, "bf16")
         w, _ = weights(cols, 53, "bf16")

@@ -34,6 +34,11 @@ transposed once into such rows:
     scales = torch.empty(K // 32, (rows + 15) // 16 * 16, dtype=torch.uint8, device="cuda")[:, :rows]
     scales.copy_(by_row.t())
 
+Around the products: rms_norm, rms_norm_i8 (whose codes and scales are the A and scale_a of
+gemm_i8_dequant) and rms_norm_backward; gemm_a16_i4, 16-bit activations times INT4 weights with
+scales by group, (ceil(K/group), N); moe_route and moe_a16_i4, a mixture-of-experts layer of
+such weights.
+
 No call here records a graph: a result carries no gradient, whatever its inputs ask for.
 A layer that trains computes dX and dW by calls of its own (see mxf4_quantize_both), for
 example from a torch.autograd.Function.

@@ -46,7 +46,9 @@ __device__ __forceinline__ void store_as(void *C, int type, int64_t at, const fl
 }
 
 // Few rows: a tile of RA rows and 16 NT columns of C to a workgroup, K split over its W waves,
-// whose sums meet in LDS and are added in wave order.
+// whose sums meet in LDS and are added in wave order.  The stream of the codes bounds it: one row of
+// bf16 against 8192 x 8192 in groups of 128 takes 8.3 us, 34.6 MB at 4.1 TB/s with the launch's start and end
+// (loads alone, of the same codes, 7), 16 rows 11.3, one row against 4096 x 4096 4.3.
 template <int T, int RA, int NT, int W, int Q, bool kS32, bool kAhead>
 __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -115,6 +117,12 @@ __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+// Chunk c (16 bytes) of row r of a step of activations lies at c ^ turn_of(r).  The LDS takes a wave's 16-byte reads in
+// four turns of 16 lanes, of which four by four rows have the same lane group g and the others the next one,
+// whose chunk differs by 1 or 4: the turns keep all sixteen in different banks for either (r % 8 in its place: 2048 x
+// 8192 x 8192 3 to 6% slower).
+__device__ __forceinline__ int turn_of(int r) { return (r & 3) | (r >> 1 & 4) | ((r << 1 ^ r) & 8); }
+
 // More rows: a tile of 16 MT rows to a workgroup, whose W waves have 16 NT columns each, so that a
 // code is converted once per tile.  Activations go through LDS, a step of 128 values of K at a time
 // and two deep, for all waves; codes are loaded whole lines to four lanes, a unit of 256 values ahead,
@@ -125,7 +133,7 @@ __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
 // 7 of 19 us with 16 splits and G = 1, so G is 4 and 2 for the tiles of few rows (14.4 us).
 // Up to some hundred rows the stream of codes bounds it, past that the vector unit: a code takes an
 // instruction and a half, and each sum of a scale's values a multiply-add beside the matrix
-// instructions.  2048 x 8192 x 8192 in groups of 128: 270 us, 1018 TFLOP/s; of 64: 381 us.
+// instructions.  2048 x 8192 x 8192 in groups of 128: 265 to 271 us, 1.02 PFLOP/s; of 64: 381 us.
 template <int T, int MT, int NT, int W, int G, int Q, bool kS32>
 __global__ __launch_bounds__(G *W *kWave) void a16_i4_tile_kernel(A16I4Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -187,7 +195,7 @@ __global__ __launch_bounds__(G *W *kWave) void a16_i4_tile_kernel(A16I4Args args
 #pragma unroll
         for (int j = 0; j < kX; ++j) {
             const int row = (tid + j * kThreads) / 16;
-            lds.xs[group][step & 1][row][(tid % 16) ^ (row % 8)] = xr[j];
+            lds.xs[group][step & 1][row][(tid % 16) ^ turn_of(row)] = xr[j];
         }
     };
     struct Codes {
@@ -266,7 +274,7 @@ __global__ __launch_bounds__(G *W *kWave) void a16_i4_tile_kernel(A16I4Args args
                     for (int i = 0; i < kRows; ++i)
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            x[i][u] = lds.xs[group][h][16 * (i0 + i) + r][position<Q>(u, g) ^ (r % 8)];
+                            x[i][u] = lds.xs[group][h][16 * (i0 + i) + r][position<Q>(u, g) ^ turn_of(r)];
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -413,7 +421,7 @@ int splits_of(int cfg, int64_t M, int64_t N, int64_t K) {
 // that, the least of a model of time: rounds of the CUs, each K / S values at a configuration's rate (us for
 // 1000 values of K), and where K is split the second launch and what the splits write and read.  Its
 // constants are fitted to all configurations' times at 88 shapes, 20 to 2048 rows against 1024 x 4096 to 14336 x
-// 8192 in groups of 64 and 128: it takes the fastest in 84 of them, and one within 3% of it in the others.
+// 8192 in groups of 64 and 128: it takes the fastest in 81 of them, and one within 6% of it in the others.
 int pick_a16_i4(int64_t M, int64_t N, int64_t K, int64_t group) {
     if (M <= 2) return tiles_n(1, N) >= 256 ? 1 : 0;
     if (M <= 8) return tiles_n(3, N) >= 256 ? 3 : 2;

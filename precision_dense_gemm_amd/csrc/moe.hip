@@ -27,7 +27,8 @@ struct RouteArgs {
 };
 
 // A wave per token, V logits to a lane.  Logits are compared as whole numbers in their order,
-// NaN above all; -infinity is 0, which is never taken.
+// NaN above all; -infinity is 0, which is never taken.  One maximum over the lanes for each slot, one after the
+// other, bounds it: 8 of 128 take 4.6 us (the shortest kernel here 2.3).
 template <int V>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -96,7 +97,10 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs args) {
 // activations of every pair, times its weight, in 16 bits: a row of `act` per pair.  The second adds
 // the experts up: 16 columns of y to a workgroup, whose waves share out all (expert, line of
 // its rows), each with sums of its own for every token, so no sum leaves the workgroup and
-// their order is fixed.
+// their order is fixed.  Both read an expert's codes once (once for RA of its pairs), and their stream
+// bounds them: 16 tokens through 8 of 128 experts (H 2048, I 768, f16, groups of 64), 206 MB of codes and
+// scales, take 73 us with the routing, 37 to 41 for the first kernel (its loads alone: 29 to 31) and 29 for the
+// second (21 to 22); one token through 4 of 32 (H 4096, I 2048, bf16, groups of 128), 52 MB, 24.
 
 struct MoeArgs {
     const uint8_t *x;

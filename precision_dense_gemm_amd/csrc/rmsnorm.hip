@@ -321,10 +321,10 @@ __global__ __launch_bounds__(1024, 4) void rms_norm_backward_kernel(GradArgs arg
         }
         // (two parts in turn: a wave writes the next row's while another reads this one's)
         over_row<kLanes>(ss, dot, part[turn & 1], first_wave, waves);
-        float mean;        // of g n
+        float mean = 0;    // of g n
         Inverse f = {1.0f, 1.0f};
         const float e = ss / (float)args.cols + args.eps;
-        float r;
+        float r = 0;
         const bool fine = in_range(ss, e) && fabsf(dot) <= 0x1p126f;
         if (fine) {
             r = f.r = 1.0f / sqrtf(e);

@@ -555,10 +555,15 @@ int pdgemm_moe_route(int64_t T, int64_t E, int64_t top, const void *logits, int6
  * multiple of 32.  H and I are any length, E <= 1024, top <= 64, T * top <= 4096,
  * T * ldx * 2 and T * top * (2 I + 16) below 2^31 (PDGEMM_EINVAL_DIM, for ldx
  * PDGEMM_EINVAL_LD).  The codes enter exactly and sums are binary32 in a fixed order;
- * silu(..) * (..), times the pair's weight, is rounded to `type` as the second
- * product's operand, and y once.  The workspace (16-byte aligned) is undefined on
+ * y is rounded once.  silu(..) * (..), times the pair's weight, passes from the one product
+ * to the other through the workspace (16-byte aligned).  In one of at least
+ * pdgemm_moe_a16_i4_wide_workspace_size() bytes it is the sum of two bf16 values: in
+ * binary32's range, and within 2^-16 of its value.  In one of at least
+ * pdgemm_moe_a16_i4_workspace_size() bytes it is rounded to `type`: an f16 one above 65504
+ * becomes infinite, and y's error grows by about 1.4.  The workspace is undefined on
  * return; calls that overlap, and graphs that may run at once, need one each. */
 int64_t pdgemm_moe_a16_i4_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top);
+int64_t pdgemm_moe_a16_i4_wide_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top);
 int pdgemm_moe_a16_i4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, const void *x, int64_t ldx, int type,
                       const int32_t *ids, const float *weights, const uint8_t *w13, int64_t ld13, int64_t expert13,
                       const void *s13, int64_t lds13, int64_t expert_s13, const uint8_t *w2, int64_t ld2,

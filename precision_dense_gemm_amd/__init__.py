@@ -168,6 +168,8 @@ lib.pdgemm_moe_route.argtypes = [_i64, _i64, _i64, _p, _i64, _i, _i, _p, _p, _p]
 lib.pdgemm_moe_route.restype = _i
 lib.pdgemm_moe_a16_i4_workspace_size.argtypes = [_i64] * 5
 lib.pdgemm_moe_a16_i4_workspace_size.restype = _i64
+lib.pdgemm_moe_a16_i4_wide_workspace_size.argtypes = [_i64] * 5
+lib.pdgemm_moe_a16_i4_wide_workspace_size.restype = _i64
 lib.pdgemm_moe_a16_i4.argtypes = ([_i64] * 5 + [_p, _i64, _i, _p, _p] + [_p, _i64, _i64] * 4
                                   + [_i, _i64, _p, _i64, _p, _i64, _p])
 lib.pdgemm_moe_a16_i4.restype = _i
@@ -1097,9 +1099,12 @@ def _moe_weights(codes, scales, E: int, N: int, K: int, group: int, name: str):
     return codes.data_ptr(), 2 * ld, 2 * e, scales.data_ptr(), lds, es
 
 
+_EWORKSPACE = -7   # PDGEMM_EWORKSPACE
+
+
 def moe_a16_i4_workspace_size(T: int, H: int, I: int, E: int, top_k: int) -> int:
     """Bytes of workspace moe_a16_i4 needs."""
-    return lib.pdgemm_moe_a16_i4_workspace_size(T, H, I, E, top_k)
+    return lib.pdgemm_moe_a16_i4_wide_workspace_size(T, H, I, E, top_k)
 
 
 def moe_a16_i4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor,
@@ -1110,7 +1115,8 @@ def moe_a16_i4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: t
     x (T, H) float16 or bfloat16, rows of a multiple of 16 bytes; ids int32 and weights float32 (T, top_k), as moe_route
     makes them; INT4 weights of E experts: w13 (E, 2 I, ceil(H/2)), the gate's rows and then the up projection's, w2
     (E, H, ceil(I/2)), and their scales s13 (E, ceil(H/group), 2 I), s2 (E, ceil(I/group), H), both of one type.  An id
-    outside 0 .. E - 1 adds nothing.  workspace: moe_a16_i4_workspace_size bytes, not shared by calls that overlap."""
+    outside 0 .. E - 1 adds nothing.  The gated activations keep binary32's range, to 2^-16 of a value.  workspace:
+    moe_a16_i4_workspace_size bytes, not shared by calls that overlap."""
     if x.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("moe_a16_i4 takes a float16 or bfloat16 x")
     T, H, ldx = _mx_rows(x, "x")
@@ -1132,12 +1138,15 @@ def moe_a16_i4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: t
     if out is not None and out.dtype is not x.dtype:
         raise TypeError("out must be of x's type")
     out, ldy, kind = _mx_dense_out(out, T, H, x.dtype, x.device, stream)
+    need = lib.pdgemm_moe_a16_i4_wide_workspace_size(T, H, I, E, top)
     if workspace is None:
-        ws_bytes = max(lib.pdgemm_moe_a16_i4_workspace_size(T, H, I, E, top), 16)
+        ws_bytes = max(need, 16)
         workspace = _new_vector(ws_bytes, torch.uint8, x.device, stream)
         ws = workspace.data_ptr()
     else:
         ws, ws_bytes = _workspace(workspace, x.device)
+        if ws_bytes < need:   # (the C call takes less, and rounds what it keeps there to x's type)
+            raise PdgemmError(_EWORKSPACE)
     _mx_call(lib.pdgemm_moe_a16_i4, (T, H, I, E, top, x.data_ptr(), ldx, kind, ids.data_ptr(), weights.data_ptr(), *first,
                                      *second, skind, group, out.data_ptr(), ldy, ws, ws_bytes),
              (x, ids, weights, w13, s13, w2, s2, out), stream)

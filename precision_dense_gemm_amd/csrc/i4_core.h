@@ -189,6 +189,7 @@ struct I4Scales {
 template <int kX, int NT, int NB>
 struct I4Source {
     const uint8_t *a;          // activations; K values a row
+    const uint8_t *a2;         // kParts 2: their second parts (kDirect: xa takes a lane to its part)
     int a_end;                 // bytes that may be read
     uint32_t xa[kX];
     const uint8_t *b[NB];      // codes
@@ -218,11 +219,13 @@ struct I4Groups {
 // 8192 took 12.1 us and not 10.9.)  RA rows of activations: 2, 8 or 16; a fragment's further rows repeat
 // them.  With RA = 2 there is little but the codes, and they do go straight to their lanes (kDirect): one row
 // against 8192 x 8192 takes 8.3 us so, and 9.5 through LDS.  Q: blocks that share a scale (4: groups of whole steps, 2: of multiples of 64 values, 1: any).
-// kS32: binary32 scales.  kAhead: see run.
-template <int T, int RA, int NT, int NB, int Q, bool kS32, bool kAhead>
+// kS32: binary32 scales.  kAhead: see run.  kParts 2: activation row p is the sum of rows 2 p and 2 p + 1 of the RA,
+// whose sums the caller adds.
+template <int T, int RA, int NT, int NB, int Q, bool kS32, bool kAhead, int kParts = 1>
 struct I4Wave {
     static constexpr int kSc = 4 / Q;                 // scales per step
     static constexpr bool kDirect = RA == 2;
+    static constexpr int kRows = RA / kParts;         // activations' rows
     static constexpr int kX = kDirect ? 1 : RA / 4;   // loads of four rows of a step of activations (two of a unit)
     static constexpr int kXs = kDirect ? 1 : 2;       // ... each for every step
     static constexpr int kRun = kDirect ? 32 : 16;    // chunks of a row of x
@@ -244,8 +247,13 @@ struct I4Wave {
     };
     floatx4_t acc[NT];
 
-    // row of activations that this lane copies in load j, and its 16 bytes of the run
-    static __device__ __forceinline__ int copied_row(int j) { return kWave / kRun * j + (threadIdx.x % kWave) / kRun; }
+    // which of the RA rows this lane copies in load j (two parts: four rows of one of them to a load), and its 16
+    // bytes of the run
+    static __device__ __forceinline__ int copied_row(int j) {
+        const int sub = (threadIdx.x % kWave) / kRun;
+        if constexpr (kParts == 1 || kDirect) return kWave / kRun * j + sub;
+        return 2 * (kWave / kRun * (j % (kX / 2)) + sub) + j / (kX / 2);
+    }
     static __device__ __forceinline__ int copied_chunk() { return threadIdx.x % kRun; }
     // and of a fragment of codes
     static __device__ __forceinline__ int code_row() { return kDirect ? threadIdx.x % 16 : threadIdx.x % kWave / 4; }
@@ -261,9 +269,9 @@ struct I4Wave {
             st.b[t][0] = load16(rb, src.vb[t], unit * 128);
             st.b[t][1] = load16(rb, src.vb[t] + 64, unit * 128);
         }
-        const auto ra = rsrc(src.a, src.a_end);
 #pragma unroll
         for (int j = 0; j < kX; ++j) {
+            const auto ra = rsrc(kParts == 2 && !kDirect && j >= kX / 2 ? src.a2 : src.a, src.a_end);
             st.x[j][0] = load16(ra, src.xa[j], unit * 512);
             if constexpr (!kDirect) st.x[j][1] = load16(ra, src.xa[j] + 256, unit * 512);
         }

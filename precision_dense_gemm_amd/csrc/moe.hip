@@ -94,7 +94,11 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs args) {
 //
 // A pair is a token and one of its slots, p = t * top + s; an expert that a token names twice is
 // computed for the first of the slots, with the weights' sum.  The first kernel computes the gated
-// activations of every pair, times its weight, in 16 bits: a row of `act` per pair.  The second adds
+// activations of every pair, times its weight: a row of `act` per pair, which the second product's matrix
+// instructions take in 16 bits.  A value of two bf16 parts (wide) keeps binary32's range and is within 2^-16 of
+// itself, a 32nd of the rounding of an f16 y; rounded to x's type it would add an error as large as y's own
+// rounding, and in f16 end at 65504.  The parts are two rows of one matrix instruction, which few pairs leave
+// room for.  Where the caller's workspace holds one part only, it is of x's type.  The second kernel adds
 // the experts up: 16 columns of y to a workgroup, whose waves share out all (expert, line of
 // its rows), each with sums of its own for every token, so no sum leaves the workgroup and
 // their order is fixed.  Both read an expert's codes once (once for RA of its pairs), and their stream
@@ -109,6 +113,7 @@ struct MoeArgs {
     const uint8_t *w13, *w2;
     const uint8_t *s13, *s2;
     uint8_t *act;
+    int64_t act2;           // bytes from a value to its second part (0: one part)
     int32_t *active;        // how many experts have a token, and which
     int32_t *offset;        // where the pairs of each of them begin in `order`, and their end
     uint16_t *order;        // the pairs by expert
@@ -119,6 +124,7 @@ struct MoeArgs {
     int64_t lds13, es13, lds2, es2;     // bytes
     int64_t ldy;            // elements
     int T, H, I, E, top;
+    int type;               // of x and y
     int most;               // of active experts
     int tiles;              // workgroups along an expert's rows
     int wk;                 // waves that share a tile's K
@@ -317,23 +323,41 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up_kernel(MoeArgs args) {
             const int at = first + 4 * g + k;
             if (4 * g + k >= RA || at >= rows) break;
             const float gate = w.acc[0][k], up = w.acc[1][k];
-            // (rounded to the type that the second product's matrix instructions take)
-            reinterpret_cast<Elem *>(args.act + (int64_t)own[at] * args.ldact)[i0 + r] =
-                (Elem)(gate / (1.0f + __expf(-gate)) * up * own_weight[at]);
+            const float v = gate / (1.0f + __expf(-gate)) * up * own_weight[at];
+            uint8_t *const row = args.act + (int64_t)own[at] * args.ldact;
+            if (args.act2) {
+                // (the first part of the largest finite values is cut off: rounded, it would be infinite)
+                const float most = __builtin_copysignf(0x1.FEp127f, v);
+                const bool finite = v * 0.0f == 0.0f;
+                const __bf16 one = (__bf16)(finite && __builtin_fabsf(v) > 0x1.FEp127f ? most : v);
+                reinterpret_cast<__bf16 *>(row)[i0 + r] = one;
+                reinterpret_cast<__bf16 *>(row + args.act2)[i0 + r] = (__bf16)(finite ? v - (float)one : 0.0f);
+            } else {
+                reinterpret_cast<Elem *>(row)[i0 + r] = (Elem)v;
+            }
         }
     }
 #endif  // __HIP_DEVICE_COMPILE__
+}
+
+__device__ __forceinline__ void store_y(const MoeArgs &args, int t, int col, float v) {
+    uint16_t *const at = reinterpret_cast<uint16_t *>(args.y) + (int64_t)t * args.ldy + col;
+    if (args.type == kF16)
+        *reinterpret_cast<_Float16 *>(at) = (_Float16)v;
+    else
+        *reinterpret_cast<__bf16 *>(at) = (__bf16)v;
 }
 
 // 16 columns of y for TT tokens.  Where there are few such tiles, args.splits workgroups share
 // the (expert, line) pairs of one, and their sums are added up by moe_join_kernel.  (With the last of them to
 // finish adding up what the others wrote, ordered by fences of the device's scope, 16 tokens through 8 of 128
 // experts took 180 us instead of 50: such a fence writes back and drops a whole L2.)
-template <int T, int RA, int TT, int W, int Q, bool kS32, bool kAhead>
+// T: the activations' type, kParts of them to a value.
+template <int T, int RA, int TT, int W, int Q, bool kS32, bool kAhead, int kParts>
 __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    using Elem = typename ElemOf<T>::type;
-    using Wave = I4Wave<T, RA, 1, 1, Q, kS32, kAhead>;
+    using Wave = I4Wave<T, RA, 1, 1, Q, kS32, kAhead, kParts>;
+    constexpr int kPairs = Wave::kRows;   // at a time
     __shared__ int expert[kMaxExperts], offset[kMaxExperts + 1];
     __shared__ uint16_t pair[kMaxPairs], token[kMaxPairs];
     __shared__ typename Wave::Lds own[W];
@@ -361,14 +385,16 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 
     const int cols = min(16, H - n0), size = kS32 ? 4 : 2;
     typename Wave::Source src;
-    src.a = args.act;
-    src.a_end = (int)((args.T * args.top - 1) * args.ldact) + ((2 * I + 15) & ~15);
+    src.a = args.act, src.a2 = args.act + args.act2;
+    // (a lane of kDirect has a part of its own: both are below 2^31 where T <= 2)
+    const uint32_t second = kParts == 2 && Wave::kDirect ? (uint32_t)args.act2 : 0u;
+    src.a_end = (int)second + (int)((args.T * args.top - 1) * args.ldact) + ((2 * I + 15) & ~15);
     src.b_end[0] = (int)((cols - 1) * args.ld2) + (((I + 1) / 2 + 15) & ~15);
     src.vb[0] = Wave::code_row() < cols ? (uint32_t)Wave::code_row() * (uint32_t)args.ld2 + 16 * Wave::code_chunk() : kOutside;
     src.vs[0] = (uint32_t)min(r, cols - 1) * size;
     src.K = I, src.group_magic = args.group_magic, src.groups = (I + args.group - 1) / args.group;
-    // (expert, line) number i is wave i's of the splits' waves, round and round; an expert of more than RA
-    // pairs takes a turn for every RA
+    // (expert, line) number i is wave i's of the splits' waves, round and round; an expert of more than kPairs
+    // pairs takes a turn for every kPairs
     const int lines = (I + 2 * kStep - 1) / (2 * kStep);
     const int stride = W * args.splits, by_expert = stride / lines, by_line = stride % lines;
     int at = (split * W + wave) / lines, line = (split * W + wave) % lines, first = 0;
@@ -380,17 +406,18 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
             const int e = __builtin_amdgcn_readfirstlane(expert[at]);
             const int from = __builtin_amdgcn_readfirstlane(offset[at]), to = __builtin_amdgcn_readfirstlane(offset[at + 1]);
             st.tag = from + first;
-            st.left = min(to - st.tag, RA);
+            st.left = min(to - st.tag, kPairs);
             src.b[0] = args.w2 + e * args.e2 + (int64_t)n0 * args.ld2;
             src.s[0] = {args.s2 + e * args.es2 + (int64_t)n0 * size, args.lds2, args.s_half};
 #pragma unroll
             for (int j = 0; j < Wave::kX; ++j) {
-                const int row = Wave::copied_row(j), i = st.tag + min(row, st.left - 1);
+                const int row = Wave::copied_row(j) / kParts, i = st.tag + min(row, st.left - 1);
                 const bool in = row < st.left && (uint32_t)(token[i] - t0) < (uint32_t)TT;
                 src.xa[j] = in ? (uint32_t)pair[i] * (uint32_t)args.ldact + 16 * Wave::copied_chunk() : kOutside;
+                if (Wave::copied_row(j) % kParts == 1) src.xa[j] += second;
             }
             const int unit = line;
-            first += RA;
+            first += kPairs;
             if (from + first >= to) {
                 first = 0, at += by_expert, line += by_line;
                 if (line >= lines) line -= lines, ++at;
@@ -400,10 +427,11 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
         [&](auto &st) {
             // a token has one pair of an expert: the lanes add to different sums
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int row = 4 * g + k;
+            for (int k = 0; k < 4; k += kParts) {
+                const int row = (4 * g + k) / kParts;
                 const int t = token[st.tag + min(row, st.left - 1)] - t0;
-                if (row < st.left && (uint32_t)t < (uint32_t)TT) sums[wave][t][r] += w.acc[0][k];
+                const float sum = kParts == 1 ? w.acc[0][k] : w.acc[0][k] + w.acc[0][k + kParts - 1];
+                if (row < st.left && (uint32_t)t < (uint32_t)TT) sums[wave][t][r] += sum;
             }
             wave_lds_order();
             w.clear();
@@ -416,7 +444,7 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 #pragma unroll
         for (int v = 1; v < W; ++v) sum += sums[v][t][col];
         if (args.splits == 1)
-            reinterpret_cast<Elem *>(args.y)[(int64_t)(t0 + t) * args.ldy + n0 + col] = (Elem)sum;
+            store_y(args, t0 + t, n0 + col, sum);
         else
             args.part[((int64_t)split * args.T + t0 + t) * H + n0 + col] = sum;
     }
@@ -424,10 +452,8 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 }
 
 // y from the splits' sums, added in their order.
-template <int T>
 __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    using Elem = typename ElemOf<T>::type;
     const int x = blockIdx.x * 256 + threadIdx.x, t = x / args.H, col = x % args.H;
     if (t >= args.T) return;
     float v[kMaxSplits], sum = 0;
@@ -436,7 +462,7 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs args) {
 #pragma unroll
     for (int k = 0; k < kMaxSplits; ++k)
         if (k < args.splits) sum += v[k];
-    reinterpret_cast<Elem *>(args.y)[(int64_t)t * args.ldy + col] = (Elem)sum;
+    store_y(args, t, col, sum);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -454,19 +480,21 @@ int splits_of(int64_t T, int64_t H, int64_t most) {
     return s < 2 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
 }
 
-// The workspace: act, the active experts, their offsets, the order of pairs, the splits' sums
+// The workspace: act (its parts one after the other), the active experts, their offsets, the order of pairs, the
+// splits' sums
 struct Workspace {
-    int64_t ldact, active, offset, order, part, bytes;   // bytes: a row of act; where the others begin; in all
+    int64_t ldact, act2, active, offset, order, part, bytes;   // bytes: a row of act; where the others begin; in all
     int most, splits;
 };
-Workspace workspace_of(int64_t T, int64_t top, int64_t H, int64_t I, int64_t E) {
+Workspace workspace_of(int64_t T, int64_t top, int64_t H, int64_t I, int64_t E, int parts) {
     const int64_t pairs = T * top;
     Workspace w;
     w.most = (int)(E < pairs ? E : pairs);
     w.splits = splits_of(T, H, w.most);
     const int64_t list = round_up(4 * (1 + w.most), 16);
     w.ldact = round_up(2 * I, 16);
-    w.active = pairs * w.ldact;
+    w.act2 = (parts - 1) * pairs * w.ldact;
+    w.active = w.act2 + pairs * w.ldact;
     w.offset = w.active + list;
     w.order = w.offset + list;
     w.part = w.order + round_up(2 * pairs, 16);
@@ -478,6 +506,17 @@ bool moe_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top) {
     const int64_t row = kMaxRowBytes;
     return T >= 0 && H > 0 && I > 0 && E > 0 && E <= kMaxExperts && top > 0 && top <= kMaxTop && T <= kMaxPairs / top &&
            H <= row / 2 && I <= row / 2 && T * top * (2 * I + 16) <= INT32_MAX;
+}
+
+template <int T, int RA, int Q, bool kS32, int kParts>
+int launch_down(MoeArgs &args, void *stream) {
+    constexpr bool kAhead = true;
+    constexpr int W = RA == 2 ? 16 : 8;   // (as registers and LDS allow)
+    const int64_t blocks = y_tiles(args.T, args.H) * args.splits;
+    return args.T <= 16 ? run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 16, W, Q, kS32, kAhead, kParts>), blocks,
+                              W * kWave, &args, stream)
+                        : run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 64, 8, Q, kS32, kAhead, kParts>), blocks, 512,
+                              &args, stream);
 }
 
 template <int T, int RA, int Q, bool kS32>
@@ -496,14 +535,15 @@ int launch_moe(MoeArgs args, void *stream) {
                                     8 * args.T * args.top + 6 * args.T, s), s);
     if (rc != PDGEMM_OK) return rc;
     args.tiles = (int)cdiv(args.H, 16);
-    constexpr int W = RA == 2 ? 16 : 8;   // (as registers and LDS allow)
-    const int64_t blocks = y_tiles(args.T, args.H) * args.splits;
-    rc = args.T <= 16 ? run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 16, W, Q, kS32, kAhead>), blocks, W * kWave,
-                            &args, stream)
-                      : run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 64, 8, Q, kS32, kAhead>), blocks, 512, &args,
-                            stream);
+    // Of two parts, 1, 4 or 8 pairs at a time.  The layer, us, with 4 and with 8: experts of 2 pairs on average
+    // (128 experts, H 2048, I 768, groups of 64) 90 and 96, of 3 104 and 105, of 4 123 and 118; (64, 2048, 1024, 128) 66 and
+    // 70, 75 and 75, 85 and 82.  Two tokens (H 4096, I 2048) with 1 and with 4: of 32 experts 30 and 32, of 4 22 and 21.
+    rc = args.act2 == 0                        ? launch_down<T, RA, Q, kS32, 1>(args, stream)
+         : args.T <= 2                         ? launch_down<kBF16, 2, Q, kS32, 2>(args, stream)
+         : args.T * args.top <= 3 * args.most ? launch_down<kBF16, 8, Q, kS32, 2>(args, stream)
+                                               : launch_down<kBF16, 16, Q, kS32, 2>(args, stream);
     if (rc != PDGEMM_OK || args.splits == 1) return rc;
-    return run(reinterpret_cast<const void *>(&moe_join_kernel<T>), cdiv((int64_t)args.T * args.H, 256), 256, &args, stream);
+    return run(reinterpret_cast<const void *>(&moe_join_kernel), cdiv((int64_t)args.T * args.H, 256), 256, &args, stream);
 }
 // Pairs that an expert's rows of codes are read for at once
 template <int T, int Q, bool kS32>
@@ -556,7 +596,11 @@ int pdgemm_moe_route(int64_t T, int64_t E, int64_t top, const void *logits, int6
 }
 
 int64_t pdgemm_moe_a16_i4_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top) {
-    return moe_sizes_ok(T, H, I, E, top) && T > 0 ? workspace_of(T, top, H, I, E).bytes : 0;
+    return moe_sizes_ok(T, H, I, E, top) && T > 0 ? workspace_of(T, top, H, I, E, 1).bytes : 0;
+}
+
+int64_t pdgemm_moe_a16_i4_wide_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top) {
+    return moe_sizes_ok(T, H, I, E, top) && T > 0 ? workspace_of(T, top, H, I, E, 2).bytes : 0;
 }
 
 int pdgemm_moe_a16_i4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, const void *x, int64_t ldx, int type,
@@ -581,16 +625,17 @@ int pdgemm_moe_a16_i4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, c
     if (rc == PDGEMM_OK && T * ldx * 2 > INT32_MAX) rc = PDGEMM_EINVAL_LD;
     if (rc == PDGEMM_OK && (ldx % 8 || ((uintptr_t)x & 15))) rc = PDGEMM_EALIGN;
     if (rc == PDGEMM_OK && !workspace) rc = PDGEMM_ENULL;
-    const Workspace w = workspace_of(T, top, H, I, E);
+    const Workspace wide = workspace_of(T, top, H, I, E, 2);
+    const Workspace w = workspace_bytes >= wide.bytes ? wide : workspace_of(T, top, H, I, E, 1);
     if (rc == PDGEMM_OK && (workspace_bytes < w.bytes || ((uintptr_t)workspace & 15))) rc = PDGEMM_EWORKSPACE;
     if (rc != PDGEMM_OK) return rc;
     uint8_t *const ws = static_cast<uint8_t *>(workspace);
     const int size = elem_size(scale_type);
     const MoeArgs args = {static_cast<const uint8_t *>(x), ids, weights, w13, w2, static_cast<const uint8_t *>(s13),
-                          static_cast<const uint8_t *>(s2), ws, reinterpret_cast<int32_t *>(ws + w.active),
+                          static_cast<const uint8_t *>(s2), ws, w.act2, reinterpret_cast<int32_t *>(ws + w.active),
                           reinterpret_cast<int32_t *>(ws + w.offset), reinterpret_cast<uint16_t *>(ws + w.order), reinterpret_cast<float *>(ws + w.part), static_cast<uint8_t *>(y), 2 * ldx, w.ldact, ld13 / 2,
                           expert13 / 2, ld2 / 2, expert2 / 2, lds13 * size, expert_s13 * size, lds2 * size, expert_s2 * size, ldy,
-                          (int)T, (int)H, (int)I, (int)E, (int)top, w.most, 0, 1, w.splits, (int)group,
+                          (int)T, (int)H, (int)I, (int)E, (int)top, type, w.most, 0, 1, w.splits, (int)group,
                           scale_type == kF16 ? ~0u : 0u, I4Groups::magic(group)};
     const bool s32 = scale_type == kF32;
     if (type == kF16) return s32 ? launch_moe<kF16, true>(args, stream) : launch_moe<kF16, false>(args, stream);

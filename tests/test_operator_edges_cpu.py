@@ -1,0 +1,27 @@
+"""CPU checks of size queries and choices of the norm, INT4-weight and expert operators at the ends of their ranges."""
+from __future__ import annotations
+
+import os
+
+import pytest
+
+from tests.test_abi_cpu import LIB
+
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libpdgemm.so not built")
+
+
+@pytest.fixture(scope="module")
+def pd():
+    pytest.importorskip("torch")
+    import precision_dense_gemm_amd as pd
+    return pd
+
+
+def test_the_wide_workspace_holds_the_activations_twice(pd):
+    for T, H, I, E, top in [(1, 1, 1, 1, 1), (5, 96, 60, 8, 2), (16, 2048, 768, 128, 8), (4096, 8, 100, 3, 1), (64, 64, 2 ** 16, 1024, 64)]:
+        least = pd.lib.pdgemm_moe_a16_i4_workspace_size(T, H, I, E, top)
+        wide = pd.lib.pdgemm_moe_a16_i4_wide_workspace_size(T, H, I, E, top)
+        assert least > 0 and wide == least + T * top * ((2 * I + 15) // 16 * 16)
+        assert pd.moe_a16_i4_workspace_size(T, H, I, E, top) == wide
+    for sizes in [(0, 96, 64, 8, 2), (-1, 96, 64, 8, 2), (5, 96, 64, 2000, 2), (5, 0, 64, 8, 2), (5, 96, 64, 8, 0), (5, 96, 64, 8, 65)]:
+        assert pd.lib.pdgemm_moe_a16_i4_wide_workspace_size(*sizes) == 0

@@ -518,7 +518,8 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
  * _cfg takes an explicit tile configuration (0 <= cfg <
  * pdgemm_a16_i4_num_configs(), any shape; the last one groups of a multiple of 128 only)
  * and the workspace of
- * _cfg_workspace_size; _pick is the one gemm_a16_i4 takes. */
+ * _cfg_workspace_size; _pick is the one gemm_a16_i4 takes (0 for sizes that are empty or that
+ * it refuses). */
 int64_t pdgemm_a16_i4_workspace_size(int64_t M, int64_t N, int64_t K, int64_t group);
 int gemm_a16_i4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                 int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc,

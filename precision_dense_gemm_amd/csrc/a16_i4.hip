@@ -526,6 +526,9 @@ int pdgemm_a16_i4_cfg(int cfg, int64_t M, int64_t N, int64_t K, const void *A, i
 
 int pdgemm_a16_i4_num_configs(void) { return kNumConfigs; }
 
-int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K, int64_t group) { return pick_a16_i4(M, N, K, group); }
+int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K, int64_t group) {
+    // (with no tiles there is nothing to choose by)
+    return sizes_ok(M, N, K) && M > 0 && N > 0 ? pick_a16_i4(M, N, K, group) : 0;
+}
 
 }  // extern "C"

@@ -25,3 +25,17 @@ def test_the_wide_workspace_holds_the_activations_twice(pd):
         assert pd.moe_a16_i4_workspace_size(T, H, I, E, top) == wide
     for sizes in [(0, 96, 64, 8, 2), (-1, 96, 64, 8, 2), (5, 96, 64, 2000, 2), (5, 0, 64, 8, 2), (5, 96, 64, 8, 0), (5, 96, 64, 8, 65)]:
         assert pd.lib.pdgemm_moe_a16_i4_wide_workspace_size(*sizes) == 0
+
+
+def test_a_choice_for_empty_and_refused_sizes(pd):
+    """(a quotient by their tiles would end the process)"""
+    for M in (-2 ** 62, -33, -1, 0, 1, 16, 17, 32, 500, 2 ** 31 - 1, 2 ** 31, 2 ** 40, 2 ** 62):
+        for N in (-2 ** 62, -7, 0, 1, 4096, 2 ** 31 - 1, 2 ** 31, 2 ** 40, 2 ** 62):
+            for K in (-1, 0, 1, 8192, 2 ** 30, 2 ** 62):
+                for group in (-32, 0, 32, 128, 2 ** 62):
+                    c = pd.a16_i4_pick(M, N, K, group)
+                    assert 0 <= c < pd.a16_i4_num_configs(), (M, N, K, group)
+                    if M <= 0 or N <= 0 or K < 0 or max(M, N) >= 2 ** 31 or K > 2 ** 30:
+                        assert c == 0 and pd.a16_i4_workspace_size(M, N, K, group) == 0
+                    for cfg in (-1, 0, 8, 10, 11):
+                        assert pd.a16_i4_workspace_size(M, N, K, group, cfg) >= 0

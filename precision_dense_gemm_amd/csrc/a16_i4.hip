@@ -212,7 +212,7 @@ __global__ __launch_bounds__(G *W *kWave) void a16_i4_tile_kernel(A16I4Args args
         }
 #pragma unroll
         for (int u = 0; u < 2 * kSc; ++u) {
-            const int q = I4Groups::of(unit * 8 + u * Q, args.group_magic, groups);
+            const int q = I4Groups::of<Q>(unit * 8 + u * Q, args.group_magic, groups);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const uint8_t *const p = args.s.p + q * args.s.ld + vs[t];

@@ -202,13 +202,17 @@ struct I4Source {
     int groups;
 };
 
-// The group of a block of 32 values: block / (group / 32), by one multiplication.  A row of 16-bit
-// activations has at most 2^21 values, 2^16 blocks, so block * (group / 32) < 2^31 wherever there is
-// more than one group, and the quotient is exact (a last group's overshoot is cut).
+// The group of a block of 32 values: block / g with g = group / 32, by one multiplication with magic =
+// (2^32 + e) / g, 0 <= e < g.  A row of 16-bit activations has at most 2^21 values, 2^16 blocks, so that block * e <
+// 2^32 wherever there is more than one group, and what e adds, block * e / (2^32 g), is below the 1 / g that a quotient
+// lacks at least of the next one: it is exact (a last group's overshoot is cut).  2^32 itself, for g = 1, is passed as 0.
 struct I4Groups {
-    static uint32_t magic(int64_t group) { return (uint32_t)(((int64_t(1) << 31) + group / 32 - 1) / (group / 32)); }
+    static uint32_t magic(int64_t group) { return (uint32_t)(((int64_t(1) << 32) + group / 32 - 1) / (group / 32)); }
+    template <int Q>
     static __device__ __forceinline__ int of(int block, uint32_t magic, int groups) {
-        return min((int)__umulhi(2u * (uint32_t)block, magic), groups - 1);
+        int q = (int)__umulhi((uint32_t)block, magic);
+        if (Q == 1 && magic == 0) q = block;   // (groups of 64 values and more have another magic)
+        return min(q, groups - 1);
     }
 };
 
@@ -280,7 +284,7 @@ struct I4Wave {
             const int i = 4 * k + threadIdx.x % kWave / 16, block = unit * 8 + i * Q;
             // (scales past K are zeros: they may not be there)
             const bool in = i < 2 * kSc && block * kBlock < src.K;
-            const int64_t q = I4Groups::of(block, src.group_magic, src.groups);
+            const int64_t q = I4Groups::of<Q>(block, src.group_magic, src.groups);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 st.s[t][k] = 0;

@@ -457,7 +457,7 @@ int pdgemm_a16_mxf4_pick(int a_type, int64_t M, int64_t N, int64_t K);   /* -1 f
  * Section VI, leaves quantisation out).
  *
  * Every matrix is dense, row-major, with only its element's alignment and any
- * ld >= cols; a row has at most 32768 values.  type (PDGEMM_F32, _F16 or _BF16)
+ * ld >= cols; there are at most 2^30 rows, of at most 32768 values.  type (PDGEMM_F32, _F16 or _BF16)
  * is that of x, residual and sum; the weight, of cols values, and the result
  * have types of their own.  Errors, streams and ownership are those of the
  * other entry points; an unknown type, or an eps that is negative or not

@@ -139,6 +139,19 @@ int run(const void *fn, int64_t blocks, int threads, void *args, void *stream) {
     return finish(hipLaunchKernel(fn, dim3((unsigned)blocks), dim3((unsigned)threads), kargs, 0, s), s);
 }
 
+// The same of more work-items: in rows of `across` workgroups, which the kernel counts by block_of()
+int run_rows(const void *fn, int64_t blocks, int across, int threads, void *args, void *stream) {
+    void *kargs[] = {args};
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return finish(hipLaunchKernel(fn, dim3((unsigned)across, (unsigned)cdiv(blocks, across)), dim3((unsigned)threads), kargs, 0, s), s);
+}
+int blocks_across(int64_t blocks, int threads) {
+    const int64_t most = (int64_t(1) << 31) / threads;
+    return (int)(blocks < most ? blocks : most);
+}
+// (the last row's workgroups may pass the last block)
+__device__ __forceinline__ int block_of(int across) { return blockIdx.y * across + blockIdx.x; }
+
 bool known_type(int t) { return t == kF32 || t == kF16 || t == kBF16; }
 
 // rows of a dense matrix with only its element's alignment

@@ -19,6 +19,7 @@ struct NormArgs {
     float *scale;
     int64_t ldx, ldr, ldsum, ldo;   // elements
     int rows, cols;
+    int across;             // of block_of()
     int w_type;
     float eps;
 };
@@ -91,7 +92,8 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
 
     const int tid = threadIdx.x;
     const int step = kLanes ? kLanes : (int)blockDim.x, t = kLanes ? tid % (kLanes ? kLanes : 1) : tid;
-    const int row = kLanes ? blockIdx.x * (256 / (kLanes ? kLanes : 1)) + tid / (kLanes ? kLanes : 1) : blockIdx.x;
+    const int block = block_of(args.across);
+    const int row = kLanes ? block * (256 / (kLanes ? kLanes : 1)) + tid / (kLanes ? kLanes : 1) : block;
     const int cols = row < args.rows ? args.cols : 0;   // (lanes of no row take part in the sums' exchanges)
 
     Elem h[V][N];
@@ -515,12 +517,14 @@ int pdgemm_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int 
     if (rc == PDGEMM_OK) rc = check_plain(out, ldo, out_type);
     if (rc == PDGEMM_OK && out_type == kI8) rc = check_plain(scale, 1, kF32);
     if (rc != PDGEMM_OK) return rc;
-    NormArgs args = {x, residual, sum, weight, out, scale, ldx, ldr, lds, ldo, (int)rows, (int)cols, weight_type, eps};
     const Share s = share_of(cols, type);
+    const int64_t blocks = s.lanes ? cdiv(rows, 256 / s.lanes) : rows;
+    const int across = blocks_across(blocks, s.threads);
+    NormArgs args = {x, residual, sum, weight, out, scale, ldx, ldr, lds, ldo, (int)rows, (int)cols, across, weight_type, eps};
     const void *fn = type == kF32   ? norm_ptr<kF32>(s, out_type)
                      : type == kF16 ? norm_ptr<kF16>(s, out_type)
                                     : norm_ptr<kBF16>(s, out_type);
-    return run(fn, s.lanes ? cdiv(rows, 256 / s.lanes) : rows, s.threads, &args, stream);
+    return run_rows(fn, blocks, across, s.threads, &args, stream);
 }
 
 int64_t pdgemm_rms_norm_backward_workspace_size(int64_t rows, int64_t cols) {

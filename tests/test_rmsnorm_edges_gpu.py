@@ -1,0 +1,47 @@
+"""GPU tests of the root-mean-square norm at the ends of its ranges."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module")
+def pd():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import precision_dense_gemm_amd as pd
+    yield pd
+    torch.cuda.empty_cache()
+
+
+def test_rows_of_one_value_past_a_launch_of_32_bits(pd):
+    """More rows than 2^32 work-items have, sixteen to a row."""
+    rows = (1 << 28) + 17
+    x = torch.full((rows, 1), 2.0, dtype=torch.float16, device="cuda")
+    x[1::2] = -0.5
+    x[-3:] = torch.tensor([[1.0], [0.0], [-4.0]])
+    w = torch.tensor([3.0], dtype=torch.float16, device="cuda")
+    few = torch.cat([x[:2], x[-3:]])
+    y, (q, scale) = pd.rms_norm(few, w, EPS), pd.rms_norm_i8(few, w, EPS)
+    got, (gq, gs) = pd.rms_norm(x, w, EPS), pd.rms_norm_i8(x, w, EPS)
+    for all_rows, of_few in ((got[:, 0], y[:, 0]), (gq[:, 0], q[:, 0]), (gs, scale)):
+        assert torch.equal(all_rows[-3:], of_few[2:])
+        assert (all_rows[:-3:2] == of_few[0]).all() and (all_rows[1:-3:2] == of_few[1]).all()
+
+
+def test_workgroups_of_a_row_past_a_launch_of_32_bits(pd):
+    """128 threads to a row, in place."""
+    rows, cols, last = (1 << 25) + 5, 513, 100
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator("cuda").manual_seed(1)
+    x[-last:] = torch.randn(last, cols, device="cuda", generator=g).bfloat16()
+    w = torch.randn(cols, device="cuda", generator=g).bfloat16()
+    first, end = pd.rms_norm(x[:1], w, EPS), pd.rms_norm(x[-last:], w, EPS)
+    pd.rms_norm(x, w, EPS, out=x)
+    assert torch.equal(x[-last:], end)
+    for part in x[:-last].split(1 << 21):
+        assert (part == first).all()

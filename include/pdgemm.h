@@ -535,7 +535,7 @@ int pdgemm_a16_i4_pick(int64_t M, int64_t N, int64_t K, int64_t group);
 /* A mixture-of-experts layer for a few tokens: what follows the router's product.
  *
  * pdgemm_moe_route: the `top` largest of each row of logits (T x E, of `type`, any
- * ld >= E), E <= 1024, top <= min(E, 64), in falling order, ties to the lower index:
+ * ld >= E), T <= 2^30, E <= 1024, top <= min(E, 64), in falling order, ties to the lower index:
  * their indices to ids and their softmax to weights (T x top both, dense), among
  * themselves (normalize != 0) or among all of the row.  An expert at -infinity is
  * not taken: slots left over take id -1 and weight 0.  A NaN counts as the largest;

@@ -23,6 +23,7 @@ struct RouteArgs {
     float *weights;
     int64_t ld;
     int T, E, top, type;
+    int across;             // of block_of()
     bool normalize;
 };
 
@@ -33,7 +34,7 @@ template <int V>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     const int lane = threadIdx.x % kWave;
-    const int t = blockIdx.x * 4 + threadIdx.x / kWave;
+    const int t = block_of(args.across) * 4 + threadIdx.x / kWave;
     if (t >= args.T) return;
     float x[V];
     uint32_t key[V];
@@ -587,12 +588,14 @@ int pdgemm_moe_route(int64_t T, int64_t E, int64_t top, const void *logits, int6
     if (rc == PDGEMM_OK) rc = check_plain(ids, 1, kF32);
     if (rc == PDGEMM_OK) rc = check_plain(weights, 1, kF32);
     if (rc != PDGEMM_OK) return rc;
-    RouteArgs args = {logits, ids, weights, ld, (int)T, (int)E, (int)top, type, normalize != 0};
+    const int64_t blocks = cdiv(T, 4);
+    const int across = blocks_across(blocks, 256);
+    RouteArgs args = {logits, ids, weights, ld, (int)T, (int)E, (int)top, type, across, normalize != 0};
     const void *fn = E <= 64    ? reinterpret_cast<const void *>(&moe_route_kernel<1>)
                      : E <= 128 ? reinterpret_cast<const void *>(&moe_route_kernel<2>)
                      : E <= 256 ? reinterpret_cast<const void *>(&moe_route_kernel<4>)
                                 : reinterpret_cast<const void *>(&moe_route_kernel<16>);
-    return run(fn, cdiv(T, 4), 256, &args, stream);
+    return run_rows(fn, blocks, across, 256, &args, stream);
 }
 
 int64_t pdgemm_moe_a16_i4_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top) {

@@ -68,3 +68,15 @@ def test_experts_scales_of_very_long_groups(pd, group):
         up = torch.tensor([2.0 if k < group else 32.0 for k in at[:rows]], dtype=torch.float64)
         want = up / (1 + np.exp(-1.0))                          # (two groups differ 16 times; one rounding, 2^-8)
         assert torch.allclose(y.cpu().double(), want[:, None].expand(rows, H), rtol=2.0 ** -8 + 2.0 ** -14, atol=0), rows
+
+
+def test_routing_of_tokens_past_a_launch_of_32_bits(pd):
+    """More tokens than 2^32 work-items have, 64 to a token."""
+    T = (1 << 26) + 3
+    logits = torch.zeros(T, 2, dtype=torch.float16, device="cuda")
+    logits[::2, 1] = 1.0
+    logits[-1] = torch.tensor([0.0, 2.0])
+    ids, weights = pd.moe_route(logits, 1, normalize=False)
+    assert (ids[:-1:2] == 1).all() and (ids[1:-1:2] == 0).all() and ids[-1, 0] == 1
+    few, share = pd.moe_route(torch.cat([logits[:2], logits[-1:]]), 1, normalize=False)
+    assert torch.equal(weights[-1], share[2]) and (weights[:-1:2] == share[0]).all() and (weights[1:-1:2] == share[1]).all()

@@ -471,7 +471,8 @@ int pdgemm_a16_mxf4_pick(int a_type, int64_t M, int64_t N, int64_t K);   /* -1 f
  *   out_type I8: with t = h * weight in binary32 and m the row's largest |t|,
  *     out = t * (127 * (1 / m)), each step in binary32, rounded to nearest even, and
  *     scale[i] = m * r / 127: the A and scale_a of gemm_i8_dequant where ldo is
- *     a multiple of 16.  A row of zeros takes zero codes and scale 0, one with an
+ *     a multiple of 16.  A row of zeros, or of no values (cols = 0, scale not
+ *     NULL), takes zero codes and scale 0, one with an
  *     infinity or a NaN in t zero codes and scale NaN.
  * Squares and their sum may leave binary32's range.  sum may be residual or x
  * itself, and out x (or sum) itself where they have one type and ld. */

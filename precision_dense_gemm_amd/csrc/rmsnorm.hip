@@ -473,6 +473,13 @@ const void *grad_ptr(const Share &s) {
     return reinterpret_cast<const void *>(&rms_norm_backward_kernel<T, 4, 0>);
 }
 
+// n zeros, by a kernel: a graph may hold it
+__global__ __launch_bounds__(256) void zeros_kernel(float *p, int n) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
 int check_norm_sizes(int64_t rows, int64_t cols) {
     return rows < 0 || cols < 0 || rows > (int64_t(1) << 30) || cols > kMaxCols ? PDGEMM_EINVAL_DIM : PDGEMM_OK;
 }
@@ -509,7 +516,17 @@ int pdgemm_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int 
     if (rc != PDGEMM_OK) return rc;
     const bool add = residual || sum;
     if (ldx < cols || ldo < cols || (add && (ldr < cols || lds < cols))) return PDGEMM_EINVAL_LD;
-    if (rows == 0 || cols == 0) return PDGEMM_OK;
+    if (rows == 0 || (cols == 0 && (out_type != kI8 || !scale))) return PDGEMM_OK;
+    if (cols == 0) {
+        rc = check_plain(scale, 1, kF32);
+        if (rc != PDGEMM_OK) return rc;
+        int n = (int)rows;
+        void *kargs[] = {&scale, &n};
+        hipStream_t s = static_cast<hipStream_t>(stream);
+        const int64_t blocks = cdiv(rows, 256);
+        return finish(hipLaunchKernel(reinterpret_cast<const void *>(&zeros_kernel), dim3(blocks < 4096 ? (unsigned)blocks : 4096u),
+                                      dim3(256), kargs, 0, s), s);
+    }
     rc = check_plain(x, ldx, type);
     if (rc == PDGEMM_OK && add) rc = check_plain(residual, ldr, type);
     if (rc == PDGEMM_OK && add) rc = check_plain(sum, lds, type);

@@ -39,3 +39,10 @@ def test_a_choice_for_empty_and_refused_sizes(pd):
                         assert c == 0 and pd.a16_i4_workspace_size(M, N, K, group) == 0
                     for cfg in (-1, 0, 8, 10, 11):
                         assert pd.a16_i4_workspace_size(M, N, K, group, cfg) >= 0
+
+
+def test_rows_without_values_need_no_pointers(pd):
+    """(the scales of a norm to INT8 are set where they are given, so their alignment is looked at)"""
+    def norm(out_type, scale):
+        return pd.lib.pdgemm_rms_norm(5, 0, None, 0, 2, None, 0, None, 0, None, 2, 1e-5, None, 0, out_type, scale, None)
+    assert norm(0, 0x10002) == 0 and norm(3, None) == 0 and norm(3, 0x10002) == -5

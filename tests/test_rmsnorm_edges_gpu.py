@@ -45,3 +45,15 @@ def test_workgroups_of_a_row_past_a_launch_of_32_bits(pd):
     assert torch.equal(x[-last:], end)
     for part in x[:-last].split(1 << 21):
         assert (part == first).all()
+
+
+def test_scales_of_rows_without_values(pd):
+    """cols = 0: no code, and a scale for every row all the same (a product over K = 0 takes it)."""
+    for rows in (1, 5, 300, 2_000_000):
+        scale = torch.full((rows + 1,), float("nan"), device="cuda")
+        x = torch.empty(rows, 0, dtype=torch.bfloat16, device="cuda")
+        w = torch.empty(0, dtype=torch.bfloat16, device="cuda")
+        q, s = pd.rms_norm_i8(x, w, EPS, out=(torch.empty(rows, 0, dtype=torch.int8, device="cuda"), scale[:rows]))
+        assert q.shape == (rows, 0) and not s.any() and scale[rows].isnan()
+        assert pd.rms_norm(x, w, EPS).shape == (rows, 0)
+    assert pd.rms_norm_i8(x[:0], w, EPS)[1].shape == (0,)

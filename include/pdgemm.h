@@ -474,7 +474,8 @@ int pdgemm_a16_mxf4_pick(int a_type, int64_t M, int64_t N, int64_t K);   /* -1 f
  *     a multiple of 16.  A row of zeros, or of no values (cols = 0, scale not
  *     NULL), takes zero codes and scale 0, one with an
  *     infinity or a NaN in t zero codes and scale NaN.
- * Squares and their sum may leave binary32's range.  sum may be residual or x
+ * Squares and their sum may leave binary32's range; where they do, t is taken 2^64 times as
+ * large if m is below 2^-64, and as small if m is above 2^64.  sum may be residual or x
  * itself, and out x (or sum) itself where they have one type and ld. */
 int pdgemm_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual,
                     int64_t ldr, void *sum, int64_t lds, const void *weight, int weight_type, float eps, void *out,

@@ -158,9 +158,12 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
         uint32_t top = largest(1.0f);
         sum_and_max_over_row<kLanes>(ss, top, part);
         const Inverse f = inverse(ss);
-        if (f.c != 1.0f) {
+        // (a row out of the range of squares takes t times c, where t is out there too: the weights may have brought it back)
+        float c = 1.0f, rest = f.c;
+        if ((f.c > 1.0f && top < bits_of(0x1p-64f)) || (f.c < 1.0f && top > bits_of(0x1p64f))) {
             float none = 0;
-            top = largest(f.c);
+            c = f.c, rest = 1.0f;
+            top = largest(c);
             if constexpr (kLanes == 0) __syncthreads();
             sum_and_max_over_row<kLanes>(none, top, part);
         }
@@ -168,14 +171,14 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
         const float m = as_float(top);
         const float d = m < 0x1p-64f ? 0x1p64f : m > 0x1p64f ? 0x1p-64f : 1.0f;   // 1 / m in binary32's normal range
         const float inv = top && fine ? 127.0f * (1.0f / (m * d)) : 0.0f;
-        if (t == 0 && row < args.rows) args.scale[row] = !fine ? __builtin_nanf("") : top ? m * f.r / 127.0f : 0.0f;
+        if (t == 0 && row < args.rows) args.scale[row] = !fine ? __builtin_nanf("") : top ? m * f.r / 127.0f * rest : 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int at = (v * step + t) * N;
             Out q[N];
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                q[i] = fine ? (Out)(int)rintf((float)h[v][i] * f.c * w[v][i] * d * inv) : (Out)0;
+                q[i] = fine ? (Out)(int)rintf((float)h[v][i] * c * w[v][i] * d * inv) : (Out)0;
             store_some<N>(out + at, q, cols - at);
         }
     } else {

@@ -1,7 +1,10 @@
 """GPU tests of the root-mean-square norm at the ends of its ranges."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
+
+import oracle.norm as rn
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -57,3 +60,18 @@ def test_scales_of_rows_without_values(pd):
         assert q.shape == (rows, 0) and not s.any() and scale[rows].isnan()
         assert pd.rms_norm(x, w, EPS).shape == (rows, 0)
     assert pd.rms_norm_i8(x[:0], w, EPS)[1].shape == (0,)
+
+
+@pytest.mark.parametrize("cols", [40, 300, 700, 5000, 20000])
+def test_codes_of_rows_out_of_the_range_of_squares_under_weights_that_bring_them_back(pd, cols):
+    """Squares below and above binary32's range, weights that make t = h w ordinary, small or large: the oracle's codes, and
+    its scales to 44 units of 2^-24 (as in test_rmsnorm_gpu.py, 40, and the product with the power of two)."""
+    rng = np.random.default_rng(cols)
+    for row, weight in ((-52, 120), (-52, 40), (-60, 60), (-75, 20), (60, -122), (60, -60), (75, -30), (100, 20), (120, -120)):
+        # (values of magnitude 1/2 to 2, so that all of t are normal)
+        h, w = (np.ldexp(rng.uniform(0.5, 2.0, n) * rng.choice([-1.0, 1.0], n), e).astype(np.float32) for n, e in
+                (((3, cols), row), (cols, weight)))
+        q, scale = pd.rms_norm_i8(torch.from_numpy(h).cuda(), torch.from_numpy(w).cuda(), 0.0)
+        want, s = rn.codes(h.astype(np.float64), w.astype(np.float64), 0.0)
+        assert np.isfinite(s).all() and np.array_equal(q.cpu().numpy(), want.astype(np.int8)), (row, weight)
+        assert (np.abs(scale.cpu().double().numpy() - s) <= 44 * 2.0 ** -24 * s + 2.0 ** -149).all(), (row, weight)

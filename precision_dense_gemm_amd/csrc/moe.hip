@@ -225,11 +225,11 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs &args, const Active &ac
 
 // 16 gate rows of an active expert and the up projection's 16 beside them to args.wk waves, which
 // split K; RA pairs at a time.
-template <int T, int RA, int Q, bool kS32, bool kAhead>
+template <int T, int RA, int Q, bool kS32>
 __global__ __launch_bounds__(kUpWaves *kWave) void moe_up_kernel(MoeArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using Elem = typename ElemOf<T>::type;
-    using Wave = I4Wave<T, RA, 2, 2, Q, kS32, kAhead>;
+    using Wave = I4Wave<T, RA, 2, 2, Q, kS32, true>;
     constexpr int W = kUpWaves;
     // all pairs' experts and weights, then the expert's own pairs and their weights
     extern __shared__ int ids[];
@@ -354,10 +354,10 @@ __device__ __forceinline__ void store_y(const MoeArgs &args, int t, int col, flo
 // finish adding up what the others wrote, ordered by fences of the device's scope, 16 tokens through 8 of 128
 // experts took 180 us instead of 50: such a fence writes back and drops a whole L2.)
 // T: the activations' type, kParts of them to a value.
-template <int T, int RA, int TT, int W, int Q, bool kS32, bool kAhead, int kParts>
+template <int T, int RA, int TT, int W, int Q, bool kS32, int kParts>
 __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs args) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    using Wave = I4Wave<T, RA, 1, 1, Q, kS32, kAhead, kParts>;
+    using Wave = I4Wave<T, RA, 1, 1, Q, kS32, true, kParts>;
     constexpr int kPairs = Wave::kRows;   // at a time
     __shared__ int expert[kMaxExperts], offset[kMaxExperts + 1];
     __shared__ uint16_t pair[kMaxPairs], token[kMaxPairs];
@@ -511,18 +511,16 @@ bool moe_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top) {
 
 template <int T, int RA, int Q, bool kS32, int kParts>
 int launch_down(MoeArgs &args, void *stream) {
-    constexpr bool kAhead = true;
     constexpr int W = RA == 2 ? 16 : 8;   // (as registers and LDS allow)
     const int64_t blocks = y_tiles(args.T, args.H) * args.splits;
-    return args.T <= 16 ? run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 16, W, Q, kS32, kAhead, kParts>), blocks,
-                              W * kWave, &args, stream)
-                        : run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 64, 8, Q, kS32, kAhead, kParts>), blocks, 512,
-                              &args, stream);
+    if constexpr (RA > 2)   // (2 serve up to two tokens)
+        if (args.T > 16)
+            return run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 64, W, Q, kS32, kParts>), blocks, W * kWave, &args, stream);
+    return run(reinterpret_cast<const void *>(&moe_down_kernel<T, RA, 16, W, Q, kS32, kParts>), blocks, W * kWave, &args, stream);
 }
 
 template <int T, int RA, int Q, bool kS32>
 int launch_moe(MoeArgs args, void *stream) {
-    constexpr bool kAhead = true;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t tiles = cdiv(args.I, 16);
     // waves that share a tile: as many as make 2048 of them, eight for each CU
@@ -531,7 +529,7 @@ int launch_moe(MoeArgs args, void *stream) {
     args.tiles = (int)cdiv(tiles * args.wk, kUpWaves);
     if ((int64_t)args.most * args.tiles * kUpWaves * kWave > (int64_t)UINT32_MAX) return PDGEMM_EINVAL_DIM;   // (as run())
     void *kargs[] = {&args};
-    int rc = finish(hipLaunchKernel(reinterpret_cast<const void *>(&moe_up_kernel<T, RA, Q, kS32, kAhead>),
+    int rc = finish(hipLaunchKernel(reinterpret_cast<const void *>(&moe_up_kernel<T, RA, Q, kS32>),
                                     dim3((unsigned)(args.most * args.tiles)), dim3(kUpWaves * kWave), kargs,
                                     8 * args.T * args.top + 6 * args.T, s), s);
     if (rc != PDGEMM_OK) return rc;

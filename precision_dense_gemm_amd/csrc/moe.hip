@@ -473,7 +473,10 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs args) {
 int64_t round_up(int64_t x, int64_t m) { return cdiv(x, m) * m; }
 
 // Tiles of y, of 16 columns for up to 64 tokens, and how many workgroups share one: as many as make
-// 256, one for each CU, each of a few experts
+// 256, one for each CU, each of a few experts.  (With 128, 256 and 512 workgroups the layer takes, us: 16 tokens through 8
+// of 128 experts, H 2048, I 768, 88, 71 and 67; 32 of them 114, 89 and 95; 64 through 4 of 64, H 1024, I 512, 42, 35 and
+// 39; 61 through 6 of 60, H 2000, I 1001, 132, 102 and 110.  Two, four or eight experts to a workgroup at least: no
+// difference in any of twelve shapes.)
 int64_t y_tiles(int64_t T, int64_t H) { return cdiv(T, 64) * cdiv(H, 16); }
 int splits_of(int64_t T, int64_t H, int64_t most) {
     int64_t s = 256 / y_tiles(T, H);
@@ -523,7 +526,9 @@ template <int T, int RA, int Q, bool kS32>
 int launch_moe(MoeArgs args, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t tiles = cdiv(args.I, 16);
-    // waves that share a tile: as many as make 2048 of them, eight for each CU
+    // waves that share a tile: as many as make 2048 of them, eight for each CU (with 1024, 2048 and 4096 the layer takes, us:
+    // one token through 8 of 32 experts, H 4096, I 2048, 37, 30 and 30; the same of 4 experts 22, 19 and 19; 61 through 6
+    // of 60, H 2000, I 1001, 102, 102 and 110)
     args.wk = 1;
     while (args.wk < kUpWaves && args.most * tiles * args.wk < 2048) args.wk *= 2;
     args.tiles = (int)cdiv(tiles * args.wk, kUpWaves);
@@ -544,12 +549,15 @@ int launch_moe(MoeArgs args, void *stream) {
     if (rc != PDGEMM_OK || args.splits == 1) return rc;
     return run(reinterpret_cast<const void *>(&moe_join_kernel), cdiv((int64_t)args.T * args.H, 256), 256, &args, stream);
 }
-// Pairs that an expert's rows of codes are read for at once
+// Pairs that the first product's rows of codes are read for at once: 8, or 16 where there are more than 4 for each expert
+// (of all, or of as many as there are pairs; the host cannot tell which pairs name none).  The layer, us, with 8 and with
+// 16, at 3, 4, 5, 6 and 8 pairs an expert: 64 experts (H 2048, I 1024, groups of 128) 74 and 77, 80 and 81, 87 and 84, 99 and 91, 111 and 98;
+// 60 (H 2000, I 1001, groups of 32) 86 and 91, 94 and 94, 104 and 100, 111 and 104, 168 and 153.
 template <int T, int Q, bool kS32>
 int launch_moe(const MoeArgs &args, void *stream) {
     const int pairs = args.T * args.top;
     return args.T <= 2              ? launch_moe<T, 2, Q, kS32>(args, stream)
-           : pairs <= 6 * args.most ? launch_moe<T, 8, Q, kS32>(args, stream)
+           : pairs <= 4 * args.most ? launch_moe<T, 8, Q, kS32>(args, stream)
                                     : launch_moe<T, 16, Q, kS32>(args, stream);
 }
 template <int T, bool kS32>

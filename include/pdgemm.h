@@ -510,7 +510,9 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
  * rounded once to out_type: |C - exact| <= (512 + K / 12) * 2^-22 * sum over k of
  * |A[i][k]| |scale| plus that rounding where no sum leaves binary32's normal range (up
  * to 16 rows a code enters as code + 24, or + 8 for f16 A, and the bias comes off in the same
- * sum; infinities and NaN of A reach C as the products make them).  As elsewhere
+ * sum; infinities and NaN of A reach C as the products make them); and <= (12 + K / 128) * 2^-22 * sum over k of
+ * |A[i][k]| |code| |scale| in the configurations of more than 16 rows, which gemm_a16_i4 takes from 17 rows on where that
+ * is faster.  As elsewhere
  * the 16-byte granule that holds a row's last element may be read whole, and
  * values outside the operands never reach a stored result.  K = 0 stores zeros.
  * Where there are too few tiles for the GPU, K is split over workgroups, whose sums

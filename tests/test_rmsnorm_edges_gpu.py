@@ -75,3 +75,27 @@ def test_codes_of_rows_out_of_the_range_of_squares_under_weights_that_bring_them
         want, s = rn.codes(h.astype(np.float64), w.astype(np.float64), 0.0)
         assert np.isfinite(s).all() and np.array_equal(q.cpu().numpy(), want.astype(np.int8)), (row, weight)
         assert (np.abs(scale.cpu().double().numpy() - s) <= 44 * 2.0 ** -24 * s + 2.0 ** -149).all(), (row, weight)
+
+
+def test_rows_past_32_bits_keep_their_bits(pd):
+    """Rows 4 MiB apart, the last ones past 2^32 bytes: norm, codes and gradients as of the same rows beside each other."""
+    rows, cols = 1100, 300
+    g = torch.Generator("cuda").manual_seed(3)
+    x, r, dy, dh = (torch.randn(rows, cols, device="cuda", generator=g) for _ in range(4))
+    w = torch.randn(cols, device="cuda", generator=g)
+
+    def far(t, dtype=torch.float32):
+        buf = torch.empty(rows, (1 << 22) // torch.empty(0, dtype=dtype).element_size(), dtype=dtype, device="cuda")
+        if t is not None:
+            buf[:, :cols] = t
+        return buf[:, :cols]
+
+    y, h = pd.rms_norm(x, w, EPS, residual=r)
+    fy, fh = pd.rms_norm(far(x), w, EPS, residual=far(r), out=far(None), sum_out=far(None))
+    assert torch.equal(y, fy) and torch.equal(h, fh)
+    q, s = pd.rms_norm_i8(x, w, EPS)
+    fq, fs = pd.rms_norm_i8(far(x), w, EPS, out=(far(None, torch.int8), torch.empty_like(s)))
+    assert torch.equal(q, fq) and torch.equal(s, fs)
+    dx, dw = pd.rms_norm_backward(dy, h, w, EPS, dh=dh)
+    fdx, fdw = pd.rms_norm_backward(far(dy), fh, w, EPS, dh=far(dh), out=far(None))
+    assert torch.equal(dx, fdx) and torch.equal(dw, fdw)

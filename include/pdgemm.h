@@ -457,8 +457,8 @@ int pdgemm_a16_mxf4_pick(int a_type, int64_t M, int64_t N, int64_t K);   /* -1 f
  * Section VI, leaves quantisation out).
  *
  * Every matrix is dense, row-major, with only its element's alignment and any
- * ld >= cols; there are at most 2^30 rows, of at most 32768 values.  type (PDGEMM_F32, _F16 or _BF16)
- * is that of x, residual and sum; the weight, of cols values, and the result
+ * ld >= cols; there are at most 2^30 rows, of at most 32768 values.  type
+ * (PDGEMM_F32, _F16 or _BF16) is that of x, residual and sum; the weight, of cols values, and the result
  * have types of their own.  Errors, streams and ownership are those of the
  * other entry points; an unknown type, or an eps that is negative or not
  * finite, returns PDGEMM_EINVAL_CFG. */
@@ -472,11 +472,11 @@ int pdgemm_a16_mxf4_pick(int a_type, int64_t M, int64_t N, int64_t K);   /* -1 f
  *     out = t * (127 * (1 / m)), each step in binary32, rounded to nearest even, and
  *     scale[i] = m * r / 127: the A and scale_a of gemm_i8_dequant where ldo is
  *     a multiple of 16.  A row of zeros, or of no values (cols = 0, scale not
- *     NULL), takes zero codes and scale 0, one with an
- *     infinity or a NaN in t zero codes and scale NaN.
- * Squares and their sum may leave binary32's range; where they do, t is taken 2^64 times as
- * large if m is below 2^-64, and as small if m is above 2^64.  sum may be residual or x
- * itself, and out x (or sum) itself where they have one type and ld. */
+ *     NULL), takes zero codes and scale 0, one with an infinity or a NaN in t
+ *     zero codes and scale NaN.
+ * Squares and their sum may leave binary32's range; where they do, t is taken 2^64
+ * times as large if m is below 2^-64, and as small if m is above 2^64.  sum may be
+ * residual or x itself, and out x (or sum) itself where they have one type and ld. */
 int pdgemm_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual,
                     int64_t ldr, void *sum, int64_t lds, const void *weight, int weight_type, float eps, void *out,
                     int64_t ldo, int out_type, float *scale, void *stream);
@@ -498,8 +498,8 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
 
 /* C = A * B of 16-bit A (a_type PDGEMM_F16 or PDGEMM_BF16, row-major, rows of a
  * multiple of 16 bytes, 16-byte aligned) and INT4 weights B with group scales,
- * the 4-bit form of most checkpoints: N rows of K signed 4-bit codes packed as
- * for gemm_i4 (ldb counts 4-bit elements, a multiple of 32, B 16-byte aligned;
+ * the symmetric 4-bit form of checkpoints (no zero points, groups of consecutive
+ * k): N rows of K signed 4-bit codes packed as for gemm_i4 (ldb counts 4-bit elements, a multiple of 32, B 16-byte aligned;
  * K may be odd), and one scale per `group` consecutive k of a row, group any
  * multiple of 32 (a group of K or more: one scale a row; else
  * PDGEMM_EINVAL_CFG).  The scales are stored by group: that of group q of row j
@@ -508,11 +508,11 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
  *   C[i][j] = sum over q of scale_b[q][j] * sum over k in q of A[i][k] * code[j][k]
  * The codes enter exactly, the sums are binary32 in a fixed order, and C is
  * rounded once to out_type: |C - exact| <= (512 + K / 12) * 2^-22 * sum over k of
- * |A[i][k]| |scale| plus that rounding where no sum leaves binary32's normal range (up
- * to 16 rows a code enters as code + 24, or + 8 for f16 A, and the bias comes off in the same
- * sum; infinities and NaN of A reach C as the products make them); and <= (12 + K / 128) * 2^-22 * sum over k of
- * |A[i][k]| |code| |scale| in the configurations of more than 16 rows, which gemm_a16_i4 takes from 17 rows on where that
- * is faster.  As elsewhere
+ * |A[i][k]| |scale| plus that rounding where no sum leaves binary32's normal range (in
+ * the configurations of up to 16 rows a code enters as code + 24, or + 8 for f16 A, and
+ * the bias comes off in the same sum; infinities and NaN of A reach C as the products
+ * make them); in those of more rows, which gemm_a16_i4 takes from 17 rows on where that is
+ * faster, <= (12 + K / 128) * 2^-22 * sum over k of |A[i][k]| |code| |scale|.  As elsewhere
  * the 16-byte granule that holds a row's last element may be read whole, and
  * values outside the operands never reach a stored result.  K = 0 stores zeros.
  * Where there are too few tiles for the GPU, K is split over workgroups, whose sums
@@ -521,9 +521,8 @@ int pdgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t
  * may run at once, need one each.
  * _cfg takes an explicit tile configuration (0 <= cfg <
  * pdgemm_a16_i4_num_configs(), any shape; the last one groups of a multiple of 128 only)
- * and the workspace of
- * _cfg_workspace_size; _pick is the one gemm_a16_i4 takes (0 for sizes that are empty or that
- * it refuses). */
+ * and the workspace of _cfg_workspace_size; _pick is the one gemm_a16_i4 takes (0 for sizes
+ * that are empty or that it refuses). */
 int64_t pdgemm_a16_i4_workspace_size(int64_t M, int64_t N, int64_t K, int64_t group);
 int gemm_a16_i4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int a_type, const uint8_t *B,
                 int64_t ldb, const void *scale_b, int64_t ldsb, int scale_type, int64_t group, void *C, int64_t ldc,
@@ -548,8 +547,9 @@ int pdgemm_moe_route(int64_t T, int64_t E, int64_t top, const void *logits, int6
                      int32_t *ids, float *weights, void *stream);
 
 /* y[t] = sum over the slots s of weights[t][s] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),
- * e = ids[t][s], in two kernels, and a third where y has few tiles.  x (T x H, rows of a multiple of 16 bytes, 16-byte
- * aligned) and y are of `type`, PDGEMM_F16 or PDGEMM_BF16; ids and weights T x top,
+ * e = ids[t][s], in two kernels, and a third where y has few tiles.  (Past 64 tokens
+ * the second product's time grows with their square; calls of 64 tokens are faster
+ * from some 128 to 256 on.)  x (T x H, rows of a multiple of 16 bytes, 16-byte aligned) and y are of `type`, PDGEMM_F16 or PDGEMM_BF16; ids and weights T x top,
  * dense.  An id outside 0 .. E - 1 adds nothing (a padded token, an expert that is
  * elsewhere); one that a token names twice adds with the weights' sum; a token of no
  * expert takes zeros.
@@ -558,12 +558,12 @@ int pdgemm_moe_route(int64_t T, int64_t E, int64_t top, const void *logits, int6
  * with group scales, as gemm_a16_i4's B (ld counts 4-bit elements; an expert's scales
  * are stored by group); expert strides are counted as the ld beside them are, those of codes a
  * multiple of 32.  H and I are any length, E <= 1024, top <= 64, T * top <= 4096,
- * T * ldx * 2 and T * top * (2 I + 16) below 2^31 (PDGEMM_EINVAL_DIM, for ldx
- * PDGEMM_EINVAL_LD).  The codes enter exactly and sums are binary32 in a fixed order;
+ * T * ldx * 2 and T * top * (2 I + 16) below 2^31, min(E, T * top) times ceil(I / 16),
+ * up to a multiple of 4, below 2^26 (PDGEMM_EINVAL_DIM, for ldx PDGEMM_EINVAL_LD).  The codes enter exactly and sums are binary32 in a fixed order;
  * y is rounded once.  silu(..) * (..), times the pair's weight, passes from the one product
  * to the other through the workspace (16-byte aligned).  In one of at least
  * pdgemm_moe_a16_i4_wide_workspace_size() bytes it is the sum of two bf16 values: in
- * binary32's range, and within 2^-16 of its value.  In one of at least
+ * binary32's range, and within 2^-16 of its value (2^-15 past bfloat16's largest).  In one of at least
  * pdgemm_moe_a16_i4_workspace_size() bytes it is rounded to `type`: an f16 one above 65504
  * becomes infinite, and y's error grows by about 1.4.  The workspace is undefined on
  * return; calls that overlap, and graphs that may run at once, need one each. */

@@ -35,9 +35,9 @@ transposed once into such rows:
     scales.copy_(by_row.t())
 
 Around the products: rms_norm, rms_norm_i8 (whose codes and scales are the A and scale_a of
-gemm_i8_dequant) and rms_norm_backward; gemm_a16_i4, 16-bit activations times INT4 weights with
-scales by group, (ceil(K/group), N); moe_route and moe_a16_i4, a mixture-of-experts layer of
-such weights.
+gemm_i8_dequant) and rms_norm_backward; gemm_a16_i4, 16-bit activations times symmetric INT4
+weights (signed codes, no zero points) with scales by group, (ceil(K/group), N), of consecutive k;
+moe_route and moe_a16_i4, a mixture-of-experts layer of such weights.
 
 No call here records a graph: a result carries no gradient, whatever its inputs ask for.
 A layer that trains computes dX and dW by calls of its own (see mxf4_quantize_both), for
@@ -1110,7 +1110,8 @@ def moe_a16_i4_workspace_size(T: int, H: int, I: int, E: int, top_k: int) -> int
 def moe_a16_i4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor,
                w2: torch.Tensor, s2: torch.Tensor, group: int, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """A mixture-of-experts layer for a few tokens (T * top_k <= 4096): y (T, H), of x's type, with
+    """A mixture-of-experts layer for a few tokens (T * top_k <= 4096; past 64 tokens its time grows with their square, and
+    calls of 64 are faster from some 128 to 256 on): y (T, H), of x's type, with
         y[t] = sum over the slots s of weights[t, s] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),  e = ids[t, s].
     x (T, H) float16 or bfloat16, rows of a multiple of 16 bytes; ids int32 and weights float32 (T, top_k), as moe_route
     makes them; INT4 weights of E experts: w13 (E, 2 I, ceil(H/2)), the gate's rows and then the up projection's, w2

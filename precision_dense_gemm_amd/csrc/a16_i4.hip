@@ -47,8 +47,8 @@ __device__ __forceinline__ void store_as(void *C, int type, int64_t at, const fl
 
 // Few rows: a tile of RA rows and 16 NT columns of C to a workgroup, K split over its W waves,
 // whose sums meet in LDS and are added in wave order.  The stream of the codes bounds it: one row of
-// bf16 against 8192 x 8192 in groups of 128 takes 8.3 us, 34.6 MB at 4.1 TB/s with the launch's start and end
-// (loads alone, of the same codes, 7), 16 rows 11.3, one row against 4096 x 4096 4.3.
+// bf16 against 8192 x 8192 in groups of 128 takes 8.4 us, 34.6 MB at 4.1 TB/s with the launch's start and end, 8 rows
+// 10.3, 16 rows 11.4, one row against 4096 x 4096 4.3 to 4.6.
 template <int T, int RA, int NT, int W, int Q, bool kS32, bool kAhead>
 __global__ __launch_bounds__(W *kWave) void a16_i4_few_kernel(A16I4Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -131,9 +131,11 @@ __device__ __forceinline__ int turn_of(int r) { return (r & 3) | (r >> 1 & 4) | 
 // and their sums meet in LDS.  With `splits`, K is split over that many workgroups too, which write
 // binary32 sums for split_join_kernel; what they write and the second launch cost 37 x 4096 x 8192
 // 7 of 19 us with 16 splits and G = 1, so G is 4 and 2 for the tiles of few rows (14.4 us).
-// Up to some hundred rows the stream of codes bounds it, past that the vector unit: a code takes an
-// instruction and a half, and each sum of a scale's values a multiply-add beside the matrix
-// instructions.  2048 x 8192 x 8192 in groups of 128: 257 to 271 us, 1.02 to 1.07 PFLOP/s; of 64: 367 to 381 us.
+// Up to some hundred rows the stream of codes bounds it.  Past that no unit is full: of the cycles of 2048 x 8192 x 8192
+// the matrix instructions take 44%, vector instructions issue in as many (a code takes an instruction and a half, each sum
+// of a scale's values a multiply-add), the LDS works in a third, and the two waves that a SIMD has between barriers
+// overlap these little.  bf16 or f16 in groups of 128: 252 to 264 us in a steady stream of calls (290 to 340 for the
+// first dozens after a pause, whose clock still rises), 1.04 to 1.09 PFLOP/s; of 64: 363 to 371 us; of 32: 464 to 485 us.
 template <int T, int MT, int NT, int W, int G, int Q, bool kS32>
 __global__ __launch_bounds__(G *W *kWave) void a16_i4_tile_kernel(A16I4Args args) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -421,7 +423,7 @@ int splits_of(int cfg, int64_t M, int64_t N, int64_t K) {
 // that, the least of a model of time: rounds of the CUs, each K / S values at a configuration's rate (us for
 // 1000 values of K), and where K is split the second launch and what the splits write and read.  Its
 // constants are fitted to all configurations' times at 88 shapes, 20 to 2048 rows against 1024 x 4096 to 14336 x
-// 8192 in groups of 64 and 128: it takes the fastest in 81 of them, and one within 6% of it in the others.
+// 8192 in groups of 64 and 128: it takes the fastest in 82 of them, and one within 6% of it in the others.
 int pick_a16_i4(int64_t M, int64_t N, int64_t K, int64_t group) {
     if (M <= 2) return tiles_n(1, N) >= 256 ? 1 : 0;
     if (M <= 8) return tiles_n(3, N) >= 256 ? 3 : 2;

@@ -102,10 +102,12 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs args) {
 // room for.  Where the caller's workspace holds one part only, it is of x's type.  The second kernel adds
 // the experts up: 16 columns of y to a workgroup, whose waves share out all (expert, line of
 // its rows), each with sums of its own for every token, so no sum leaves the workgroup and
-// their order is fixed.  Both read an expert's codes once (once for RA of its pairs), and their stream
+// their order is fixed.  Both read an expert's codes once (once for 1 to 16 of its pairs), and their stream
 // bounds them: 16 tokens through 8 of 128 experts (H 2048, I 768, f16, groups of 64), 206 MB of codes and
-// scales, take 73 us with the routing, 37 to 41 for the first kernel (its loads alone: 29 to 31) and 29 for the
-// second (21 to 22); one token through 4 of 32 (H 4096, I 2048, bf16, groups of 128), 52 MB, 24.
+// scales, take 75 us with the routing, 38 to 42 for the first kernel (137 MB) and 28 to 29 for the second (69 MB, one
+// workgroup to a CU: 2.4 TB/s); one token through 4 of 32 (H 4096, I 2048, bf16, groups of 128), 52 MB, 24.
+// Past 64 tokens a workgroup of the second kernel goes through all experts' pairs for its 64, so its time grows with the
+// square: through 8 of 32 experts (H 2048, I 1024) 64 tokens take 85 us, 128 192, 256 570 and 512 1980.
 
 struct MoeArgs {
     const uint8_t *x;
@@ -551,8 +553,8 @@ int launch_moe(MoeArgs args, void *stream) {
 }
 // Pairs that the first product's rows of codes are read for at once: 8, or 16 where there are more than 4 for each expert
 // (of all, or of as many as there are pairs; the host cannot tell which pairs name none).  The layer, us, with 8 and with
-// 16, at 3, 4, 5, 6 and 8 pairs an expert: 64 experts (H 2048, I 1024, groups of 128) 74 and 77, 80 and 81, 87 and 84, 99 and 91, 111 and 98;
-// 60 (H 2000, I 1001, groups of 32) 86 and 91, 94 and 94, 104 and 100, 111 and 104, 168 and 153.
+// 16, at 3, 4, 5, 6 and 8 pairs an expert: 64 experts (H 2048, I 1024, groups of 128) 74 and 77, 80 and 81, 87 and 84, 99
+// and 91, 111 and 98; 60 (H 2000, I 1001, groups of 32) 86 and 91, 94 and 94, 104 and 100, 111 and 104, 168 and 153.
 template <int T, int Q, bool kS32>
 int launch_moe(const MoeArgs &args, void *stream) {
     const int pairs = args.T * args.top;
